@@ -1,7 +1,7 @@
 """ctypes loader for libmxq.so, the HIP library behind this package.
 
 Loads the in-tree ``libmxq.so`` and declares the C signatures of
-``include/mxq.h``.  There is no fallback: if the library is missing or cannot
+``include/mxq.h`` and ``include/mxq_moe.h``.  There is no fallback: if the library is missing or cannot
 be loaded, using any op raises.
 """
 
@@ -23,9 +23,17 @@ EXPORTS = (
     "mxq_validate_offs", "mxq_status_string",
 )
 
+# include/mxq_moe.h
+MOE_EXPORTS = (
+    "moe_route", "moe_route_bwd", "moe_plan_workspace", "moe_plan", "moe_dispatch", "moe_dispatch_bwd",
+    "moe_dispatch_quantized", "moe_combine", "moe_combine_bwd", "swiglu_fwd", "swiglu_bwd",
+)
+
 _lib = None
+_moe_declared = None
 
 _vp, _i64, _i32, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+_f64 = ctypes.c_double
 _SIGS = {
     "quantize_mxfp4": ([_vp, _int, _i64, _i64, _vp, _vp, _vp], _int),
     "dequantize_mxfp4": ([_vp, _vp, _i64, _i64, _vp, _int, _vp], _int),
@@ -42,6 +50,19 @@ _SIGS = {
     "mxfp4_grouped_mm_fwd_w4a8": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp], _int),
     "mxq_validate_offs": ([_vp, _i64, _i64, _vp, _vp], _int),
     "mxq_status_string": ([_int], ctypes.c_char_p),
+}
+_MOE_SIGS = {
+    "moe_route": ([_vp, _int, _i64, _i64, _i64, _int, _vp, _i64, _i64, _int, _int, _f64, _vp, _vp, _vp, _vp], _int),
+    "moe_route_bwd": ([_vp, _int, _i64, _i64, _i64, _int, _int, _f64, _vp, _vp, _vp, _vp], _int),
+    "moe_plan_workspace": ([_i64, _i64, _i64], _i64),
+    "moe_plan": ([_vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "moe_dispatch": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "moe_dispatch_bwd": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "moe_dispatch_quantized": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp], _int),
+    "moe_combine": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp], _int),
+    "moe_combine_bwd": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp], _int),
+    "swiglu_fwd": ([_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp], _int),
+    "swiglu_bwd": ([_vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _i64, _vp, _vp], _int),
 }
 
 
@@ -64,6 +85,19 @@ def lib():
             f.restype = res
         _lib = l
     return _lib
+
+
+def moe_lib():
+    """The loaded library with the entry points of ``include/mxq_moe.h`` declared too."""
+    global _moe_declared
+    if _moe_declared is None:
+        l = lib()
+        for name, (args, res) in _MOE_SIGS.items():
+            f = getattr(l, name)
+            f.argtypes = args
+            f.restype = res
+        _moe_declared = l
+    return _moe_declared
 
 
 def check(status, fn):

@@ -1,0 +1,140 @@
+// The experts' activation h = silu(gate) * up between the two grouped
+// products, and its gradient from an input that was kept in 8 bits.
+//
+// All of it is one HBM stream each way.  A lane owns 8 consecutive columns of
+// gate and the same 8 of up, four lanes a block of 32 columns of each, whose
+// largest magnitudes meet by DPP; inter is a multiple of 32, so no block
+// straddles gate and up and every group of four lanes is whole.
+//
+// Keeping gate and up as E4M3 under a power of two per 32 columns (the form
+// that quantize_cache_packed gives for fp8 and block_size 32) holds 1.03 bytes
+// an element between forward and backward instead of 2 or 4.  The backward
+// uses the kept values throughout, so it is the gradient of silu(gate) * up at
+// a point within half an E4M3 step (2^-4 relative, or 2^-10 of the block's
+// power of two) of the true one.
+#include "moe_launch.hpp"
+#include "moe_device.hpp"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t rows_that_count(const int32_t* total, int64_t rows) {
+  return total ? min(rows, max((int64_t)0, (int64_t)*total)) : rows;
+}
+
+template <int DT, bool KEEP>
+__global__ void __launch_bounds__(kThreads) k_swiglu_fwd(const uint8_t* __restrict__ gate_up, int64_t rows, int chunks,
+                                                         const int32_t* __restrict__ total, uint8_t* __restrict__ h,
+                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t count = rows_that_count(total, rows), n = rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / chunks;
+    const int c = (int)(i - row * chunks);
+    if (row >= count) {
+      store8<DT>(h, i * 8, 8, zero8<DT>());
+      continue;
+    }
+    const int64_t at = row * 2 * chunks + c;     // chunk of gate; up is `chunks` further
+    float g[8], u[8], o[8];
+    to_f32<DT>(load8<DT>(gate_up, at * 8, 8), g);
+    to_f32<DT>(load8<DT>(gate_up, (at + chunks) * 8, 8), u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = g[k] * sigmoid_f32(g[k]) * u[k];
+    store8<DT>(h, i * 8, 8, from_f32<DT>(o));
+    if constexpr (KEEP) {
+      const int kg = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(g)));
+      const int ku = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(u)));
+      *reinterpret_cast<u32x2_any*>(codes + at * 8) = encode_fp8(g, pow2f(kg));
+      *reinterpret_cast<u32x2_any*>(codes + (at + chunks) * 8) = encode_fp8(u, pow2f(ku));
+      if ((c & 3) == 0) {
+        scales[at >> 2] = (uint8_t)(kg + 127);
+        scales[(at + chunks) >> 2] = (uint8_t)(ku + 127);
+      }
+    }
+  }
+}
+
+template <int DT, bool KEPT>
+__global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const uint8_t* __restrict__ grad_h,
+                                                         const uint8_t* __restrict__ gate_up,
+                                                         const uint8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int64_t rows, int chunks,
+                                                         const int32_t* __restrict__ total,
+                                                         uint8_t* __restrict__ grad) {
+  const int64_t count = rows_that_count(total, rows), n = rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / chunks;
+    const int c = (int)(i - row * chunks);
+    const int64_t at = row * 2 * chunks + c;
+    if (row >= count) {
+      store8<DT>(grad, at * 8, 8, zero8<DT>());
+      store8<DT>(grad, (at + chunks) * 8, 8, zero8<DT>());
+      continue;
+    }
+    float g[8], u[8], d[8];
+    to_f32<DT>(load8<DT>(grad_h, i * 8, 8), d);
+    if constexpr (KEPT) {
+      decode_fp8(*reinterpret_cast<const u32x2_any*>(codes + at * 8), e8m0_to_f32(scales[at >> 2]), g);
+      decode_fp8(*reinterpret_cast<const u32x2_any*>(codes + (at + chunks) * 8),
+                 e8m0_to_f32(scales[(at + chunks) >> 2]), u);
+    } else {
+      to_f32<DT>(load8<DT>(gate_up, at * 8, 8), g);
+      to_f32<DT>(load8<DT>(gate_up, (at + chunks) * 8, 8), u);
+    }
+    float dg[8], du[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float s = sigmoid_f32(g[k]);
+      dg[k] = d[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
+      du[k] = d[k] * g[k] * s;
+    }
+    store8<DT>(grad, at * 8, 8, from_f32<DT>(dg));
+    store8<DT>(grad, (at + chunks) * 8, 8, from_f32<DT>(du));
+  }
+}
+
+unsigned grid_of(int64_t n) { return (unsigned)min((n + kThreads - 1) / kThreads, (int64_t)1 << 20); }
+
+}  // namespace
+
+hipError_t launch_swiglu_fwd(const void* gate_up, int dt, int64_t rows, int64_t inter, const int32_t* total, void* h,
+                             uint8_t* codes, uint8_t* scales, hipStream_t st) {
+  const int chunks = (int)(inter / 8);
+  const unsigned grid = grid_of(rows * chunks);
+#define CALL(DT)                                                                                                   \
+  if (codes)                                                                                                       \
+    k_swiglu_fwd<DT, true><<<grid, kThreads, 0, st>>>((const uint8_t*)gate_up, rows, chunks, total, (uint8_t*)h,   \
+                                                      codes, scales);                                              \
+  else                                                                                                             \
+    k_swiglu_fwd<DT, false><<<grid, kThreads, 0, st>>>((const uint8_t*)gate_up, rows, chunks, total, (uint8_t*)h,  \
+                                                       codes, scales)
+  if (dt == DT_F32) { CALL(DT_F32); }
+  else if (dt == DT_BF16) { CALL(DT_BF16); }
+  else { CALL(DT_F16); }
+#undef CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd(const void* grad_h, const void* gate_up, const uint8_t* codes, const uint8_t* scales,
+                             int dt, int64_t rows, int64_t inter, const int32_t* total, void* grad_gate_up,
+                             hipStream_t st) {
+  const int chunks = (int)(inter / 8);
+  const unsigned grid = grid_of(rows * chunks);
+#define CALL(DT)                                                                                                      \
+  if (codes)                                                                                                          \
+    k_swiglu_bwd<DT, true><<<grid, kThreads, 0, st>>>((const uint8_t*)grad_h, (const uint8_t*)gate_up, codes, scales, \
+                                                      rows, chunks, total, (uint8_t*)grad_gate_up);                   \
+  else                                                                                                                \
+    k_swiglu_bwd<DT, false><<<grid, kThreads, 0, st>>>((const uint8_t*)grad_h, (const uint8_t*)gate_up, codes,        \
+                                                       scales, rows, chunks, total, (uint8_t*)grad_gate_up)
+  if (dt == DT_F32) { CALL(DT_F32); }
+  else if (dt == DT_BF16) { CALL(DT_BF16); }
+  else { CALL(DT_F16); }
+#undef CALL
+  return hipGetLastError();
+}
+
+}  // namespace mxq

@@ -1,0 +1,381 @@
+"""The routed-expert layer around the grouped GEMM: router, grouped order,
+the rows' way to their experts and back, and the experts' activation with its
+input kept in 8 bits.
+
+Argument marshalling and autograd only: every step runs in the HIP kernels
+behind the C ABI (``include/mxq_moe.h``, which defines each operation).
+Tensors must be CUDA (ROCm) tensors on one device; calls are enqueued on the
+current stream of that device, outputs and workspaces are allocated with
+PyTorch's caching allocator.  There is no CPU path.
+
+A layer's pass, as :func:`mxfp4_moe` makes it::
+
+    weights, experts = moe_route(logits, 8, score="sigmoid", bias=bias, groups=8, top_groups=4)
+    plan = moe_plan(experts, num_experts)
+    rows = moe_dispatch(x, plan)
+    rows = MXFP4GroupedMM.apply(rows, gate_up, gate_up_scales, plan.offs)
+    rows = swiglu(rows, plan.offs)
+    rows = MXFP4GroupedMM.apply(rows, down, down_scales, plan.offs)
+    out = moe_combine(rows, weights, plan)
+"""
+
+from typing import NamedTuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .ops import _DT, _E8M0, _FMT, _need_cuda, _ptr, _stream
+from .ops import (MXFP4GroupedMM, mxfp4_grouped_mm_fwd_w4a4, mxfp4_grouped_mm_fwd_w4a4_quantized,
+                  mxfp4_grouped_mm_fwd_w4a8, mxfp4_grouped_mm_fwd_w4a8_quantized)
+
+CHECKPOINT_BLOCK = 32
+_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+class MoEPlan(NamedTuple):
+    """Grouped order of the routed slots (slot t * top_k + j is token t's j-th expert).
+
+    offs: int32 [local experts], cumulative row counts, what the grouped GEMM takes.
+    rows: int32 [tokens, top_k], each slot's row r, or ~r (negative) for a slot
+        that no local expert serves; such rows lie behind offs[-1].
+    slots: int32 [tokens * top_k], the slot in each row.
+    """
+    offs: torch.Tensor
+    rows: torch.Tensor
+    slots: torch.Tensor
+
+
+def _call(name, device, *args):
+    """Run entry point ``name`` on ``device``'s current stream (appended as the last argument)."""
+    fn = getattr(_lib.moe_lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    _lib.check(status, name)
+
+
+def _float_type(t, name):
+    if t.dtype not in _DT:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return _DT[t.dtype]
+
+
+def _grad_wanted(*ts):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+
+
+# ------------------------------------------------------------------- router
+def _route(logits, top_k, score, bias, groups, top_groups, group_best, renormalize, scale, mask):
+    T, E = logits.shape
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
+    experts = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
+    _call("moe_route", logits.device, _ptr(logits), _DT[logits.dtype], T, E, top_k, _SCORE[score],
+          None if bias is None else bias.data_ptr(), groups, top_groups, group_best, int(renormalize), float(scale),
+          None if mask is None else _ptr(mask), _ptr(weights), _ptr(experts))
+    return weights, experts
+
+
+class _MoERoute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, score, bias, groups, top_groups, group_best, renormalize, scale, mask):
+        weights, experts = _route(logits, top_k, score, bias, groups, top_groups, group_best, renormalize, scale, mask)
+        ctx.save_for_backward(logits, experts)
+        ctx.how = score, renormalize, scale
+        ctx.mark_non_differentiable(experts)
+        return weights, experts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_weights, _):
+        logits, experts = ctx.saved_tensors
+        score, renormalize, scale = ctx.how
+        g = grad_weights.contiguous()
+        grad = torch.empty_like(logits)
+        T, E = logits.shape
+        _call("moe_route_bwd", logits.device, _ptr(logits), _DT[logits.dtype], T, E, experts.shape[1], _SCORE[score],
+              int(renormalize), float(scale), _ptr(experts), _ptr(g), _ptr(grad))
+        return (grad,) + (None,) * 9
+
+
+def moe_route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups=1, group_best=2, renormalize=True,
+              scale=1.0, token_mask=None):
+    """Experts and weights of each token from its router logits [T, E].
+
+    ``score``: "softmax" over the experts or "sigmoid" of each; ``bias``
+    (float32 [E]) is added to the scores for the choice only; with ``groups``
+    runs of experts only the ``top_groups`` best (by the sum of their
+    ``group_best`` largest biased scores) are kept; the ``top_k`` best experts
+    are taken, ties to the lower index.  The weights are the chosen scores,
+    divided by their sum with ``renormalize``, times ``scale``.  Tokens with
+    ``token_mask`` (bool [T]) false, and places for which no expert is left
+    (logits or biases of -inf), get expert -1 and weight 0.
+
+    Returns (weights float32 [T, top_k], experts int32 [T, top_k]); the weights
+    have a gradient with respect to the logits."""
+    if score not in _SCORE:
+        raise ValueError("moe_route: score must be 'softmax' or 'sigmoid'")
+    _need_cuda(*(t for t in (logits, bias, token_mask) if t is not None))
+    _float_type(logits, "moe_route")
+    if logits.dim() != 2:
+        raise ValueError("moe_route: logits must be [tokens, experts]")
+    if bias is not None:
+        if bias.dtype != torch.float32 or tuple(bias.shape) != (logits.shape[1],):
+            raise TypeError("moe_route: bias must be float32 [experts]")
+        bias = bias.detach().contiguous()
+    if token_mask is not None:
+        if token_mask.dtype != torch.bool or tuple(token_mask.shape) != (logits.shape[0],):
+            raise TypeError("moe_route: token_mask must be bool [tokens]")
+        token_mask = token_mask.contiguous()
+    args = (logits.contiguous(), int(top_k), score, bias, int(groups), int(top_groups), int(group_best),
+            bool(renormalize), float(scale), token_mask)
+    if not 1 <= args[1] <= min(32, logits.shape[1]):
+        raise ValueError("moe_route: top_k must be between 1 and 32 and no more than the experts")
+    return _MoERoute.apply(*args) if _grad_wanted(logits) else _route(*args)
+
+
+# ------------------------------------------------------------ grouped order
+def moe_plan(experts, num_experts, first_expert=0, local_experts=None):
+    """Grouped order of the slots of ``experts`` (int32 [T, top_k], as
+    ``moe_route`` returns them) for the ``local_experts`` experts from
+    ``first_expert`` on (default: all ``num_experts``): a stable sort by
+    expert.  Every other value, -1 among them, is a slot that is not served."""
+    _need_cuda(experts)
+    local = num_experts - first_expert if local_experts is None else local_experts
+    if experts.dtype != torch.int32:
+        raise TypeError("moe_plan: experts must be int32")
+    if experts.dim() != 2:
+        raise ValueError("moe_plan: experts must be [tokens, top_k]")
+    if first_expert < 0 or local < 1 or first_expert + local > num_experts:
+        raise ValueError("moe_plan: the local experts must lie within num_experts")
+    e = experts.contiguous()
+    T, k = e.shape
+    need = _lib.moe_lib().moe_plan_workspace(T, k, local)
+    if need < 0:
+        raise ValueError("moe_plan: at most 1024 local experts and fewer than 2^31 - 2^16 slots, top_k at least 1")
+    offs = torch.empty(local, dtype=torch.int32, device=e.device)
+    rows = torch.empty_like(e)
+    slots = torch.empty(T * k, dtype=torch.int32, device=e.device)
+    work = torch.empty(need // 4, dtype=torch.int32, device=e.device) if need else None
+    _call("moe_plan", e.device, _ptr(e), T, k, first_expert, local, _ptr(offs), _ptr(rows), _ptr(slots),
+          None if work is None else work.data_ptr(), need)
+    return MoEPlan(offs, rows, slots)
+
+
+def _plan_rows(rows, tokens, device, name):
+    if rows.dtype != torch.int32 or rows.dim() != 2:
+        raise TypeError(f"{name}: plan.rows must be int32 [tokens, top_k]")
+    if rows.device != device:
+        raise ValueError("all tensors must be on the same device")
+    if tokens is not None and rows.shape[0] != tokens:
+        raise ValueError(f"{name}: the plan is of {rows.shape[0]} tokens, not {tokens}")
+    if rows.shape[1] < 1:
+        raise ValueError(f"{name}: the plan has no slot for a token")
+    return rows.contiguous()
+
+
+def _dispatch(x, rows):
+    (T, H), k = x.shape, rows.shape[1]
+    out = torch.empty(T * k, H, dtype=x.dtype, device=x.device)
+    _call("moe_dispatch", x.device, _ptr(x), _DT[x.dtype], T, H, k, _ptr(rows), _ptr(out))
+    return out
+
+
+class _MoEDispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rows):
+        ctx.save_for_backward(rows)
+        return _dispatch(x, rows)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        rows, = ctx.saved_tensors
+        g = grad.contiguous()
+        (T, k), H = rows.shape, g.shape[1]
+        out = torch.empty(T, H, dtype=g.dtype, device=g.device)
+        _call("moe_dispatch_bwd", g.device, _ptr(g), _DT[g.dtype], T, H, k, _ptr(rows), _ptr(out))
+        return out, None
+
+
+def moe_dispatch(x, plan):
+    """Tokens' rows in the grouped order: x [T, H] -> [T * top_k, H], zeros in
+    the rows behind ``plan.offs[-1]``.  The gradient of x sums its served rows
+    in float32."""
+    _need_cuda(x)
+    _float_type(x, "moe_dispatch")
+    if x.dim() != 2:
+        raise ValueError("moe_dispatch: x must be [tokens, hidden]")
+    rows = _plan_rows(plan.rows, x.shape[0], x.device, "moe_dispatch")
+    x = x.contiguous()
+    return _MoEDispatch.apply(x, rows) if _grad_wanted(x) else _dispatch(x, rows)
+
+
+def moe_dispatch_quantized(x, plan, format):
+    """``moe_dispatch`` with the rows quantized on the way, in the form that a
+    grouped GEMM with low-bit activations takes (no gradient).
+
+    "fp8": (codes uint8 [T * top_k, H], scales uint8 [T * top_k, H / 32]) as
+    ``quantize_cache_packed(rows, "fp8", 32)`` gives them, for
+    ``mxfp4_grouped_mm_fwd_w4a8_quantized``; "mxfp4": (int8 [T * top_k, H / 2],
+    float8_e8m0fnu [T * top_k, H / 32]) as ``quantize_mxfp4(rows)``, for
+    ``mxfp4_grouped_mm_fwd_w4a4_quantized``.  H % 32 == 0."""
+    _need_cuda(x)
+    dt = _float_type(x, "moe_dispatch_quantized")
+    if format not in ("fp8", "mxfp4"):
+        raise ValueError("moe_dispatch_quantized: format must be 'fp8' or 'mxfp4'")
+    if x.dim() != 2 or x.shape[1] % 32:
+        raise ValueError("moe_dispatch_quantized: x must be [tokens, hidden] with hidden a multiple of 32")
+    rows = _plan_rows(plan.rows, x.shape[0], x.device, "moe_dispatch_quantized")
+    x = x.detach().contiguous()
+    (T, H), k = x.shape, rows.shape[1]
+    fp4 = format == "mxfp4"
+    codes = torch.empty(T * k, H // 2 if fp4 else H, dtype=torch.int8 if fp4 else torch.uint8, device=x.device)
+    scales = torch.empty(T * k, H // 32, dtype=torch.uint8, device=x.device)
+    _call("moe_dispatch_quantized", x.device, _ptr(x), dt, T, H, k, _ptr(rows), _FMT[format], _ptr(codes),
+          _ptr(scales))
+    return codes, (scales.view(_E8M0) if fp4 and _E8M0 is not None else scales)
+
+
+# ------------------------------------------------------------------ combine
+def _combine(y, weights, rows):
+    (T, k), H = rows.shape, y.shape[1]
+    out = torch.empty(T, H, dtype=y.dtype, device=y.device)
+    _call("moe_combine", y.device, _ptr(y), _DT[y.dtype], T, H, k, _ptr(rows), _ptr(weights), _ptr(out))
+    return out
+
+
+class _MoECombine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, rows):
+        ctx.save_for_backward(y if ctx.needs_input_grad[1] else None, weights, rows)
+        ctx.kind = y.dtype, y.shape
+        return _combine(y, weights, rows)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        y, weights, rows = ctx.saved_tensors
+        dtype, shape = ctx.kind
+        g = grad.contiguous()
+        (T, k), H = rows.shape, shape[1]
+        gy = torch.empty(shape, dtype=dtype, device=g.device) if ctx.needs_input_grad[0] else None
+        gw = torch.empty_like(weights) if ctx.needs_input_grad[1] else None
+        _call("moe_combine_bwd", g.device, _ptr(g), None if y is None else _ptr(y), _DT[dtype], T, H, k, _ptr(rows),
+              _ptr(weights), None if gy is None else _ptr(gy), None if gw is None else _ptr(gw))
+        return gy, gw, None
+
+
+def moe_combine(y, weights, plan):
+    """The experts' rows back to their tokens: out[t] = sum over the served
+    slots of weights[t, j] * y[row of (t, j)], summed in float32 in slot
+    order.  y [T * top_k, H], weights float32 [T, top_k]; both have
+    gradients."""
+    _need_cuda(y, weights)
+    _float_type(y, "moe_combine")
+    if weights.dtype != torch.float32:
+        raise TypeError("moe_combine: weights must be float32")
+    rows = _plan_rows(plan.rows, None, y.device, "moe_combine")
+    if weights.shape != rows.shape:
+        raise ValueError("moe_combine: weights must be [tokens, top_k] like plan.rows")
+    if y.dim() != 2 or y.shape[0] != rows.numel():
+        raise ValueError("moe_combine: y must be [tokens * top_k, hidden]")
+    y, weights = y.contiguous(), weights.contiguous()
+    return _MoECombine.apply(y, weights, rows) if _grad_wanted(y, weights) else _combine(y, weights, rows)
+
+
+# ------------------------------------------------------------------- swiglu
+def _swiglu(x, offs, keep):
+    R, I = x.shape[0], x.shape[1] // 2
+    h = torch.empty(R, I, dtype=x.dtype, device=x.device)
+    codes = scales = None
+    if keep:
+        codes = torch.empty(R, 2 * I, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(R, 2 * I // CHECKPOINT_BLOCK, dtype=torch.uint8, device=x.device)
+    _call("swiglu_fwd", x.device, _ptr(x), _DT[x.dtype], R, I, None if offs is None else _ptr(offs),
+          0 if offs is None else offs.numel(), _ptr(h), _ptr(codes) if keep else None, _ptr(scales) if keep else None)
+    return h, codes, scales
+
+
+class _SwiGLU(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, offs, checkpoint):
+        h, codes, scales = _swiglu(x, offs, checkpoint == "fp8")
+        ctx.save_for_backward(None if checkpoint == "fp8" else x, codes, scales, offs)
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        x, codes, scales, offs = ctx.saved_tensors
+        g = grad.contiguous()
+        R, I = g.shape
+        out = torch.empty(R, 2 * I, dtype=g.dtype, device=g.device)
+        _call("swiglu_bwd", g.device, _ptr(g), None if x is None else _ptr(x), None if codes is None else _ptr(codes),
+              None if scales is None else _ptr(scales), _DT[g.dtype], R, I, None if offs is None else _ptr(offs),
+              0 if offs is None else offs.numel(), _ptr(out))
+        return out, None, None
+
+
+def swiglu(gate_up, offs=None, checkpoint="fp8"):
+    """h = silu(gate) * up of gate_up [rows, 2 * inter] = [gate | up], inter a
+    multiple of 32.  With ``offs`` (int32 cumulative counts, as the grouped
+    GEMM takes them) the rows from offs[-1] on are not read and come out as
+    zeros, as do their gradients.
+
+    Where a gradient is wanted, ``checkpoint="fp8"`` keeps gate_up for the
+    backward as E4M3 codes with one power-of-two scale per 32 columns (what
+    ``quantize_cache_packed(gate_up, "fp8", 32)`` gives), and the gradient is
+    that of silu(gate) * up at the kept values; ``checkpoint=None`` keeps
+    gate_up itself."""
+    _need_cuda(*(t for t in (gate_up, offs) if t is not None))
+    _float_type(gate_up, "swiglu")
+    if checkpoint not in ("fp8", None):
+        raise ValueError("swiglu: checkpoint must be 'fp8' or None")
+    if gate_up.dim() != 2 or gate_up.shape[1] % 64:
+        raise ValueError("swiglu: gate_up must be [rows, 2 * inter] with inter a multiple of 32")
+    if offs is not None:
+        if offs.dtype != torch.int32 or offs.dim() != 1 or offs.numel() == 0:
+            raise TypeError("swiglu: offs must be int32 [experts]")
+        offs = offs.contiguous()
+    x = gate_up.contiguous()
+    return _SwiGLU.apply(x, offs, checkpoint) if _grad_wanted(x) else _swiglu(x, offs, False)[0]
+
+
+# -------------------------------------------------------------------- layer
+def mxfp4_moe(x, weights, experts, gate_up, gate_up_scales, down, down_scales, *, num_experts=None, first_expert=0,
+              activations="bf16", checkpoint="fp8"):
+    """The routed experts of one layer on bf16 x [T, H]: gather, gate/up
+    product, SwiGLU, down product, weighted sum.
+
+    ``weights``, ``experts``: as ``moe_route`` returns them.  ``gate_up`` and
+    ``gate_up_scales``: mxfp4 [E, 2 * inter, H] packed as int8 [E, 2 * inter,
+    H / 2] with E8M0 [E, 2 * inter, H / 32]; ``down`` and ``down_scales``:
+    [E, H, inter] likewise, of the E local experts, which are experts
+    first_expert .. first_expert + E - 1 of ``num_experts`` (default: the last
+    of them); slots of other experts add nothing.
+    ``activations``: "bf16" (gradients for x and weights; ``checkpoint`` is
+    swiglu's), or "fp8" / "mxfp4" activations in both products (W4A8 / W4A4,
+    no gradients; H and inter multiples of 512)."""
+    if activations not in ("bf16", "fp8", "mxfp4"):
+        raise ValueError("mxfp4_moe: activations must be 'bf16', 'fp8' or 'mxfp4'")
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise TypeError("mxfp4_moe: x must be bfloat16 [tokens, hidden]")
+    if activations != "bf16" and _grad_wanted(x, weights):
+        raise ValueError("mxfp4_moe: low-bit activations have no gradient")
+    local = gate_up.shape[0]
+    plan = moe_plan(experts, first_expert + local if num_experts is None else num_experts, first_expert, local)
+    if activations == "bf16":
+        rows = MXFP4GroupedMM.apply(moe_dispatch(x, plan), gate_up, gate_up_scales, plan.offs)
+        rows = MXFP4GroupedMM.apply(swiglu(rows, plan.offs, checkpoint), down, down_scales, plan.offs)
+    elif activations == "fp8":
+        q, s = moe_dispatch_quantized(x, plan, "fp8")
+        rows = mxfp4_grouped_mm_fwd_w4a8_quantized(q, s, gate_up, gate_up_scales, plan.offs)
+        rows = mxfp4_grouped_mm_fwd_w4a8(swiglu(rows, plan.offs), down, down_scales, plan.offs)
+    else:
+        q, s = moe_dispatch_quantized(x, plan, "mxfp4")
+        rows = mxfp4_grouped_mm_fwd_w4a4_quantized(q, s, gate_up, gate_up_scales, plan.offs)
+        rows = mxfp4_grouped_mm_fwd_w4a4(swiglu(rows, plan.offs), down, down_scales, plan.offs)
+    return moe_combine(rows, weights, plan)
