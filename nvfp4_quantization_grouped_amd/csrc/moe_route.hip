@@ -1,10 +1,15 @@
 // The router: scores, balance bias, expert groups, top-k and weights
 // (moe_route), and the weights' gradient with respect to the logits.
 //
-// One wave per token.  The keys that decide the choice are fp64: two experts
-// whose scores differ by less than fp32 resolves are still told apart, and
-// equal ones go to the lower index.  Each wave holds its token's keys in LDS;
-// a chosen expert's key is overwritten with -inf.
+// One wave per token.  Which expert comes next may hang on keys that fp32 does
+// not tell apart, so the choice is made on fp64 keys, ties to the lower index
+// -- but an fp64 exponential for every expert costs more than all the rest, so
+// k_moe_route computes fp32 keys, whose error is bounded (kKeyError), takes as
+// candidates every expert that the bound leaves in the running for the top_k
+// (a few more than top_k), and gives each candidate a lane, an fp64 key and a
+// rank: the number of candidates before it.  k_moe_route_general works with
+// fp64 keys in LDS throughout; it serves the group sizes that do not fit the
+// lanes of the other.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -130,11 +135,303 @@ __device__ void route_token(const RouteArgs& a, int64_t token, double* key) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
+__global__ void __launch_bounds__(kThreads) k_moe_route_general(RouteArgs a) {
   extern __shared__ double keys[];
   const int wave = threadIdx.x >> 6;
   const int64_t token = (int64_t)blockIdx.x * kTokens + wave;
   if (token < a.tokens) route_token<DT>(a, token, keys + wave * a.experts);
+}
+
+// ------------------------------------------------- fp32 keys, fp64 candidates
+// Bound on the error of an fp32 key, in units of 2^-24: a score (at most 1)
+// carries at most 24 roundings (softmax: the difference to the largest logit,
+// exp_neg's 4, 14 in the sum of 1024 terms, the reciprocal and the product;
+// sigmoid: 7), the bias adds the rounding of the sum, at most half an ulp of it.
+constexpr float kUlp = 0x1p-24f;
+__device__ __forceinline__ float key_error(float key) { return kUlp * (32.0f + 2.0f * fabsf(key)); }
+
+template <typename T>
+__device__ __forceinline__ T lane_value(T v, int lane);   // v of a lane that is the same for the whole wave
+template <>
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+template <>
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+template <>
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+template <int CTRL, typename T>
+__device__ __forceinline__ T dpp_value(T v) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+  } else {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp<CTRL>((uint32_t)b), hi = dpp<CTRL>((uint32_t)(b >> 32));
+    return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+  }
+}
+// `op` over the wave, the same in every lane: within rows of 16 by DPP, across them by lane reads.
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_all(T v, Op op) {
+  v = op(v, dpp_value<0xB1>(v));
+  v = op(v, dpp_value<0x4E>(v));
+  v = op(v, dpp_value<0x141>(v));
+  v = op(v, dpp_value<0x140>(v));
+  return op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
+}
+
+// The two largest of a set of keys; adding another set's two is the union.
+template <typename T>
+struct Two {
+  T best = -INFINITY, next = -INFINITY;
+  __device__ __forceinline__ void add(T k) {
+    next = k > best ? best : (k > next ? k : next);
+    best = k > best ? k : best;
+  }
+};
+
+// A group's value, and a bound on its error where its keys are fp32 ones.
+template <typename T>
+struct GroupValue {
+  T value;
+  float error;
+};
+
+union GroupPairs {
+  float f[128];
+  double d[128];
+};
+
+// Value of the group that this lane's experts belong to, the same in every
+// lane of the group: its `best` (1 or 2) largest keys summed.  t: the two
+// largest of this lane's keys; lanes: lanes of a group; lds: the wave's own.
+template <typename T>
+__device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int best, T* lds) {
+  const int lane = threadIdx.x & 63;
+  if ((lanes & (lanes - 1)) == 0) {
+    auto meet = [&](T b, T n) { t.add(b); t.add(n); };
+    if (lanes > 1) meet(dpp_value<0xB1>(t.best), dpp_value<0xB1>(t.next));
+    if (lanes > 2) meet(dpp_value<0x4E>(t.best), dpp_value<0x4E>(t.next));
+    if (lanes > 4) meet(dpp_value<0x141>(t.best), dpp_value<0x141>(t.next));
+    if (lanes > 8) meet(dpp_value<0x140>(t.best), dpp_value<0x140>(t.next));
+    if (lanes > 16) meet(__shfl_xor(t.best, 16), __shfl_xor(t.next, 16));
+    if (lanes > 32) meet(__shfl_xor(t.best, 32), __shfl_xor(t.next, 32));
+  } else {
+    lds[2 * lane] = t.best;
+    lds[2 * lane + 1] = t.next;
+    wave_sync();
+    const int first = lane / lanes * lanes;
+    t = Two<T>();
+    for (int i = first; i < min(64, first + lanes); ++i) {
+      t.add(lds[2 * i]);
+      t.add(lds[2 * i + 1]);
+    }
+    wave_sync();
+  }
+  if (!(t.best > -INFINITY)) return {t.best, 0.0f};
+  if (best == 2 && t.next > -INFINITY)
+    return {t.best + t.next, kUlp * (64.0f + 4.0f * (fabsf((float)t.best) + fabsf((float)t.next)))};
+  return {t.best, kUlp * (64.0f + 4.0f * fabsf((float)t.best))};
+}
+
+// Whether this lane's group is among the `top` groups of largest value; near:
+// whether a group's place inside or outside hangs on a difference that the
+// values' errors leave open.
+template <typename T>
+__device__ __forceinline__ bool group_kept(const GroupValue<T>& own, int groups, int lanes, int top, bool& near) {
+  const int g = (threadIdx.x & 63) / lanes;
+  int rank = 0;
+  bool close = false;
+  for (int o = 0; o < groups; ++o) {
+    const T v = lane_value(own.value, o * lanes);
+    const float e = lane_value(own.error, o * lanes);
+    rank += v > own.value || (v == own.value && o < g);
+    close |= o != g && v <= own.value && (float)(own.value - v) <= own.error + e;
+  }
+  near = __ballot(g < groups && rank == top - 1 && close) != 0;
+  return rank < top;
+}
+
+struct Candidate {
+  int expert;
+  float logit;
+};
+
+// Experts lane * V .. lane * V + V - 1 in each lane; experts <= 64 V, and a
+// group (if there are groups) is whole lanes.
+template <int DT, int V>
+__global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
+  __shared__ Candidate found[kTokens][64];
+  __shared__ GroupPairs pairs[kTokens];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, E = a.experts;
+  const int64_t token = (int64_t)blockIdx.x * kTokens + wave;
+  if (token >= a.tokens) return;
+  const bool alive = !a.token_mask || a.token_mask[token];
+  const uint8_t* row = (const uint8_t*)a.logits + token * E * kElemBytes<DT>;
+  const int e0 = lane * V, mine = alive ? min(V, max(0, E - e0)) : 0;
+
+  float x[V], key[V], bias[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : -INFINITY;
+    bias[v] = a.bias && v < mine ? a.bias[e0 + v] : 0.0f;
+    if (!(x[v] > -INFINITY)) x[v] = -INFINITY;            // NaN too
+  }
+  const bool by_logit = !a.bias && a.groups == 1;
+  // softmax statistics: z in fp64, as it moves every key
+  float top = -INFINITY;
+  double z = 1.0;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
+    top = wave_all(top, [](float p, float q) { return fmaxf(p, q); });
+    if (!by_logit || !a.renormalize) {
+      double s = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) s += x[v] > -INFINITY ? exp((double)x[v] - (double)top) : 0.0;
+      z = wave_all(s, [](double p, double q) { return p + q; });
+    }
+  }
+  const float rz = (float)(1.0 / z);
+  auto score64 = [&](float l) { return a.sigmoid ? sigmoid_f64((double)l) : exp((double)l - (double)top) / z; };
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float s = by_logit ? x[v] : a.sigmoid ? sigmoid_f32(x[v]) : exp_neg(top - x[v]) * rz;
+    const float k = s + bias[v];
+    key[v] = x[v] > -INFINITY && k > -INFINITY ? k : -INFINITY;
+  }
+
+  // fp64 key of this lane's expert e0 + v, read again: the rare paths below keep no registers for it
+  auto key64 = [&](int v, float& l) {
+    l = elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>));
+    const float b = a.bias ? a.bias[e0 + v] : 0.0f;
+    if (!eligible(l) || !eligible(b)) return (double)-INFINITY;
+    return by_logit ? (double)l : score64(l) + (double)b;
+  };
+  bool kept = true;
+  if (a.groups > 1) {
+    const int lanes = E / a.groups / V;
+    Two<float> t;
+#pragma unroll
+    for (int v = 0; v < V; ++v) t.add(key[v]);
+    bool near;
+    kept = group_kept(group_value<float>(t, lanes, a.group_best, pairs[wave].f), a.groups, lanes, a.top_groups, near);
+    if (near) {
+      Two<double> t64;
+#pragma unroll 1
+      for (int v = 0; v < mine; ++v) {
+        float l;
+        t64.add(key64(v, l));
+      }
+      kept = group_kept(group_value<double>(t64, lanes, a.group_best, pairs[wave].d), a.groups, lanes, a.top_groups,
+                        near);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = kept ? key[v] : -INFINITY;
+  }
+
+  // A bound `cut` with at least top_k keys at or above it and not many more:
+  // halving between the smallest and the largest key.
+  auto count = [&](float at) {
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) n += __popcll(__ballot(key[v] >= at));
+    return n;
+  };
+  const int able = count(-0x1.fffffep+127f);
+  float cut = -0x1.fffffep+127f;
+  if (able > a.top_k + 8) {
+    float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      lo = key[v] > -INFINITY ? fminf(lo, key[v]) : lo;
+      hi = fmaxf(hi, key[v]);
+    }
+    lo = wave_all(lo, [](float p, float q) { return fminf(p, q); });
+    hi = wave_all(hi, [](float p, float q) { return fmaxf(p, q); });
+    cut = lo;
+    for (int i = 0; i < 40; ++i) {
+      const float mid = 0.5f * lo + 0.5f * hi;
+      const int n = count(mid);
+      if (n >= a.top_k) {
+        cut = lo = mid;
+        if (n <= a.top_k + 8) break;
+      } else {
+        hi = mid;
+      }
+    }
+    if (!by_logit) cut -= 2.0f * key_error(cut);
+  }
+  const int n = count(cut);
+
+  int expert = -1;
+  double s = 0.0, k64 = -INFINITY;
+  int rank = lane;
+  bool chosen = false;
+  if (n <= 64) {
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint64_t in = __ballot(key[v] >= cut);
+      if (key[v] >= cut) found[wave][at + __popcll(in & ((1ull << lane) - 1))] = {e0 + v, x[v]};
+      at += __popcll(in);
+    }
+    wave_sync();
+    if (lane < n) {
+      const Candidate c = found[wave][lane];
+      expert = c.expert;
+      s = score64(c.logit);
+      k64 = by_logit ? (double)c.logit : s + (a.bias ? (double)a.bias[expert] : 0.0);
+      rank = 0;
+    }
+    for (int o = 0; o < n; ++o) {
+      const double k = lane_value(k64, o);
+      const int e = lane_value(expert, o);
+      if (lane < n) rank += k > k64 || (k == k64 && e < expert);
+    }
+    chosen = lane < n && rank < a.top_k;
+  } else {
+    // More experts than lanes within the error of each other (many equal
+    // logits): lane j takes the largest (key, expert) that comes after lane
+    // j - 1's.  There are top_k of them, as n > 64.
+    double last = INFINITY;
+    int last_e = -1;
+    for (int j = 0; j < a.top_k; ++j) {
+      double best = -INFINITY;
+      int best_e = -1;
+      float best_x = 0.0f;
+#pragma unroll 1
+      for (int v = 0; v < (kept ? mine : 0); ++v) {
+        float l;
+        const double k = key64(v, l);
+        if ((k < last || (k == last && e0 + v > last_e)) && k > best) { best = k; best_e = e0 + v; best_x = l; }
+      }
+      const double own = best;
+      int at = best_e;
+      wave_argmax(best, at);
+      const int from = __ffsll((unsigned long long)__ballot(own == best && best_e == at && at >= 0)) - 1;
+      const float l = lane_value(best_x, from);
+      if (lane == j) { expert = at; s = score64(l); chosen = true; }
+      last = best;
+      last_e = at;
+    }
+  }
+  double w = a.scale * s;
+  if (a.renormalize) {
+    const double sum = wave_all(chosen ? s : 0.0, [](double p, double q) { return p + q; });
+    w = sum > 0.0 ? w / sum : 0.0;
+  }
+  // places without an expert: those from n on
+  if (chosen || (lane >= n && lane < a.top_k)) {
+    a.index[token * a.top_k + rank] = chosen ? expert : -1;
+    a.weights[token * a.top_k + rank] = chosen ? (float)w : 0.0f;
+  }
 }
 
 // One wave per token; u: experts floats of the wave's own LDS, the gradient of each score.
@@ -205,10 +502,22 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __res
 hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   const int64_t blocks = (a.tokens + kTokens - 1) / kTokens;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  // experts of a lane: enough for 64 lanes, and no group cut inside a lane
+  int v = 1;
+  while (v * 64 < a.experts) v *= 2;
+  const bool whole = a.groups == 1 || (a.experts / a.groups) % v == 0;
   const size_t lds = (size_t)kTokens * a.experts * sizeof(double);   // at most 32 KB
-  if (dt == DT_F32) k_moe_route<DT_F32><<<(unsigned)blocks, kThreads, lds, st>>>(a);
-  else if (dt == DT_BF16) k_moe_route<DT_BF16><<<(unsigned)blocks, kThreads, lds, st>>>(a);
-  else k_moe_route<DT_F16><<<(unsigned)blocks, kThreads, lds, st>>>(a);
+#define CALL(DT)                                                                             \
+  if (!whole) k_moe_route_general<DT><<<(unsigned)blocks, kThreads, lds, st>>>(a);           \
+  else if (v == 1) k_moe_route<DT, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a);             \
+  else if (v == 2) k_moe_route<DT, 2><<<(unsigned)blocks, kThreads, 0, st>>>(a);             \
+  else if (v == 4) k_moe_route<DT, 4><<<(unsigned)blocks, kThreads, 0, st>>>(a);             \
+  else if (v == 8) k_moe_route<DT, 8><<<(unsigned)blocks, kThreads, 0, st>>>(a);             \
+  else k_moe_route<DT, 16><<<(unsigned)blocks, kThreads, 0, st>>>(a)
+  if (dt == DT_F32) { CALL(DT_F32); }
+  else if (dt == DT_BF16) { CALL(DT_BF16); }
+  else { CALL(DT_F16); }
+#undef CALL
   return hipGetLastError();
 }
 
