@@ -19,6 +19,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = kThreads / 64;   // per workgroup
+// From this many tokens on four share a wave.
+constexpr int64_t kRowTokens = 2048;
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -143,12 +145,22 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_general(RouteArgs a) {
 }
 
 // ------------------------------------------------- fp32 keys, fp64 candidates
-// Bound on the error of an fp32 key, in units of 2^-24: a score (at most 1)
-// carries at most 24 roundings (softmax: the difference to the largest logit,
-// exp_neg's 4, 14 in the sum of 1024 terms, the reciprocal and the product;
-// sigmoid: 7), the bias adds the rounding of the sum, at most half an ulp of it.
+// fp32 score: of an exponential at full rate, as its error is bounded, not
+// small.  In units of u = 2^-24 (half an ulp of 1), with scores of at most 1:
+// sigmoid 1 / (1 + e), e = 2^(-x log2 e): e is off by |x| u (two roundings of
+// the exponent) and 2 u, which moves the score by s (1 - s) times that, at
+// most u; the sum adds u and the reciprocal 2 u.  softmax p = e / z, e = 2^((x
+// - top) log2 e): p |x - top| 3 u <= 2 u, the exponential 2 u, z in fp64, its
+// reciprocal and the product 3 u.  A bias adds half an ulp of the key.
 constexpr float kUlp = 0x1p-24f;
-__device__ __forceinline__ float key_error(float key) { return kUlp * (32.0f + 2.0f * fabsf(key)); }
+constexpr float kLog2e = 0x1.715476p+0f;
+__device__ __forceinline__ float key_error(float key) { return kUlp * (16.0f + 2.0f * fabsf(key)); }
+__device__ __forceinline__ float sigmoid_key(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
+}
+__device__ __forceinline__ float softmax_key(float x, float top, float rz) {
+  return __builtin_amdgcn_exp2f((x - top) * kLog2e) * rz;
+}
 
 template <typename T>
 __device__ __forceinline__ T lane_value(T v, int lane);   // v of a lane that is the same for the whole wave
@@ -190,9 +202,14 @@ __device__ __forceinline__ T wave_all(T v, Op op) {
 template <typename T>
 struct Two {
   T best = -INFINITY, next = -INFINITY;
-  __device__ __forceinline__ void add(T k) {
-    next = k > best ? best : (k > next ? k : next);
-    best = k > best ? k : best;
+  __device__ __forceinline__ void add(T k) {       // a NaN changes nothing
+    if constexpr (sizeof(T) == 4) {
+      next = __builtin_amdgcn_fmed3f(best, next, k);
+      best = fmaxf(best, k);
+    } else {
+      next = k > best ? best : (k > next ? k : next);
+      best = k > best ? k : best;
+    }
   }
 };
 
@@ -210,9 +227,10 @@ union GroupPairs {
 
 // Value of the group that this lane's experts belong to, the same in every
 // lane of the group: its `best` (1 or 2) largest keys summed.  t: the two
-// largest of this lane's keys; lanes: lanes of a group; lds: the wave's own.
+// largest of this lane's keys; lanes: lanes of a group; lds: the wave's own;
+// the token's lanes are those from `base` to `end`.
 template <typename T>
-__device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int best, T* lds) {
+__device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int best, T* lds, int base, int end) {
   const int lane = threadIdx.x & 63;
   if ((lanes & (lanes - 1)) == 0) {
     auto meet = [&](T b, T n) { t.add(b); t.add(n); };
@@ -226,9 +244,9 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
     lds[2 * lane] = t.best;
     lds[2 * lane + 1] = t.next;
     wave_sync();
-    const int first = lane / lanes * lanes;
+    const int first = base + (lane - base) / lanes * lanes;
     t = Two<T>();
-    for (int i = first; i < min(64, first + lanes); ++i) {
+    for (int i = first; i < min(end, first + lanes); ++i) {
       t.add(lds[2 * i]);
       t.add(lds[2 * i + 1]);
     }
@@ -236,8 +254,8 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
   }
   if (!(t.best > -INFINITY)) return {t.best, 0.0f};
   if (best == 2 && t.next > -INFINITY)
-    return {t.best + t.next, kUlp * (64.0f + 4.0f * (fabsf((float)t.best) + fabsf((float)t.next)))};
-  return {t.best, kUlp * (64.0f + 4.0f * fabsf((float)t.best))};
+    return {t.best + t.next, kUlp * (32.0f + 4.0f * (fabsf((float)t.best) + fabsf((float)t.next)))};
+  return {t.best, kUlp * (32.0f + 4.0f * fabsf((float)t.best))};
 }
 
 // Whether this lane's group is among the `top` groups of largest value; near:
@@ -298,11 +316,11 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
       z = wave_all(s, [](double p, double q) { return p + q; });
     }
   }
-  const float rz = (float)(1.0 / z);
+  const float rz = a.sigmoid ? 1.0f : (float)(1.0 / z);
   auto score64 = [&](float l) { return a.sigmoid ? sigmoid_f64((double)l) : exp((double)l - (double)top) / z; };
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const float s = by_logit ? x[v] : a.sigmoid ? sigmoid_f32(x[v]) : exp_neg(top - x[v]) * rz;
+    const float s = by_logit ? x[v] : a.sigmoid ? sigmoid_key(x[v]) : softmax_key(x[v], top, rz);
     const float k = s + bias[v];
     key[v] = x[v] > -INFINITY && k > -INFINITY ? k : -INFINITY;
   }
@@ -321,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) t.add(key[v]);
     bool near;
-    kept = group_kept(group_value<float>(t, lanes, a.group_best, pairs[wave].f), a.groups, lanes, a.top_groups, near);
+    kept = group_kept(group_value<float>(t, lanes, a.group_best, pairs[wave].f, 0, 64), a.groups, lanes, a.top_groups, near);
     if (near) {
       Two<double> t64;
 #pragma unroll 1
@@ -329,8 +347,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
         float l;
         t64.add(key64(v, l));
       }
-      kept = group_kept(group_value<double>(t64, lanes, a.group_best, pairs[wave].d), a.groups, lanes, a.top_groups,
-                        near);
+      kept = group_kept(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, 0, 64), a.groups, lanes,
+                        a.top_groups, near);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = kept ? key[v] : -INFINITY;
@@ -434,6 +452,281 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
   }
 }
 
+// ------------------------------------------------------ four tokens a wave
+// The same for up to 256 experts and 16 places with 16 lanes a token: one
+// instruction serves four tokens in what is done once a token (the fp64 scores
+// of the candidates, their ranks, the groups), which is most of the work.  The
+// wave-wide kernel above keeps fewer steps one after another, which counts
+// where there are few tokens.
+
+// Number of set lanes of `m` in this lane's row of 16.
+__device__ __forceinline__ int row_count(uint64_t m) {
+  return __builtin_popcount((uint32_t)(m >> (threadIdx.x & 48)) & 0xFFFFu);
+}
+template <typename T, typename Op>
+__device__ __forceinline__ T row_all(T v, Op op) {
+  v = op(v, dpp_value<0xB1>(v));
+  v = op(v, dpp_value<0x4E>(v));
+  v = op(v, dpp_value<0x141>(v));
+  return op(v, dpp_value<0x140>(v));
+}
+// Sum over the lower lanes of the row.
+__device__ __forceinline__ int row_before(int v) {
+  int s = v;
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, true);
+  return s - v;
+}
+// Value of lane `from` (0..15) of this lane's row.
+template <typename T>
+__device__ __forceinline__ T row_lane(T v, int from) {
+  return __shfl(v, (int)(threadIdx.x & 48) + from);
+}
+// Rank of key among the row's: larger keys come first, equal ones in lane order.
+template <int N>
+__device__ __forceinline__ int row_rank(double key) {
+  if constexpr (N == 0) return 0;
+  else {
+    const double k = dpp_value<0x120 + N>(key);       // row_ror: from lane - N
+    return (int)(k > key || (k == key && (int)(threadIdx.x & 15) >= N)) + row_rank<N - 1>(key);
+  }
+}
+
+// Experts l * V .. l * V + V - 1 in lane l of a token's row; experts <= 16 V,
+// top_k <= 16, a group (if there are groups) is whole lanes.
+template <int DT, int V>
+__global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
+  __shared__ int32_t found[kTokens][64];
+  __shared__ GroupPairs pairs[kTokens];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, E = a.experts;
+  const int64_t token = ((int64_t)blockIdx.x * kTokens + wave) * 4 + (lane >> 4);
+  const bool alive = token < a.tokens && (!a.token_mask || a.token_mask[token]);
+  const uint8_t* row = (const uint8_t*)a.logits + token * E * kElemBytes<DT>;
+  const int e0 = l * V, mine = alive ? min(V, max(0, E - e0)) : 0;
+  constexpr float kNone = -INFINITY, kLowest = -0x1.fffffep+127f;
+
+  float x[V], key[V];
+  if (mine == V) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      if constexpr (DT == DT_F32) {
+        const u32x4_t w = *reinterpret_cast<const u32x4_any*>(row + (e0 + v) * 4);
+        x[v] = as_f32(w.x); x[v + 1] = as_f32(w.y); x[v + 2] = as_f32(w.z); x[v + 3] = as_f32(w.w);
+      } else {
+        const u32x2_t w = *reinterpret_cast<const u32x2_any*>(row + (e0 + v) * 2);
+        x[v] = elem_value<DT>(w.x & 0xFFFFu); x[v + 1] = elem_value<DT>(w.x >> 16);
+        x[v + 2] = elem_value<DT>(w.y & 0xFFFFu); x[v + 3] = elem_value<DT>(w.y >> 16);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : kNone;
+  }
+  const bool by_logit = !a.bias && a.groups == 1;
+  float top = kNone;
+  double z = 1.0;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
+    top = row_all(top, [](float p, float q) { return fmaxf(p, q); });
+    if (!by_logit || !a.renormalize) {
+      double s = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) s += x[v] > kNone ? exp((double)x[v] - (double)top) : 0.0;
+      z = row_all(s, [](double p, double q) { return p + q; });
+    }
+  }
+  auto score64 = [&](float v) { return a.sigmoid ? sigmoid_f64((double)v) : exp((double)v - (double)top) / z; };
+  // fp32 keys; where x is NaN the key is too, and no comparison takes it
+  if (by_logit) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = x[v];
+  } else {
+    const float rz = a.sigmoid ? 1.0f : (float)(1.0 / z);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float s = a.sigmoid ? sigmoid_key(x[v]) : softmax_key(x[v], top, rz);
+      key[v] = x[v] == kNone ? kNone : s;
+    }
+    if (a.bias) {
+      if (e0 + V <= E) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+          const u32x4_t b = *reinterpret_cast<const u32x4_any*>(a.bias + e0 + v);
+          key[v] += as_f32(b.x); key[v + 1] += as_f32(b.y); key[v + 2] += as_f32(b.z); key[v + 3] += as_f32(b.w);
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] += e0 + v < E ? a.bias[e0 + v] : 0.0f;
+      }
+    }
+  }
+  auto key64 = [&](int e, float& logit) {
+    logit = elem_value<DT>(load_bits<DT>(row + e * kElemBytes<DT>));
+    const float b = a.bias ? a.bias[e] : 0.0f;
+    if (!eligible(logit) || !eligible(b)) return (double)-INFINITY;
+    return by_logit ? (double)logit : score64(logit) + (double)b;
+  };
+
+  Two<float> two;
+#pragma unroll
+  for (int v = 0; v < V; ++v) two.add(key[v]);
+  bool kept = true;
+  if (a.groups > 1) {
+    const int lanes = E / a.groups / V, base = lane & 48;
+    auto keep = [&](auto own, bool& near) {
+      const int g = l / lanes;
+      int rank = 0;
+      bool close = false;
+      for (int o = 0; o < a.groups; ++o) {
+        const auto v = row_lane(own.value, o * lanes);
+        const float e = row_lane(own.error, o * lanes);
+        rank += v > own.value || (v == own.value && o < g);
+        close |= o != g && v <= own.value && (float)(own.value - v) <= own.error + e;
+      }
+      near = g < a.groups && rank == a.top_groups - 1 && close;
+      return rank < a.top_groups;
+    };
+    bool near;
+    kept = keep(group_value<float>(two, lanes, a.group_best, pairs[wave].f, base, base + 16), near);
+    if (__any(near)) {
+      Two<double> t64;
+#pragma unroll 1
+      for (int v = 0; v < mine; ++v) {
+        float logit;
+        t64.add(key64(e0 + v, logit));
+      }
+      kept = keep(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, base, base + 16), near);
+    }
+    if (!kept) {
+      two = Two<float>();
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = kNone;
+    }
+  }
+
+  // `cut`: at least top_k keys at or above it, and at most 16 (the lanes) once
+  // the error is taken off.  First halving between the two largest keys of
+  // every lane alone, whose top_k-th largest is a lower bound of the token's
+  // and mostly close to it; then, where that leaves too many, or a token has
+  // fewer than top_k such pairs' keys, among all keys.
+  const int k = a.top_k;
+  float cut = kLowest;
+  {
+    float lo = fminf(two.best > kNone ? two.best : INFINITY, two.next > kNone ? two.next : INFINITY), hi = two.best;
+    lo = row_all(lo, [](float p, float q) { return fminf(p, q); });
+    hi = row_all(hi, [](float p, float q) { return fmaxf(p, q); });
+    int n = row_count(__ballot(two.best > kNone)) + row_count(__ballot(two.next > kNone));
+    const bool enough = n >= k;
+    if (enough) cut = lo;
+    for (int i = 0; i < 24 && __any(enough && n > k + 1); ++i) {
+      const float mid = 0.5f * lo + 0.5f * hi;
+      const int m = row_count(__ballot(two.best >= mid)) + row_count(__ballot(two.next >= mid));
+      if (m >= k) { lo = mid; n = m; if (enough) cut = mid; }
+      else hi = mid;
+    }
+  }
+  auto slack = [&](float c) { return by_logit || c == kLowest ? c : c - 2.0f * key_error(c); };
+  // this lane's experts at or above c, bit v for expert e0 + v
+  auto in_reach = [&](float c) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) m = m + m + (key[v] >= c ? 1u : 0u);
+    return m;
+  };
+  auto row_total = [&](uint32_t m) {
+    return row_all(__builtin_popcount(m), [](int p, int q) { return p + q; });
+  };
+  uint32_t reach = in_reach(slack(cut));
+  int n = row_total(reach);
+  if (__any(n > 16)) {
+    float lo = INFINITY, hi = kNone;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      lo = key[v] > kNone ? fminf(lo, key[v]) : lo;
+      hi = fmaxf(hi, key[v]);
+    }
+    lo = row_all(lo, [](float p, float q) { return fminf(p, q); });
+    hi = row_all(hi, [](float p, float q) { return fmaxf(p, q); });
+    lo = fmaxf(lo, cut);
+    for (int i = 0; i < 40 && __any(n > 16); ++i) {
+      const float mid = 0.5f * lo + 0.5f * hi;
+      if (row_total(in_reach(mid)) >= k) {
+        lo = mid;
+        if (n > 16) {
+          reach = in_reach(slack(mid));
+          n = row_total(reach);
+        }
+      } else {
+        hi = mid;
+      }
+    }
+  }
+
+  int expert = -1, rank = l;
+  double s = 0.0;
+  bool chosen = false;
+  {
+    const bool fits = n <= 16;
+    int at = (lane & 48) + row_before(__builtin_popcount(reach));
+    if (fits) {
+#pragma unroll 1
+      for (uint32_t m = reach; m; m &= m - 1) found[wave][at++] = e0 + __builtin_ctz(m);
+    }
+    wave_sync();
+    double k64 = -INFINITY;
+    if (fits && l < n) {
+      float logit;
+      expert = found[wave][lane];
+      k64 = key64(expert, logit);
+      s = score64(logit);
+    }
+    // candidates stand in expert order, so equal keys go by lane
+    const int r = row_rank<15>(k64);
+    if (fits && l < n) {
+      rank = r;
+      chosen = r < k;
+    }
+  }
+  if (__any(n > 16)) {
+    // More experts than lanes within the error of each other (many equal
+    // logits): lane j takes the largest (key, expert) that comes after lane
+    // j - 1's.  Such a token has top_k of them, as n > 16.
+    double last = INFINITY;
+    int last_e = -1;
+    for (int j = 0; j < k; ++j) {
+      double best = -INFINITY;
+      int best_e = -1;
+      float best_x = 0.0f;
+#pragma unroll 1
+      for (int v = 0; v < (kept && n > 16 ? mine : 0); ++v) {
+        float logit;
+        const double q = key64(e0 + v, logit);
+        if ((q < last || (q == last && e0 + v > last_e)) && q > best) { best = q; best_e = e0 + v; best_x = logit; }
+      }
+      const double all = row_all(best, [](double p, double q) { return p > q ? p : q; });
+      const int e = row_all(best == all && best_e >= 0 ? best_e : 0x7FFFFFFF, [](int p, int q) { return min(p, q); });
+      const uint64_t who = __ballot(best_e == e);
+      const int from = __builtin_ctz(((uint32_t)(who >> (lane & 48)) & 0xFFFFu) | 0x10000u) & 15;
+      const float logit = row_lane(best_x, from);
+      if (n > 16 && l == j) { expert = e; s = score64(logit); chosen = true; }
+      last = all;
+      last_e = e;
+    }
+  }
+  double w = a.scale * s;
+  if (a.renormalize) {
+    const double sum = row_all(chosen ? s : 0.0, [](double p, double q) { return p + q; });
+    w = sum > 0.0 ? w / sum : 0.0;
+  }
+  if (token < a.tokens && (chosen || (l >= n && l < k))) {
+    a.index[token * k + rank] = chosen ? expert : -1;
+    a.weights[token * k + rank] = chosen ? (float)w : 0.0f;
+  }
+}
+
 // One wave per token; u: experts floats of the wave's own LDS, the gradient of each score.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __restrict__ logits, int64_t tokens, int E,
@@ -506,6 +799,21 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   int v = 1;
   while (v * 64 < a.experts) v *= 2;
   const bool whole = a.groups == 1 || (a.experts / a.groups) % v == 0;
+  // 16 lanes a token
+  const int v16 = a.experts <= 64 ? 4 : a.experts <= 128 ? 8 : 16;
+  if (a.tokens >= kRowTokens && a.experts <= 256 && a.top_k <= 16 &&
+      (a.groups == 1 || (a.experts / a.groups) % v16 == 0)) {
+    const unsigned grid = (unsigned)((a.tokens + 4 * kTokens - 1) / (4 * kTokens));
+#define CALL(DT)                                                                 \
+  if (v16 == 4) k_moe_route_rows<DT, 4><<<grid, kThreads, 0, st>>>(a);           \
+  else if (v16 == 8) k_moe_route_rows<DT, 8><<<grid, kThreads, 0, st>>>(a);      \
+  else k_moe_route_rows<DT, 16><<<grid, kThreads, 0, st>>>(a)
+    if (dt == DT_F32) { CALL(DT_F32); }
+    else if (dt == DT_BF16) { CALL(DT_BF16); }
+    else { CALL(DT_F16); }
+#undef CALL
+    return hipGetLastError();
+  }
   const size_t lds = (size_t)kTokens * a.experts * sizeof(double);   // at most 32 KB
 #define CALL(DT)                                                                             \
   if (!whole) k_moe_route_general<DT><<<(unsigned)blocks, kThreads, lds, st>>>(a);           \

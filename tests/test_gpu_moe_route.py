@@ -134,6 +134,44 @@ def test_route_far_values(score):
     check(x, 8, score=score, renormalize=False, grad=False)
 
 
+def many(g, T, E, dtype="f32", distinct=40):
+    """T tokens' logits with `distinct` different rows in a random order, so that the oracle stays quick."""
+    x = values(g, (distinct, E), dtype, 1.5)
+    return x, torch.from_numpy(g.integers(0, distinct, T)).to(dev())
+
+
+MANY = [(4096, 256, 8, dict(groups=8, top_groups=4)), (5001, 256, 8, dict()), (2050, 60, 4, dict()), (3000, 64, 16, dict()),
+        (2048, 128, 1, dict(groups=4, top_groups=1)), (2049, 17, 3, dict()), (2500, 96, 6, dict(groups=12, top_groups=5)),
+        (2500, 240, 8, dict(groups=5, top_groups=2)), (2300, 256, 16, dict(groups=2, top_groups=1, group_best=1)),
+        (2100, 384, 8, dict(groups=8, top_groups=3)), (2100, 200, 17, dict())]
+
+
+@pytest.mark.parametrize("T,E,k,kw", MANY)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_route_many_tokens(T, E, k, kw, score, dtype):
+    """The choice of a token does not hang on how many there are, nor on its neighbours: every row of a large call
+    equals the oracle's answer for it, with ties, closed experts, masked and NaN rows among them."""
+    g = np.random.default_rng(T + E)
+    x, order = many(g, T, E, dtype)
+    x[3] = 0.5
+    x[4, 1:] = float("-inf")
+    x[5, ::3] = float("-inf")
+    x[6] = float("-inf")
+    x[7, 5] = float("nan")
+    x[8] = torch.round(x[8])
+    for bias in (None, (0.1 * g.standard_normal(E)).astype(np.float32), np.zeros(E, np.float32)):
+        args = dict(score=score, renormalize=bias is not None, **kw)
+        want_w, want_e = moe.route(f64(x), k, bias=None if bias is None else bias.astype(np.float64), **args)
+        mask = torch.from_numpy(g.random(T) > 0.1).to(dev())
+        w, e = mxq.moe_route(x[order], k, bias=None if bias is None else torch.from_numpy(bias).to(dev()),
+                             token_mask=mask, **args)
+        on, at = mask.cpu().numpy(), order.cpu().numpy()
+        assert np.array_equal(e.cpu().numpy(), np.where(on[:, None], want_e[at], -1))
+        want = np.where(on[:, None], want_w[at], 0.0)
+        assert_rounded(w, want, "f32", 4 * U * np.abs(want), "weights")
+
+
 def test_route_strided_and_misaligned_logits():
     g = np.random.default_rng(14)
     base = values(g, (33, 2 * 60 + 1), "bf16")
