@@ -1,15 +1,20 @@
 // The grouped order of the routed slots and the rows' way there and back:
 // moe_plan, moe_dispatch (plain and quantized), moe_combine and its gradient.
 //
-// moe_plan is a stable counting sort of n slots by local expert, without
-// atomics on the result: a wave owns a contiguous run of slots, so an
-// exclusive scan over (expert, wave) of the waves' histograms gives every
-// wave its first row per expert, and inside 64 slots a slot's place among
-// equal experts is the number of lower lanes that hold the same expert.
+// moe_plan is a stable counting sort of n slots by local expert, bound by
+// latency: its bytes are nothing.  A workgroup places 1024 slots at a time, one
+// a thread.  A slot's row is the sum of four counts: the rows of lower experts,
+// the expert's slots in earlier tiles, in earlier waves of this tile, and in
+// lower lanes of this wave (the lanes with an equal expert, found bit by bit
+// with ballots).  Up to kPlanRecount slots every workgroup counts all of them
+// itself, which takes one launch; above, a first launch writes one histogram a
+// tile.  Integer counts do not depend on the order of the LDS atomics.
 //
-// The row kernels are HBM streams.  A lane owns a chunk of 8 consecutive
-// elements of one token and visits the token's top_k rows, so a token's row is
-// read once (dispatch) or written once (combine) whatever top_k is.
+// The row kernels are HBM streams.  A wave owns 64 chunks of 8 consecutive
+// columns of one token, so the token's rows and weights are scalars, and visits
+// its top_k rows: a token's row is read once (dispatch) or written once
+// (combine) whatever top_k is, and the combine has the loads of 8 rows in
+// flight.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -20,10 +25,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
-// Slots that one workgroup sorts by itself; more are cut into tiles.
-constexpr int64_t kPlanOneSlots = 16384;
-constexpr int64_t kPlanTile = 4096;
-constexpr int kPlanMaxTiles = 256;
+constexpr int64_t kPlanRecount = 16384;
+constexpr int kPlanMaxTiles = 128;   // histograms that every workgroup of the second launch adds up
 
 // Buckets: the local experts, and one for the slots that are not served.
 __device__ __forceinline__ int bucket_of(int expert, int first, int local) {
@@ -31,184 +34,162 @@ __device__ __forceinline__ int bucket_of(int expert, int first, int local) {
   return expert >= 0 && e < (unsigned)local ? (int)e : local;
 }
 
-// Lanes of the wave that hold the same bucket (bits < 11), among the active ones.
-__device__ __forceinline__ uint64_t same_bucket(int b, uint64_t active) {
-  uint64_t m = active;
-#pragma unroll
-  for (int i = 0; i < 11; ++i) {
-    const uint64_t set = __ballot((b >> i) & 1);
-    m &= (b >> i) & 1 ? set : ~set;
+// Lanes of the wave that hold the same bucket (of `bits` bits).
+__device__ __forceinline__ uint64_t same_bucket(int b, int bits) {
+  uint64_t m = ~0ull;
+  for (int i = 0; i < bits; ++i) {
+    const bool one = (b >> i) & 1;
+    const uint64_t set = __ballot(one);
+    m &= one ? set : ~set;
   }
   return m;
 }
 
-// Histogram of slots [lo, hi) into hist[local + 1] by the lanes of one wave.
-__device__ __forceinline__ void wave_histogram(const int32_t* __restrict__ index, int64_t lo, int64_t hi, int first,
-                                               int local, int32_t* hist) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t s = lo + lane; s < hi; s += 64) atomicAdd(&hist[bucket_of(index[s], first, local)], 1);
-}
-
-// Rows of slots [lo, hi), 64 at a time; next[b] is the wave's next row of bucket b.
-__device__ __forceinline__ void wave_place(const int32_t* __restrict__ index, int64_t lo, int64_t hi, int first,
-                                           int local, int32_t* next, int32_t* __restrict__ rows,
-                                           int32_t* __restrict__ slot_of_row) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t s0 = lo; s0 < hi; s0 += 64) {
-    const int64_t s = s0 + lane;
-    const bool on = s < hi;
-    const int b = on ? bucket_of(index[s], first, local) : 0x7FF;
-    const uint64_t same = same_bucket(b, __ballot(on));
-    const int before = __popcll(same & ((1ull << lane) - 1));
-    if (on) {
-      const int r = next[b] + before;
-      rows[s] = b < local ? r : ~r;
-      slot_of_row[r] = (int32_t)s;
-    }
-    wave_sync();                       // every lane has read next
-    if (on && before == 0) next[b] += __popcll(same);
-    wave_sync();
-  }
-}
-
-// Exclusive scan over buckets of `total` (one int per thread, bucket = thread), in LDS; returns this thread's start.
-__device__ __forceinline__ int block_exclusive_scan(int total, int32_t* part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int v = total;
+// Histogram of slots [lo, hi) into hist[local] (LDS); slots that are not served are not counted.
+__device__ __forceinline__ void count_slots(const int32_t* __restrict__ index, int64_t lo, int64_t hi, int first,
+                                            int local, int32_t* hist) {
+  constexpr int kDeep = 4;             // loads in flight
+  for (int64_t s0 = lo + threadIdx.x; s0 < hi; s0 += kDeep * kPlanThreads) {
+    int32_t e[kDeep];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
-  if (lane == 63) part[wave] = v;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w < wave; ++w) before += part[w];
-  return before + v - total;
-}
-
-// One workgroup: hist [waves][local + 1] in LDS.  local + 1 <= 1025 buckets:
-// the first 1024 are scanned one per thread and the last starts where they end.
-__global__ void __launch_bounds__(kPlanThreads) k_moe_plan_one(const int32_t* __restrict__ index, int64_t n, int first,
-                                                               int local, int32_t* __restrict__ offs,
-                                                               int32_t* __restrict__ rows,
-                                                               int32_t* __restrict__ slot_of_row) {
-  __shared__ int32_t hist[kPlanWaves * (kMaxExperts + 1)];
-  __shared__ int32_t part[kPlanWaves];
-  const int nb = local + 1, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < kPlanWaves * nb; i += kPlanThreads) hist[i] = 0;
-  __syncthreads();
-  const int64_t run = (n + kPlanThreads - 1) / kPlanThreads * 64;   // slots of a wave
-  const int64_t lo = min(n, wave * run), hi = min(n, lo + run);
-  wave_histogram(index, lo, hi, first, local, hist + wave * nb);
-  __syncthreads();
-  const int b = threadIdx.x;
-  int total = 0;
-  if (b < local)
-    for (int w = 0; w < kPlanWaves; ++w) total += hist[w * nb + b];
-  int at = block_exclusive_scan(total, part);
-  if (b < local) {
-    offs[b] = at + total;
-    if (b == local - 1) {              // the slots that are not served follow the last expert
-      int rest = at + total;
-      for (int w = 0; w < kPlanWaves; ++w) {
-        const int c = hist[w * nb + local];
-        hist[w * nb + local] = rest;
-        rest += c;
-      }
-    }
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int c = hist[w * nb + b];
-      hist[w * nb + b] = at;
-      at += c;
+    for (int u = 0; u < kDeep; ++u) e[u] = s0 + u * kPlanThreads < hi ? index[s0 + u * kPlanThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int b = bucket_of(e[u], first, local);
+      if (b < local) atomicAdd(&hist[b], 1);
     }
   }
-  __syncthreads();
-  wave_place(index, lo, hi, first, local, hist + wave * nb, rows, slot_of_row);
 }
 
-// Many workgroups: a histogram per tile, then every tile adds up what lies before it.
 __global__ void __launch_bounds__(kPlanThreads) k_moe_plan_count(const int32_t* __restrict__ index, int64_t n,
                                                                  int64_t tile, int first, int local,
                                                                  int32_t* __restrict__ counts) {
-  __shared__ int32_t hist[kMaxExperts + 1];
-  const int nb = local + 1;
-  for (int i = threadIdx.x; i < nb; i += kPlanThreads) hist[i] = 0;
+  __shared__ int32_t hist[kMaxExperts];
+  if ((int)threadIdx.x < local) hist[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t lo = blockIdx.x * tile, hi = min(n, lo + tile);
-  for (int64_t s = lo + threadIdx.x; s < hi; s += kPlanThreads) atomicAdd(&hist[bucket_of(index[s], first, local)], 1);
+  const int64_t lo = blockIdx.x * tile;
+  count_slots(index, lo, min(n, lo + tile), first, local, hist);
   __syncthreads();
-  for (int i = threadIdx.x; i < nb; i += kPlanThreads) counts[(int64_t)blockIdx.x * nb + i] = hist[i];
+  if ((int)threadIdx.x < local) counts[(int64_t)blockIdx.x * local + threadIdx.x] = hist[threadIdx.x];
 }
 
+// COUNTED: counts holds a histogram a tile.  Slots [tile * block, tile * block + tile) are placed here.
+template <bool COUNTED>
 __global__ void __launch_bounds__(kPlanThreads) k_moe_plan_place(const int32_t* __restrict__ index, int64_t n,
-                                                                 int64_t tile, int first, int local,
+                                                                 int64_t tile, int first, int local, int bits,
                                                                  const int32_t* __restrict__ counts,
                                                                  int32_t* __restrict__ offs, int32_t* __restrict__ rows,
                                                                  int32_t* __restrict__ slot_of_row) {
-  __shared__ int32_t hist[kPlanWaves * (kMaxExperts + 1)];
-  __shared__ int32_t part[kPlanWaves];
-  __shared__ int32_t rest_before;
-  const int nb = local + 1, wave = threadIdx.x >> 6, me = blockIdx.x, tiles = gridDim.x;
-  for (int i = threadIdx.x; i < kPlanWaves * nb; i += kPlanThreads) hist[i] = 0;
+  __shared__ int32_t in_wave[kPlanWaves * (kMaxExperts + 1)];
+  __shared__ int32_t before[kMaxExperts + 1], after[kMaxExperts];   // slots of an expert before this tile, and from it on
+  __shared__ uint64_t part[kPlanWaves];
+  const int nb = local + 1, b = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t0 = blockIdx.x * tile, t1 = min(n, t0 + tile);
+  int64_t s = t0 + threadIdx.x;
+  int32_t expert = s < t1 ? index[s] : -1;
+  for (int i = threadIdx.x; i < kPlanWaves * nb; i += kPlanThreads) in_wave[i] = 0;
+  if (b < local) before[b] = after[b] = 0;
   __syncthreads();
-  const int64_t t0 = me * tile, t1 = min(n, t0 + tile);
-  const int64_t run = (tile + kPlanThreads - 1) / kPlanThreads * 64;
-  const int64_t lo = min(t1, t0 + wave * run), hi = min(t1, lo + run);
-  wave_histogram(index, lo, hi, first, local, hist + wave * nb);
-  const int b = threadIdx.x;
-  int total = 0, before = 0;
-  if (b < local)
-    for (int w = 0; w < tiles; ++w) {
-      const int c = counts[(int64_t)w * nb + b];
-      total += c;
-      before += w < me ? c : 0;
-    }
-  if (b == 0) {
-    int r = 0;
-    for (int w = 0; w < me; ++w) r += counts[(int64_t)w * nb + local];
-    rest_before = r;
-  }
-  __syncthreads();
-  const int start = block_exclusive_scan(total, part);
-  if (b < local) {
-    if (me == 0) offs[b] = start + total;
-    int at = start + before;
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int c = hist[w * nb + b];
-      hist[w * nb + b] = at;
-      at += c;
-    }
-    if (b == local - 1) {
-      int rest = start + total + rest_before;
-      for (int w = 0; w < kPlanWaves; ++w) {
-        const int c = hist[w * nb + local];
-        hist[w * nb + local] = rest;
-        rest += c;
+  if constexpr (COUNTED) {
+    // threads of a bucket share its tiles
+    const int parts = kPlanThreads / local, p = b / local, e = b - p * local;
+    if (p < parts) {
+      int32_t lo = 0, hi = 0;
+#pragma unroll 4
+      for (int w = p; w < (int)gridDim.x; w += parts) {
+        const int32_t c = counts[(int64_t)w * local + e];
+        lo += w < (int)blockIdx.x ? c : 0;
+        hi += w < (int)blockIdx.x ? 0 : c;
       }
+      atomicAdd(&before[e], lo);
+      atomicAdd(&after[e], hi);
     }
+  } else {
+    count_slots(index, 0, t0, first, local, before);
+    count_slots(index, t0, n, first, local, after);
   }
   __syncthreads();
-  wave_place(index, lo, hi, first, local, hist + wave * nb, rows, slot_of_row);
+  // exclusive scan over the experts of (all slots, slots before this tile), both below 2^31
+  const uint64_t own = b < local ? ((uint64_t)(uint32_t)(before[b] + after[b]) << 32) | (uint32_t)before[b] : 0;
+  uint64_t sum = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t u = __shfl_up(sum, d);
+    if (lane >= d) sum += u;
+  }
+  if (lane == 63) part[wave] = sum;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += part[w];
+  if (b < local) {
+    if (blockIdx.x == 0) offs[b] = (int32_t)(sum >> 32);
+    before[b] += (int32_t)((sum - own) >> 32);
+    // the slots that are not served follow the last expert's
+    if (b == local - 1) before[local] = (int32_t)(sum >> 32) + (int32_t)(t0 - (int64_t)(uint32_t)sum);
+  }
+  for (;;) {
+    const int mine = s < t1 ? bucket_of(expert, first, local) : nb;     // nb: no slot
+    const uint64_t same = same_bucket(mine, bits);
+    const int lower = __popcll(same & ((1ull << lane) - 1));
+    if (s < t1 && lower == 0) in_wave[wave * nb + mine] = __popcll(same);
+    __syncthreads();
+    if (s < t1) {
+      int r = before[mine] + lower;
+      for (int w = 0; w < wave; ++w) r += in_wave[w * nb + mine];
+      rows[s] = mine < local ? r : ~r;
+      if ((uint64_t)(int64_t)r < (uint64_t)n) slot_of_row[r] = (int32_t)s;   // always, unless index changed meanwhile
+    }
+    if (s - threadIdx.x + kPlanThreads >= t1) break;                    // the same for the whole workgroup
+    s += kPlanThreads;
+    expert = s < t1 ? index[s] : -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < nb; i += kPlanThreads) {              // this round's slots lie before the next's
+      int c = 0;
+      for (int w = 0; w < kPlanWaves; ++w) {
+        c += in_wave[w * nb + i];
+        in_wave[w * nb + i] = 0;
+      }
+      before[i] += c;
+    }
+    __syncthreads();
+  }
 }
 
 int64_t plan_tile(int64_t n) {
+  if (n <= kPlanRecount) return kPlanThreads;
   const int64_t t = (n + kPlanMaxTiles - 1) / kPlanMaxTiles;
-  return max(kPlanTile, (t + kPlanThreads - 1) / kPlanThreads * kPlanThreads);
+  return (t + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
 }
 
 // ------------------------------------------------------------- row streams
-// Chunk c of the flat list tokens x chunks-per-token that this lane owns.
+constexpr int kDeep = 8;               // rows in flight
+
+// The token and the chunk of 8 columns of this lane: 64 consecutive chunks of
+// one token a wave, `segs` waves a token.
 struct Place {
   int64_t token;
   int chunk;
 };
-__device__ __forceinline__ Place place_of(int chunks) {
-  const int64_t base = (int64_t)blockIdx.x * kThreads;
-  const int64_t t0 = base / chunks;
-  const unsigned at = (unsigned)(base - t0 * chunks) + threadIdx.x;
-  const unsigned dt = at / (unsigned)chunks;
-  return {t0 + dt, (int)(at - dt * (unsigned)chunks)};
+__device__ __forceinline__ Place place_of(unsigned segs) {
+  const unsigned w = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned token = w / segs;
+  return {token, (int)((w - token * segs) * 64 + (threadIdx.x & 63))};
+}
+
+// Columns of a chunk.  The last chunk of a row whose width is no multiple of 8
+// is moved back to end with the row: it repeats the columns that it shares with
+// the chunk before it (the same values, so both may be written), and every
+// access takes 16 bytes.  NARROW rows (under 8 columns) have one chunk, of
+// `live` columns.
+struct Columns {
+  int64_t first;
+  int live, repeated;
+};
+template <bool NARROW>
+__device__ __forceinline__ Columns columns_of(int chunk, int64_t hidden) {
+  const int64_t at = (int64_t)chunk * 8;
+  if constexpr (NARROW) return {at, (int)hidden, 0};
+  const int64_t first = min(at, hidden - 8);
+  return {first, 8, (int)(at - first)};
 }
 
 // The row that a value of `rows` names, or -1.  served: whether it belongs to an expert.
@@ -218,31 +199,32 @@ __device__ __forceinline__ int64_t row_of(int32_t v, int64_t n, bool& served) {
   return r < n ? r : -1;
 }
 
-template <int DT>
+template <int DT, bool NARROW>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const uint8_t* __restrict__ x, int64_t tokens, int64_t hidden,
-                                                           int chunks, int top_k, const int32_t* __restrict__ rows,
+                                                           int chunks, unsigned segs, int top_k,
+                                                           const int32_t* __restrict__ rows,
                                                            uint8_t* __restrict__ out) {
-  const Place p = place_of(chunks);
-  if (p.token >= tokens) return;
-  const int64_t e = (int64_t)p.chunk * 8, rb = hidden * kElemBytes<DT>, n = tokens * top_k;
-  const int live = (int)min((int64_t)8, hidden - e);
-  const Raw8<DT> v = load8<DT>(x + p.token * rb, e, live);
+  const Place p = place_of(segs);
+  if (p.token >= tokens || p.chunk >= chunks) return;
+  const Columns c = columns_of<NARROW>(p.chunk, hidden);
+  const int64_t rb = hidden * kElemBytes<DT>, n = tokens * top_k;
+  const Raw8<DT> v = load8<DT>(x + p.token * rb, c.first, c.live);
   for (int j = 0; j < top_k; ++j) {
     bool served;
     const int64_t r = row_of(rows[p.token * top_k + j], n, served);
-    if (r >= 0) store8<DT>(out + r * rb, e, live, served ? v : zero8<DT>());
+    if (r >= 0) store8<DT>(out + r * rb, c.first, c.live, served ? v : zero8<DT>());
   }
 }
 
 // Four lanes hold a block of 32 columns.
 template <int DT, bool FP4>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch_quantized(const uint8_t* __restrict__ x, int64_t tokens,
-                                                                     int64_t hidden, int chunks, int top_k,
-                                                                     const int32_t* __restrict__ rows,
+                                                                     int64_t hidden, int chunks, unsigned segs,
+                                                                     int top_k, const int32_t* __restrict__ rows,
                                                                      uint8_t* __restrict__ codes,
                                                                      uint8_t* __restrict__ scales) {
-  const Place p = place_of(chunks);
-  if (p.token >= tokens) return;       // whole groups of four lanes: chunks is a multiple of 4
+  const Place p = place_of(segs);
+  if (p.token >= tokens || p.chunk >= chunks) return;   // whole groups of four lanes: chunks is a multiple of 4
   float v[8];
   to_f32<DT>(load8<DT>(x + p.token * hidden * kElemBytes<DT>, (int64_t)p.chunk * 8, 8), v);
   const uint32_t amax = group_max_u32<4>(amax_bits(v));
@@ -262,82 +244,115 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch_quantized(const uint8
   }
 }
 
-// WEIGHTED false: weights of 1.
-template <int DT, bool WEIGHTED>
+// WEIGHTED false: weights of 1.  A slot that is not served reads row 0, which
+// the caches hold, and adds nothing of it.
+template <int DT, bool WEIGHTED, bool NARROW>
 __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint8_t* __restrict__ y, int64_t tokens, int64_t hidden,
-                                                          int chunks, int top_k, const int32_t* __restrict__ rows,
+                                                          int chunks, unsigned segs, int top_k,
+                                                          const int32_t* __restrict__ rows,
                                                           const float* __restrict__ weights,
                                                           uint8_t* __restrict__ out) {
-  const Place p = place_of(chunks);
-  if (p.token >= tokens) return;
-  const int64_t e = (int64_t)p.chunk * 8, rb = hidden * kElemBytes<DT>, n = tokens * top_k;
-  const int live = (int)min((int64_t)8, hidden - e);
+  const Place p = place_of(segs);
+  if (p.token >= tokens || p.chunk >= chunks) return;
+  const Columns c = columns_of<NARROW>(p.chunk, hidden);
+  const int64_t rb = hidden * kElemBytes<DT>, n = tokens * top_k;
   float acc[8] = {};
-  for (int j = 0; j < top_k; ++j) {
-    bool served;
-    const int64_t r = row_of(rows[p.token * top_k + j], n, served);
-    if (r < 0 || !served) continue;
-    const float w = WEIGHTED ? weights[p.token * top_k + j] : 1.0f;
-    float v[8];
-    to_f32<DT>(load8<DT>(y + r * rb, e, live), v);
+  for (int j0 = 0; j0 < top_k; j0 += kDeep) {
+    Raw8<DT> raw[kDeep];
+    bool use[kDeep];
+    float w[kDeep];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
-  }
-  store8<DT>(out + p.token * rb, e, live, from_f32<DT>(acc));
-}
-
-// One workgroup per token: a lane keeps its chunks of grad_out for all slots
-// by reading them again from the caches; dots go lane -> wave -> workgroup in
-// a fixed order.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const uint8_t* __restrict__ grad_out,
-                                                              const uint8_t* __restrict__ y, int64_t tokens,
-                                                              int64_t hidden, int chunks, int top_k,
-                                                              const int32_t* __restrict__ rows,
-                                                              const float* __restrict__ weights,
-                                                              uint8_t* __restrict__ grad_y,
-                                                              float* __restrict__ grad_weights) {
-  __shared__ float dots[kMaxTopK][kThreads / 64];
-  const int64_t token = blockIdx.x, rb = hidden * kElemBytes<DT>, n = tokens * top_k;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int j0 = 0; j0 < top_k; j0 += kMaxTopK) {
-    const int jn = min(kMaxTopK, top_k - j0);
-    for (int j = 0; j < jn; ++j) {
-      const int64_t slot = token * top_k + j0 + j;
+    for (int u = 0; u < kDeep; ++u) {
+      const int64_t slot = p.token * top_k + min(j0 + u, top_k - 1);
       bool served;
       const int64_t r = row_of(rows[slot], n, served);
-      float dot = 0.0f;
-      if (r >= 0) {
-        const float w = served && grad_y ? weights[slot] : 0.0f;
-        for (int c = threadIdx.x; c < chunks; c += kThreads) {
-          const int64_t e = (int64_t)c * 8;
-          const int live = (int)min((int64_t)8, hidden - e);
-          float g[8], v[8];
-          to_f32<DT>(load8<DT>(grad_out + token * rb, e, live), g);
-          if (grad_weights && served) {
-            to_f32<DT>(load8<DT>(y + r * rb, e, live), v);
+      use[u] = served && r >= 0 && j0 + u < top_k;
+      w[u] = WEIGHTED ? weights[slot] : 1.0f;
+      raw[u] = load8<DT>(y + (use[u] ? r : 0) * rb, c.first, c.live);
+    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(g[i], v[i], dot);
+    for (int u = 0; u < kDeep; ++u) {
+      if (!use[u]) continue;
+      float v[8];
+      to_f32<DT>(raw[u], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[u], v[i], acc[i]);
+    }
+  }
+  store8<DT>(out + p.token * rb, c.first, c.live, from_f32<DT>(acc));
+}
+
+// One workgroup per token, 8 slots at a time: a lane reads its chunk of
+// grad_out once for the 8, and keeps 8 partial dots, which go lane -> wave ->
+// workgroup in a fixed order.
+constexpr int kBwdWaves = 8;
+template <int DT, bool GY, bool GW, bool NARROW>
+__global__ void __launch_bounds__(kBwdWaves * 64) k_moe_combine_bwd(const uint8_t* __restrict__ grad_out,
+                                                                    const uint8_t* __restrict__ y, int64_t tokens,
+                                                                    int64_t hidden, int chunks, int top_k,
+                                                                    const int32_t* __restrict__ rows,
+                                                                    const float* __restrict__ weights,
+                                                                    uint8_t* __restrict__ grad_y,
+                                                                    float* __restrict__ grad_weights) {
+  __shared__ float dots[kDeep][kBwdWaves];
+  const int64_t token = blockIdx.x, rb = hidden * kElemBytes<DT>, n = tokens * top_k;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int j0 = 0; j0 < top_k; j0 += kDeep) {
+    int64_t r[kDeep];
+    bool served[kDeep];
+    float w[kDeep], dot[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int64_t slot = token * top_k + min(j0 + u, top_k - 1);
+      r[u] = row_of(rows[slot], n, served[u]);
+      served[u] = served[u] && r[u] >= 0 && j0 + u < top_k;
+      if (j0 + u >= top_k) r[u] = -1;
+      w[u] = GY && served[u] ? weights[slot] : 0.0f;
+      dot[u] = 0.0f;
+    }
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+      const Columns at = columns_of<NARROW>(c, hidden);
+      Raw8<DT> raw[kDeep];
+      float g[8];
+      if constexpr (GW) {
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) raw[u] = load8<DT>(y + (served[u] ? r[u] : 0) * rb, at.first, at.live);
+      }
+      to_f32<DT>(load8<DT>(grad_out + token * rb, at.first, at.live), g);
+      float once[8];                   // g where this chunk's columns count for the dots
+#pragma unroll
+      for (int i = 0; i < 8; ++i) once[i] = i < at.repeated ? 0.0f : g[i];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        float v[8];
+        if constexpr (GW) {
+          if (served[u]) {
+            to_f32<DT>(raw[u], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot[u] = __builtin_fmaf(once[i], v[i], dot[u]);
           }
-          if (grad_y) {
+        }
+        if constexpr (GY) {
+          if (r[u] >= 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = served ? w * g[i] : 0.0f;
-            store8<DT>(grad_y + r * rb, e, live, from_f32<DT>(v));
+            for (int i = 0; i < 8; ++i) v[i] = w[u] * g[i];
+            store8<DT>(grad_y + r[u] * rb, at.first, at.live, served[u] ? from_f32<DT>(v) : zero8<DT>());
           }
         }
       }
-      if (grad_weights) {
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
-        if (lane == 0) dots[j][wave] = dot;
-      }
     }
-    if (grad_weights) {
-      __syncthreads();
-      if ((int)threadIdx.x < jn) {
-        float s = 0.0f;
+    if constexpr (GW) {
 #pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w) s += dots[threadIdx.x][w];
+      for (int u = 0; u < kDeep; ++u) {
+        float d = dot[u];
+#pragma unroll
+        for (int i = 32; i > 0; i >>= 1) d += __shfl_xor(d, i);
+        if (lane == 0) dots[u][wave] = d;
+      }
+      __syncthreads();
+      if ((int)threadIdx.x < min(kDeep, top_k - j0)) {
+        float s = 0.0f;
+        for (int i = 0; i < waves; ++i) s += dots[threadIdx.x][i];
         grad_weights[token * top_k + j0 + threadIdx.x] = s;
       }
       __syncthreads();
@@ -345,47 +360,59 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const uint8_t* __r
   }
 }
 
-int64_t flat_blocks(int64_t tokens, int64_t chunks) { return (tokens * chunks + kThreads - 1) / kThreads; }
+// Waves a token of the row streams, and their workgroups (0: more than a launch takes).
+unsigned segs_of(int chunks) { return (unsigned)(chunks + 63) / 64; }
+unsigned stream_blocks(int64_t tokens, int chunks) {
+  const int64_t waves = tokens * segs_of(chunks);
+  return waves > 0x7FFFFFF0 ? 0u : (unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64));
+}
 
 }  // namespace
 
 int64_t plan_workspace_bytes(int64_t slots, int local) {
-  if (slots <= kPlanOneSlots) return 0;
+  if (slots <= kPlanRecount) return 0;
   const int64_t tile = plan_tile(slots);
-  return (slots + tile - 1) / tile * (local + 1) * 4;
+  return (slots + tile - 1) / tile * local * 4;
 }
 
 hipError_t launch_moe_plan(const int32_t* index, int64_t slots, int first, int local, int32_t* offs, int32_t* rows,
                            int32_t* slot_of_row, int32_t* workspace, hipStream_t st) {
-  if (slots <= kPlanOneSlots) {
-    k_moe_plan_one<<<1, kPlanThreads, 0, st>>>(index, slots, first, local, offs, rows, slot_of_row);
+  const int64_t tile = plan_tile(slots);
+  const int tiles = (int)max((int64_t)1, (slots + tile - 1) / tile);
+  int bits = 1;                        // of the buckets 0 .. local, and local + 1 for lanes without a slot
+  while ((1 << bits) <= local + 1) ++bits;
+  if (slots <= kPlanRecount) {
+    k_moe_plan_place<false><<<tiles, kPlanThreads, 0, st>>>(index, slots, tile, first, local, bits, nullptr, offs, rows,
+                                                            slot_of_row);
     return hipGetLastError();
   }
-  const int64_t tile = plan_tile(slots);
-  const int tiles = (int)((slots + tile - 1) / tile);
   k_moe_plan_count<<<tiles, kPlanThreads, 0, st>>>(index, slots, tile, first, local, workspace);
-  k_moe_plan_place<<<tiles, kPlanThreads, 0, st>>>(index, slots, tile, first, local, workspace, offs, rows,
-                                                     slot_of_row);
+  k_moe_plan_place<true><<<tiles, kPlanThreads, 0, st>>>(index, slots, tile, first, local, bits, workspace, offs, rows,
+                                                         slot_of_row);
   return hipGetLastError();
 }
 
-#define MXQ_BY_DTYPE(dt, CALL)                 \
-  do {                                         \
-    if ((dt) == DT_F32) { CALL(DT_F32); }      \
+#define MXQ_BY_DTYPE(dt, CALL)                   \
+  do {                                           \
+    if ((dt) == DT_F32) { CALL(DT_F32); }        \
     else if ((dt) == DT_BF16) { CALL(DT_BF16); } \
-    else { CALL(DT_F16); }                     \
+    else { CALL(DT_F16); }                       \
   } while (0)
 
 hipError_t launch_moe_dispatch(const void* x, int dt, int64_t tokens, int64_t hidden, int top_k, const int32_t* rows,
                                void* out, hipStream_t st) {
   const int chunks = (int)((hidden + 7) / 8);
-  const int64_t blocks = flat_blocks(tokens, chunks);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-#define CALL(DT)                                                                                                     \
-  k_moe_dispatch<DT><<<(unsigned)blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden, chunks, top_k, rows, \
-                                                            (uint8_t*)out)
+  const unsigned blocks = stream_blocks(tokens, chunks), segs = segs_of(chunks);
+  if (blocks == 0) return hipErrorInvalidValue;
+#define LAUNCH(DT, NARROW)                                                                                          \
+  k_moe_dispatch<DT, NARROW><<<blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden, chunks, segs, top_k, \
+                                                          rows, (uint8_t*)out)
+#define CALL(DT)                      \
+  if (hidden < 8) LAUNCH(DT, true);   \
+  else LAUNCH(DT, false)
   MXQ_BY_DTYPE(dt, CALL);
 #undef CALL
+#undef LAUNCH
   return hipGetLastError();
 }
 
@@ -393,15 +420,15 @@ hipError_t launch_moe_dispatch_quantized(const void* x, int dt, int64_t tokens, 
                                          const int32_t* rows, int fmt, uint8_t* codes, uint8_t* scales,
                                          hipStream_t st) {
   const int chunks = (int)(hidden / 8);
-  const int64_t blocks = flat_blocks(tokens, chunks);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const unsigned blocks = stream_blocks(tokens, chunks), segs = segs_of(chunks);
+  if (blocks == 0) return hipErrorInvalidValue;
 #define CALL(DT)                                                                                                    \
   if (fmt == FMT_MXFP4)                                                                                             \
-    k_moe_dispatch_quantized<DT, true><<<(unsigned)blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden,   \
-                                                                              chunks, top_k, rows, codes, scales);  \
+    k_moe_dispatch_quantized<DT, true><<<blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden,   \
+                                                                              chunks, segs, top_k, rows, codes, scales);  \
   else                                                                                                              \
-    k_moe_dispatch_quantized<DT, false><<<(unsigned)blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden,  \
-                                                                               chunks, top_k, rows, codes, scales)
+    k_moe_dispatch_quantized<DT, false><<<blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden,  \
+                                                                               chunks, segs, top_k, rows, codes, scales)
   MXQ_BY_DTYPE(dt, CALL);
 #undef CALL
   return hipGetLastError();
@@ -410,17 +437,20 @@ hipError_t launch_moe_dispatch_quantized(const void* x, int dt, int64_t tokens, 
 hipError_t launch_moe_combine(const void* y, int dt, int64_t tokens, int64_t hidden, int top_k, const int32_t* rows,
                               const float* weights, void* out, hipStream_t st) {
   const int chunks = (int)((hidden + 7) / 8);
-  const int64_t blocks = flat_blocks(tokens, chunks);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-#define CALL(DT)                                                                                                   \
-  if (weights)                                                                                                     \
-    k_moe_combine<DT, true><<<(unsigned)blocks, kThreads, 0, st>>>((const uint8_t*)y, tokens, hidden, chunks,      \
-                                                                   top_k, rows, weights, (uint8_t*)out);           \
-  else                                                                                                             \
-    k_moe_combine<DT, false><<<(unsigned)blocks, kThreads, 0, st>>>((const uint8_t*)y, tokens, hidden, chunks,     \
-                                                                    top_k, rows, weights, (uint8_t*)out)
+  const unsigned blocks = stream_blocks(tokens, chunks), segs = segs_of(chunks);
+  if (blocks == 0) return hipErrorInvalidValue;
+#define LAUNCH(DT, WEIGHTED, NARROW)                                                                              \
+  k_moe_combine<DT, WEIGHTED, NARROW><<<blocks, kThreads, 0, st>>>((const uint8_t*)y, tokens, hidden, chunks,    \
+                                                                   segs, top_k, rows, weights, (uint8_t*)out)
+#define CALL(DT)                                        \
+  if (hidden < 8) {                                     \
+    if (weights) LAUNCH(DT, true, true);                \
+    else LAUNCH(DT, false, true);                       \
+  } else if (weights) LAUNCH(DT, true, false);          \
+  else LAUNCH(DT, false, false)
   MXQ_BY_DTYPE(dt, CALL);
 #undef CALL
+#undef LAUNCH
   return hipGetLastError();
 }
 
@@ -428,13 +458,24 @@ hipError_t launch_moe_combine_bwd(const void* grad_out, const void* y, int dt, i
                                   int top_k, const int32_t* rows, const float* weights, void* grad_y,
                                   float* grad_weights, hipStream_t st) {
   const int chunks = (int)((hidden + 7) / 8);
-  if (tokens > 0x7FFFFFFF) return hipErrorInvalidValue;
-#define CALL(DT)                                                                                               \
-  k_moe_combine_bwd<DT><<<(unsigned)tokens, kThreads, 0, st>>>((const uint8_t*)grad_out, (const uint8_t*)y,    \
-                                                               tokens, hidden, chunks, top_k, rows, weights,   \
-                                                               (uint8_t*)grad_y, grad_weights)
+  // waves of a workgroup: as few rounds over the columns as 8 waves give, and no idle wave in the last
+  const int segs = max(1, (int)segs_of(chunks)), rounds = (segs + kBwdWaves - 1) / kBwdWaves;
+  const unsigned threads = 64u * ((segs + rounds - 1) / rounds);
+#define LAUNCH(DT, GY, GW, NARROW)                                                                                \
+  k_moe_combine_bwd<DT, GY, GW, NARROW><<<(unsigned)tokens, threads, 0, st>>>(                                   \
+      (const uint8_t*)grad_out, (const uint8_t*)y, tokens, hidden, chunks, top_k, rows, weights, (uint8_t*)grad_y, \
+      grad_weights)
+#define WANTED(DT, NARROW)                                        \
+  if (grad_y && grad_weights) LAUNCH(DT, true, true, NARROW);     \
+  else if (grad_y) LAUNCH(DT, true, false, NARROW);               \
+  else LAUNCH(DT, false, true, NARROW)
+#define CALL(DT)                          \
+  if (hidden < 8) { WANTED(DT, true); }   \
+  else { WANTED(DT, false); }
   MXQ_BY_DTYPE(dt, CALL);
 #undef CALL
+#undef WANTED
+#undef LAUNCH
   return hipGetLastError();
 }
 
