@@ -50,16 +50,28 @@ __device__ __forceinline__ void store_bits(uint8_t* p, uint32_t b) {
   else *reinterpret_cast<u16_any*>(p) = (uint16_t)b;
 }
 
+// 16 bytes at any address; STREAM goes past the caches (non-temporal).
+template <bool STREAM>
+__device__ __forceinline__ u32x4_t load16(const uint8_t* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+  else return *reinterpret_cast<const u32x4_any*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint8_t* p, u32x4_t v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
+  else *reinterpret_cast<u32x4_any*>(p) = v;
+}
+
 // Elements e .. e + 7 of the row at `row`, of which `n` (1..8) exist; the others read as 0.
-template <int DT>
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ Raw8<DT> load8(const uint8_t* row, int64_t e, int n) {
   Raw8<DT> r;
   const uint8_t* p = row + e * kElemBytes<DT>;
   if (n == 8) {
-    const u32x4_t a = *reinterpret_cast<const u32x4_any*>(p);
+    const u32x4_t a = load16<STREAM>(p);
     r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
     if constexpr (DT == DT_F32) {
-      const u32x4_t b = *reinterpret_cast<const u32x4_any*>(p + 16);
+      const u32x4_t b = load16<STREAM>(p + 16);
       r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
     }
   } else {
@@ -75,12 +87,12 @@ __device__ __forceinline__ Raw8<DT> load8(const uint8_t* row, int64_t e, int n) 
   }
   return r;
 }
-template <int DT>
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ void store8(uint8_t* row, int64_t e, int n, const Raw8<DT>& r) {
   uint8_t* p = row + e * kElemBytes<DT>;
   if (n == 8) {
-    *reinterpret_cast<u32x4_any*>(p) = u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]};
-    if constexpr (DT == DT_F32) *reinterpret_cast<u32x4_any*>(p + 16) = u32x4_t{r.w[4], r.w[5], r.w[6], r.w[7]};
+    store16<STREAM>(p, u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]});
+    if constexpr (DT == DT_F32) store16<STREAM>(p + 16, u32x4_t{r.w[4], r.w[5], r.w[6], r.w[7]});
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i)

@@ -178,14 +178,17 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// v of the lane that the DPP control names (one that names a lane for every
+// lane: with bound_ctrl the old value does not matter, so the move folds into
+// the operation that uses it).
 template <int CTRL, typename T>
 __device__ __forceinline__ T dpp_value(T v) {
+  auto move = [](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, CTRL, 0xF, 0xF, true); };
   if constexpr (sizeof(T) == 4) {
-    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+    return __builtin_bit_cast(T, move(__builtin_bit_cast(uint32_t, v)));
   } else {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = dpp<CTRL>((uint32_t)b), hi = dpp<CTRL>((uint32_t)(b >> 32));
-    return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+    return __builtin_bit_cast(T, ((uint64_t)move((uint32_t)(b >> 32)) << 32) | move((uint32_t)b));
   }
 }
 // `op` over the wave, the same in every lane: within rows of 16 by DPP, across them by lane reads.
@@ -490,13 +493,13 @@ __device__ __forceinline__ int row_rank(double key) {
   if constexpr (N == 0) return 0;
   else {
     const double k = dpp_value<0x120 + N>(key);       // row_ror: from lane - N
-    return (int)(k > key || (k == key && (int)(threadIdx.x & 15) >= N)) + row_rank<N - 1>(key);
+    return ((int)(k > key) | ((int)(k == key) & (int)((threadIdx.x & 15) >= N))) + row_rank<N - 1>(key);
   }
 }
 
 // Experts l * V .. l * V + V - 1 in lane l of a token's row; experts <= 16 V,
 // top_k <= 16, a group (if there are groups) is whole lanes.
-template <int DT, int V>
+template <int DT, int V, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   __shared__ int32_t found[kTokens][64];
   __shared__ GroupPairs pairs[kTokens];
@@ -527,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   const bool by_logit = !a.bias && a.groups == 1;
   float top = kNone;
   double z = 1.0;
-  if (!a.sigmoid) {
+  if (!SIGMOID) {
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
     top = row_all(top, [](float p, float q) { return fmaxf(p, q); });
@@ -538,16 +541,16 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       z = row_all(s, [](double p, double q) { return p + q; });
     }
   }
-  auto score64 = [&](float v) { return a.sigmoid ? sigmoid_f64((double)v) : exp((double)v - (double)top) / z; };
+  auto score64 = [&](float v) { return SIGMOID ? sigmoid_f64((double)v) : exp((double)v - (double)top) / z; };
   // fp32 keys; where x is NaN the key is too, and no comparison takes it
   if (by_logit) {
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = x[v];
   } else {
-    const float rz = a.sigmoid ? 1.0f : (float)(1.0 / z);
+    const float rz = SIGMOID ? 1.0f : (float)(1.0 / z);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float s = a.sigmoid ? sigmoid_key(x[v]) : softmax_key(x[v], top, rz);
+      const float s = SIGMOID ? sigmoid_key(x[v]) : softmax_key(x[v], top, rz);
       key[v] = x[v] == kNone ? kNone : s;
     }
     if (a.bias) {
@@ -563,11 +566,13 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       }
     }
   }
-  auto key64 = [&](int e, float& logit) {
-    logit = elem_value<DT>(load_bits<DT>(row + e * kElemBytes<DT>));
+  // fp64 score s of expert e of this token, and its key
+  auto key64 = [&](int e, double& s) {
+    const float logit = elem_value<DT>(load_bits<DT>(row + e * kElemBytes<DT>));
     const float b = a.bias ? a.bias[e] : 0.0f;
-    if (!eligible(logit) || !eligible(b)) return (double)-INFINITY;
-    return by_logit ? (double)logit : score64(logit) + (double)b;
+    s = score64(logit);
+    if (!((int)eligible(logit) & (int)eligible(b))) return (double)-INFINITY;
+    return by_logit ? (double)logit : s + (double)b;
   };
 
   Two<float> two;
@@ -579,12 +584,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     auto keep = [&](auto own, bool& near) {
       const int g = l / lanes;
       int rank = 0;
-      bool close = false;
+      int close = 0;
+      const float error = 2.0f * row_all(own.error, [](float p, float q) { return fmaxf(p, q); });
       for (int o = 0; o < a.groups; ++o) {
         const auto v = row_lane(own.value, o * lanes);
-        const float e = row_lane(own.error, o * lanes);
-        rank += v > own.value || (v == own.value && o < g);
-        close |= o != g && v <= own.value && (float)(own.value - v) <= own.error + e;
+        rank += (int)(v > own.value) | ((int)(v == own.value) & (int)(o < g));
+        close |= (int)(o != g) & (int)(v <= own.value) & (int)((float)(own.value - v) <= error);
       }
       near = g < a.groups && rank == a.top_groups - 1 && close;
       return rank < a.top_groups;
@@ -595,8 +600,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       Two<double> t64;
 #pragma unroll 1
       for (int v = 0; v < mine; ++v) {
-        float logit;
-        t64.add(key64(e0 + v, logit));
+        double unused;
+        t64.add(key64(e0 + v, unused));
       }
       kept = keep(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, base, base + 16), near);
     }
@@ -678,10 +683,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     wave_sync();
     double k64 = -INFINITY;
     if (fits && l < n) {
-      float logit;
       expert = found[wave][lane];
-      k64 = key64(expert, logit);
-      s = score64(logit);
+      k64 = key64(expert, s);
     }
     // candidates stand in expert order, so equal keys go by lane
     const int r = row_rank<15>(k64);
@@ -699,19 +702,19 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     for (int j = 0; j < k; ++j) {
       double best = -INFINITY;
       int best_e = -1;
-      float best_x = 0.0f;
+      double best_s = 0.0;
 #pragma unroll 1
       for (int v = 0; v < (kept && n > 16 ? mine : 0); ++v) {
-        float logit;
-        const double q = key64(e0 + v, logit);
-        if ((q < last || (q == last && e0 + v > last_e)) && q > best) { best = q; best_e = e0 + v; best_x = logit; }
+        double sv;
+        const double q = key64(e0 + v, sv);
+        if ((q < last || (q == last && e0 + v > last_e)) && q > best) { best = q; best_e = e0 + v; best_s = sv; }
       }
       const double all = row_all(best, [](double p, double q) { return p > q ? p : q; });
       const int e = row_all(best == all && best_e >= 0 ? best_e : 0x7FFFFFFF, [](int p, int q) { return min(p, q); });
       const uint64_t who = __ballot(best_e == e);
       const int from = __builtin_ctz(((uint32_t)(who >> (lane & 48)) & 0xFFFFu) | 0x10000u) & 15;
-      const float logit = row_lane(best_x, from);
-      if (n > 16 && l == j) { expert = e; s = score64(logit); chosen = true; }
+      const double sv = row_lane(best_s, from);
+      if (n > 16 && l == j) { expert = e; s = sv; chosen = true; }
       last = all;
       last_e = e;
     }
@@ -804,14 +807,18 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   if (a.tokens >= kRowTokens && a.experts <= 256 && a.top_k <= 16 &&
       (a.groups == 1 || (a.experts / a.groups) % v16 == 0)) {
     const unsigned grid = (unsigned)((a.tokens + 4 * kTokens - 1) / (4 * kTokens));
-#define CALL(DT)                                                                 \
-  if (v16 == 4) k_moe_route_rows<DT, 4><<<grid, kThreads, 0, st>>>(a);           \
-  else if (v16 == 8) k_moe_route_rows<DT, 8><<<grid, kThreads, 0, st>>>(a);      \
-  else k_moe_route_rows<DT, 16><<<grid, kThreads, 0, st>>>(a)
+#define LAUNCH(DT, SIGMOID)                                                               \
+  if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<grid, kThreads, 0, st>>>(a);           \
+  else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<grid, kThreads, 0, st>>>(a);      \
+  else k_moe_route_rows<DT, 16, SIGMOID><<<grid, kThreads, 0, st>>>(a)
+#define CALL(DT)                            \
+  if (a.sigmoid) { LAUNCH(DT, true); }      \
+  else { LAUNCH(DT, false); }
     if (dt == DT_F32) { CALL(DT_F32); }
     else if (dt == DT_BF16) { CALL(DT_BF16); }
     else { CALL(DT_F16); }
 #undef CALL
+#undef LAUNCH
     return hipGetLastError();
   }
   const size_t lds = (size_t)kTokens * a.experts * sizeof(double);   // at most 32 KB

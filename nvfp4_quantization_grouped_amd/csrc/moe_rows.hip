@@ -208,11 +208,11 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const uint8_t* __rest
   if (p.token >= tokens || p.chunk >= chunks) return;
   const Columns c = columns_of<NARROW>(p.chunk, hidden);
   const int64_t rb = hidden * kElemBytes<DT>, n = tokens * top_k;
-  const Raw8<DT> v = load8<DT>(x + p.token * rb, c.first, c.live);
+  const Raw8<DT> v = load8<DT, true>(x + p.token * rb, c.first, c.live);
   for (int j = 0; j < top_k; ++j) {
     bool served;
     const int64_t r = row_of(rows[p.token * top_k + j], n, served);
-    if (r >= 0) store8<DT>(out + r * rb, c.first, c.live, served ? v : zero8<DT>());
+    if (r >= 0) store8<DT, true>(out + r * rb, c.first, c.live, served ? v : zero8<DT>());
   }
 }
 
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint8_t* __restr
       const int64_t r = row_of(rows[slot], n, served);
       use[u] = served && r >= 0 && j0 + u < top_k;
       w[u] = WEIGHTED ? weights[slot] : 1.0f;
-      raw[u] = load8<DT>(y + (use[u] ? r : 0) * rb, c.first, c.live);
+      raw[u] = load8<DT, true>(y + (use[u] ? r : 0) * rb, c.first, c.live);
     }
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint8_t* __restr
       for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[u], v[i], acc[i]);
     }
   }
-  store8<DT>(out + p.token * rb, c.first, c.live, from_f32<DT>(acc));
+  store8<DT, true>(out + p.token * rb, c.first, c.live, from_f32<DT>(acc));
 }
 
 // One workgroup per token, 8 slots at a time: a lane reads its chunk of
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kBwdWaves * 64) k_moe_combine_bwd(const uint8_
       float g[8];
       if constexpr (GW) {
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) raw[u] = load8<DT>(y + (served[u] ? r[u] : 0) * rb, at.first, at.live);
+        for (int u = 0; u < kDeep; ++u) raw[u] = load8<DT, true>(y + (served[u] ? r[u] : 0) * rb, at.first, at.live);
       }
       to_f32<DT>(load8<DT>(grad_out + token * rb, at.first, at.live), g);
       float once[8];                   // g where this chunk's columns count for the dots
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kBwdWaves * 64) k_moe_combine_bwd(const uint8_
           if (r[u] >= 0) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = w[u] * g[i];
-            store8<DT>(grad_y + r[u] * rb, at.first, at.live, served[u] ? from_f32<DT>(v) : zero8<DT>());
+            store8<DT, true>(grad_y + r[u] * rb, at.first, at.live, served[u] ? from_f32<DT>(v) : zero8<DT>());
           }
         }
       }

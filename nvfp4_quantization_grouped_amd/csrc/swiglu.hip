@@ -34,16 +34,16 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_fwd(const uint8_t* __restri
     const int64_t row = i / chunks;
     const int c = (int)(i - row * chunks);
     if (row >= count) {
-      store8<DT>(h, i * 8, 8, zero8<DT>());
+      store8<DT, true>(h, i * 8, 8, zero8<DT>());
       continue;
     }
     const int64_t at = row * 2 * chunks + c;     // chunk of gate; up is `chunks` further
     float g[8], u[8], o[8];
-    to_f32<DT>(load8<DT>(gate_up, at * 8, 8), g);
-    to_f32<DT>(load8<DT>(gate_up, (at + chunks) * 8, 8), u);
+    to_f32<DT>(load8<DT, true>(gate_up, at * 8, 8), g);
+    to_f32<DT>(load8<DT, true>(gate_up, (at + chunks) * 8, 8), u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] = g[k] * sigmoid_f32(g[k]) * u[k];
-    store8<DT>(h, i * 8, 8, from_f32<DT>(o));
+    store8<DT, true>(h, i * 8, 8, from_f32<DT>(o));
     if constexpr (KEEP) {
       const int kg = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(g)));
       const int ku = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(u)));
@@ -70,19 +70,19 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const uint8_t* __restri
     const int c = (int)(i - row * chunks);
     const int64_t at = row * 2 * chunks + c;
     if (row >= count) {
-      store8<DT>(grad, at * 8, 8, zero8<DT>());
-      store8<DT>(grad, (at + chunks) * 8, 8, zero8<DT>());
+      store8<DT, true>(grad, at * 8, 8, zero8<DT>());
+      store8<DT, true>(grad, (at + chunks) * 8, 8, zero8<DT>());
       continue;
     }
     float g[8], u[8], d[8];
-    to_f32<DT>(load8<DT>(grad_h, i * 8, 8), d);
+    to_f32<DT>(load8<DT, true>(grad_h, i * 8, 8), d);
     if constexpr (KEPT) {
       decode_fp8(*reinterpret_cast<const u32x2_any*>(codes + at * 8), e8m0_to_f32(scales[at >> 2]), g);
       decode_fp8(*reinterpret_cast<const u32x2_any*>(codes + (at + chunks) * 8),
                  e8m0_to_f32(scales[(at + chunks) >> 2]), u);
     } else {
-      to_f32<DT>(load8<DT>(gate_up, at * 8, 8), g);
-      to_f32<DT>(load8<DT>(gate_up, (at + chunks) * 8, 8), u);
+      to_f32<DT>(load8<DT, true>(gate_up, at * 8, 8), g);
+      to_f32<DT>(load8<DT, true>(gate_up, (at + chunks) * 8, 8), u);
     }
     float dg[8], du[8];
 #pragma unroll
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const uint8_t* __restri
       dg[k] = d[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
       du[k] = d[k] * g[k] * s;
     }
-    store8<DT>(grad, at * 8, 8, from_f32<DT>(dg));
-    store8<DT>(grad, (at + chunks) * 8, 8, from_f32<DT>(du));
+    store8<DT, true>(grad, at * 8, 8, from_f32<DT>(dg));
+    store8<DT, true>(grad, (at + chunks) * 8, 8, from_f32<DT>(du));
   }
 }
 
