@@ -62,6 +62,17 @@ __device__ __forceinline__ void store16(uint8_t* p, u32x4_t v) {
   else *reinterpret_cast<u32x4_any*>(p) = v;
 }
 
+template <bool STREAM>
+__device__ __forceinline__ void store_8(uint8_t* p, u32x2_t v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any*>(p));
+  else *reinterpret_cast<u32x2_any*>(p) = v;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store4(uint8_t* p, uint32_t v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32_any*>(p));
+  else *reinterpret_cast<u32_any*>(p) = v;
+}
+
 // Elements e .. e + 7 of the row at `row`, of which `n` (1..8) exist; the others read as 0.
 template <int DT, bool STREAM = false>
 __device__ __forceinline__ Raw8<DT> load8(const uint8_t* row, int64_t e, int n) {
@@ -156,6 +167,15 @@ __device__ __forceinline__ uint32_t encode_fp4(const float (&v)[8], float s) {
   c = enc_fp4_f2<1>(c, v[2] + 0.0f, v[3] + 0.0f, s);
   c = enc_fp4_f2<2>(c, v[4] + 0.0f, v[5] + 0.0f, s);
   return enc_fp4_f2<3>(c, v[6] + 0.0f, v[7] + 0.0f, s);
+}
+
+// E8M0 bytes of four blocks of 32 columns, block b in byte b, in every lane of
+// the 16 (aligned) that hold them; k is the block's exponent, the same in its
+// four lanes, whose chunks are 16 consecutive ones from a multiple of 16.
+__device__ __forceinline__ uint32_t scale_bytes(int k, int chunk) {
+  uint32_t b = (uint32_t)(k + 127) << (8 * ((chunk >> 2) & 3));
+  b |= dpp<0x141>(b);                  // row_half_mirror: the other block of 8 lanes
+  return b | dpp<0x140>(b);            // row_mirror: the other 8 lanes
 }
 
 // exp(-a) for a >= 0 to a few ulp: the rounding error of a * log2(e), and the

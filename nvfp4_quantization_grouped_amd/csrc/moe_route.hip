@@ -279,6 +279,28 @@ __device__ __forceinline__ bool group_kept(const GroupValue<T>& own, int groups,
   return rank < top;
 }
 
+// Logits of experts e0 .. e0 + V - 1 of a row, of which `mine` exist; the others read as -inf.
+template <int DT, int V>
+__device__ __forceinline__ void load_logits(const uint8_t* row, int e0, int mine, float (&x)[V]) {
+  if (V % 4 == 0 && mine == V) {
+#pragma unroll
+    for (int v = 0; v + 3 < V; v += 4) {
+      if constexpr (DT == DT_F32) {
+        const u32x4_t w = *reinterpret_cast<const u32x4_any*>(row + (e0 + v) * 4);
+        x[v] = as_f32(w.x); x[v + 1] = as_f32(w.y); x[v + 2] = as_f32(w.z); x[v + 3] = as_f32(w.w);
+      } else {
+        const u32x2_t w = *reinterpret_cast<const u32x2_any*>(row + (e0 + v) * 2);
+        x[v] = elem_value<DT>(w.x & 0xFFFFu); x[v + 1] = elem_value<DT>(w.x >> 16);
+        x[v + 2] = elem_value<DT>(w.y & 0xFFFFu); x[v + 3] = elem_value<DT>(w.y >> 16);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : -INFINITY;
+  }
+}
+
 struct Candidate {
   int expert;
   float logit;
@@ -298,9 +320,9 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
   const int e0 = lane * V, mine = alive ? min(V, max(0, E - e0)) : 0;
 
   float x[V], key[V], bias[V];
+  load_logits<DT, V>(row, e0, mine, x);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : -INFINITY;
     bias[v] = a.bias && v < mine ? a.bias[e0 + v] : 0.0f;
     if (!(x[v] > -INFINITY)) x[v] = -INFINITY;            // NaN too
   }
@@ -511,22 +533,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   constexpr float kNone = -INFINITY, kLowest = -0x1.fffffep+127f;
 
   float x[V], key[V];
-  if (mine == V) {
-#pragma unroll
-    for (int v = 0; v < V; v += 4) {
-      if constexpr (DT == DT_F32) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_any*>(row + (e0 + v) * 4);
-        x[v] = as_f32(w.x); x[v + 1] = as_f32(w.y); x[v + 2] = as_f32(w.z); x[v + 3] = as_f32(w.w);
-      } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_any*>(row + (e0 + v) * 2);
-        x[v] = elem_value<DT>(w.x & 0xFFFFu); x[v + 1] = elem_value<DT>(w.x >> 16);
-        x[v + 2] = elem_value<DT>(w.y & 0xFFFFu); x[v + 3] = elem_value<DT>(w.y >> 16);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : kNone;
-  }
+  load_logits<DT, V>(row, e0, mine, x);
   const bool by_logit = !a.bias && a.groups == 1;
   float top = kNone;
   double z = 1.0;
@@ -730,67 +737,94 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   }
 }
 
-// One wave per token; u: experts floats of the wave's own LDS, the gradient of each score.
-template <int DT>
+// G lanes a token (16 or 64), experts l * V .. l * V + V - 1 in its lane l, the
+// j-th chosen one in lane j.  Chosen experts' gradients are fp64 and meet the
+// rest of the row (zeros, or what a softmax takes off) in LDS, from where the
+// row goes out in whole vectors.  A softmax's exponentials are fp32, each off
+// by a few 2^-24.
+template <int DT, int G, int V, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __restrict__ logits, int64_t tokens, int E,
-                                                            int top_k, bool sigmoid, bool renormalize, double scale,
+                                                            int top_k, bool renormalize, double scale,
                                                             const int32_t* __restrict__ index,
                                                             const float* __restrict__ grad_weights,
                                                             uint8_t* __restrict__ grad_logits) {
-  extern __shared__ float rows_u[];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t token = (int64_t)blockIdx.x * kTokens + wave;
-  if (token >= tokens) return;
-  float* u = rows_u + wave * E;
-  const uint8_t* x = logits + token * E * kElemBytes<DT>;
-  uint8_t* out = grad_logits + token * E * kElemBytes<DT>;
+  __shared__ __attribute__((aligned(16))) float grad[kThreads / G][G * V];
+  const int slot = threadIdx.x / G, l = threadIdx.x % G;
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / G) + slot;
+  const bool on = token < tokens;
+  const int64_t at = on ? token * E : 0;
+  const uint8_t* row = logits + at * kElemBytes<DT>;
+  auto all = [](auto v, auto op) {
+    if constexpr (G == 16) return row_all(v, op);
+    else return wave_all(v, op);
+  };
+  auto add = [](double p, double q) { return p + q; };
+  const int e0 = l * V;
+
   int mine = -1;
-  double g = 0.0;
-  if (lane < top_k) {
-    mine = index[token * top_k + lane];
+  double g = 0.0, s = 0.0;
+  if (on && l < top_k) {
+    mine = index[token * top_k + l];
     if ((unsigned)mine >= (unsigned)E) mine = -1;
-    if (mine >= 0) g = (double)grad_weights[token * top_k + lane];
+    if (mine >= 0) g = (double)grad_weights[token * top_k + l];
   }
-  const bool any = __ballot(mine >= 0) != 0;
-  float top = -INFINITY;
+  const bool any = all(mine, [](int p, int q) { return max(p, q); }) >= 0;
+  float out[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) out[v] = 0.0f;
+  float top = 0.0f;
   double z = 1.0;
-  if (!sigmoid && any) {
-    for (int e = lane; e < E; e += 64) {
-      const float v = elem_value<DT>(load_bits<DT>(x + e * kElemBytes<DT>));
-      if (eligible(v)) top = fmaxf(top, v);
+  if constexpr (!SIGMOID) {
+    load_logits<DT, V>(row, e0, on && any ? min(V, max(0, E - e0)) : 0, out);
+    float most = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) most = fmaxf(most, out[v]);
+    top = all(most, [](float p, float q) { return fmaxf(p, q); });
+    if (!renormalize) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        out[v] = out[v] > -INFINITY ? exp_neg(top - out[v]) : 0.0f;
+        sum += out[v];
+      }
+      z = all((double)sum, add);
     }
-    top = wave_max(top);
-    double s = 0.0;
-    for (int e = lane; e < E; e += 64) {
-      const float v = elem_value<DT>(load_bits<DT>(x + e * kElemBytes<DT>));
-      if (eligible(v)) s += exp((double)v - (double)top);
-    }
-    z = wave_sum(s);
   }
-  double s = 0.0;
   if (mine >= 0) {
-    const double v = (double)elem_value<DT>(load_bits<DT>(x + mine * kElemBytes<DT>));
-    s = sigmoid ? sigmoid_f64(v) : exp(v - (double)top) / z;
+    const double x = (double)elem_value<DT>(load_bits<DT>(row + mine * kElemBytes<DT>));
+    s = SIGMOID ? sigmoid_f64(x) : exp(x - (double)top) / z;
   }
   double du = scale * g;
   if (renormalize) {
-    const double sum = wave_sum(s), mean = wave_sum(g * s);
+    const double sum = all(s, add), mean = all(g * s, add);
     du = sum > 0.0 ? scale * (g - mean / sum) / sum : 0.0;
   }
-  const double dot = sigmoid || !any ? 0.0 : wave_sum(mine >= 0 ? du * s : 0.0);
-  for (int e = lane; e < E; e += 64) {
-    float v = 0.0f;
-    if (!sigmoid && any) {
-      const float l = elem_value<DT>(load_bits<DT>(x + e * kElemBytes<DT>));
-      // what the sum of all gradients takes off; with renormalized weights it is 0 but for rounding
-      if (eligible(l) && !renormalize) v = (float)(-exp((double)l - (double)top) / z * dot);
+  // what a softmax takes off every expert; 0 but for rounding where the weights are renormalized
+  const double dot = SIGMOID || renormalize ? 0.0 : all(du * s, add);
+  const float off = SIGMOID || renormalize || !any ? 0.0f : (float)(dot / z);
+#pragma unroll
+  for (int v = 0; v < V; ++v) grad[slot][e0 + v] = SIGMOID || renormalize ? 0.0f : -out[v] * off;
+  wave_sync();
+  if (mine >= 0) grad[slot][mine] = (float)(SIGMOID ? du * s * (1.0 - s) : s * (du - dot));
+  wave_sync();
+  if (!on) return;
+  // the token's lanes write neighbouring columns together
+  uint8_t* to = grad_logits + at * kElemBytes<DT>;
+  if (E % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < V / 4; ++v) {
+      const int e = (v * G + l) * 4;
+      if (e >= E) break;
+      const float* p = &grad[slot][e];
+      if constexpr (DT == DT_F32)
+        store16<false>(to + e * 4, u32x4_t{as_u32(p[0]), as_u32(p[1]), as_u32(p[2]), as_u32(p[3])});
+      else
+        store_8<false>(to + e * 2, u32x2_t{elem_bits<DT>(p[0]) | (elem_bits<DT>(p[1]) << 16),
+                                           elem_bits<DT>(p[2]) | (elem_bits<DT>(p[3]) << 16)});
     }
-    u[e] = v;
+  } else {
+    for (int e = l; e < E; e += G) store_bits<DT>(to + e * kElemBytes<DT>, elem_bits<DT>(grad[slot][e]));
   }
-  wave_sync();
-  if (mine >= 0) u[mine] = (float)(sigmoid ? du * s * (1.0 - s) : renormalize ? du * s : s * (du - dot));
-  wave_sync();
-  for (int e = lane; e < E; e += 64) store_bits<DT>(out + e * kElemBytes<DT>, elem_bits<DT>(u[e]));
 }
 
 }  // namespace
@@ -839,17 +873,28 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
 hipError_t launch_moe_route_bwd(const void* logits, int dt, int64_t tokens, int experts, int top_k, bool sigmoid,
                                 bool renormalize, double scale, const int32_t* index, const float* grad_weights,
                                 void* grad_logits, hipStream_t st) {
-  const int64_t blocks = (tokens + kTokens - 1) / kTokens;
+  const bool rows = experts <= 256 && top_k <= 16;
+  const int lanes = rows ? 16 : 64, v = (experts + lanes - 1) / lanes;
+  const int64_t blocks = (tokens * lanes + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const size_t lds = (size_t)kTokens * experts * sizeof(float);
-#define CALL(DT)                                                                                                  \
-  k_moe_route_bwd<DT><<<(unsigned)blocks, kThreads, lds, st>>>((const uint8_t*)logits, tokens, experts, top_k,    \
-                                                               sigmoid, renormalize, scale, index, grad_weights, \
-                                                               (uint8_t*)grad_logits)
-  if (dt == DT_F32) CALL(DT_F32);
-  else if (dt == DT_BF16) CALL(DT_BF16);
-  else CALL(DT_F16);
+#define LAUNCH(DT, G, V, SIGMOID)                                                                             \
+  k_moe_route_bwd<DT, G, V, SIGMOID><<<(unsigned)blocks, kThreads, 0, st>>>(                                  \
+      (const uint8_t*)logits, tokens, experts, top_k, renormalize, scale, index, grad_weights, (uint8_t*)grad_logits)
+#define SIZES(DT, SIGMOID)                                  \
+  if (!rows && v <= 8) LAUNCH(DT, 64, 8, SIGMOID);          \
+  else if (!rows) LAUNCH(DT, 64, 16, SIGMOID);              \
+  else if (v <= 4) LAUNCH(DT, 16, 4, SIGMOID);              \
+  else if (v <= 8) LAUNCH(DT, 16, 8, SIGMOID);              \
+  else LAUNCH(DT, 16, 16, SIGMOID)
+#define CALL(DT)                           \
+  if (sigmoid) { SIZES(DT, true); }        \
+  else { SIZES(DT, false); }
+  if (dt == DT_F32) { CALL(DT_F32); }
+  else if (dt == DT_BF16) { CALL(DT_BF16); }
+  else { CALL(DT_F16); }
 #undef CALL
+#undef SIZES
+#undef LAUNCH
   return hipGetLastError();
 }
 

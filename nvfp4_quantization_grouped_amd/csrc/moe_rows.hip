@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const uint8_t* __rest
   if (p.token >= tokens || p.chunk >= chunks) return;
   const Columns c = columns_of<NARROW>(p.chunk, hidden);
   const int64_t rb = hidden * kElemBytes<DT>, n = tokens * top_k;
-  const Raw8<DT> v = load8<DT, true>(x + p.token * rb, c.first, c.live);
+  const Raw8<DT> v = load8<DT>(x + p.token * rb, c.first, c.live);
   for (int j = 0; j < top_k; ++j) {
     bool served;
     const int64_t r = row_of(rows[p.token * top_k + j], n, served);
@@ -233,14 +233,22 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch_quantized(const uint8
   u32x2_t c = {0u, 0u};
   if constexpr (FP4) c.x = encode_fp4(v, pow2f(k));
   else c = encode_fp8(v, pow2f(k));
+  const uint32_t bytes = scale_bytes(k, p.chunk);
+  const bool whole = (p.chunk | 15) < chunks;          // the same for 16 lanes
   const int64_t n = tokens * top_k;
   for (int j = 0; j < top_k; ++j) {
     bool served;
     const int64_t r = row_of(rows[p.token * top_k + j], n, served);
     if (r < 0) continue;
-    if constexpr (FP4) *reinterpret_cast<u32_any*>(codes + (r * chunks + p.chunk) * 4) = served ? c.x : 0u;
-    else *reinterpret_cast<u32x2_any*>(codes + (r * chunks + p.chunk) * 8) = served ? c : u32x2_t{0u, 0u};
-    if ((p.chunk & 3) == 0) scales[(r * chunks + p.chunk) >> 2] = (uint8_t)((served ? k : none) + 127);
+    const int64_t at = r * chunks + p.chunk;
+    if constexpr (FP4) store4<true>(codes + at * 4, served ? c.x : 0u);
+    else store_8<true>(codes + at * 8, served ? c : u32x2_t{0u, 0u});
+    const uint32_t sb = served ? bytes : (uint32_t)(none + 127) * 0x01010101u;
+    if (whole) {
+      if ((p.chunk & 15) == 0) store4<false>(scales + (at >> 2), sb);
+    } else if ((p.chunk & 3) == 0) {
+      scales[at >> 2] = (uint8_t)(sb >> (8 * ((p.chunk >> 2) & 3)));
+    }
   }
 }
 

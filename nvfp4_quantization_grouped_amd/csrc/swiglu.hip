@@ -25,14 +25,28 @@ __device__ __forceinline__ int64_t rows_that_count(const int32_t* total, int64_t
   return total ? min(rows, max((int64_t)0, (int64_t)*total)) : rows;
 }
 
+// Chunk i of this workgroup's run that starts at chunk `base` of rows x chunks:
+// its row and its place in the row, by one division of 32 bits a lane.
+struct Spot {
+  int64_t row;
+  int chunk;
+};
+__device__ __forceinline__ Spot spot_of(int64_t row0, unsigned first, unsigned i, unsigned chunks) {
+  const unsigned at = first + i, d = at / chunks;
+  return {row0 + d, (int)(at - d * chunks)};
+}
+
 template <int DT, bool KEEP>
 __global__ void __launch_bounds__(kThreads) k_swiglu_fwd(const uint8_t* __restrict__ gate_up, int64_t rows, int chunks,
                                                          const int32_t* __restrict__ total, uint8_t* __restrict__ h,
                                                          uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int64_t count = rows_that_count(total, rows), n = rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / chunks;
-    const int c = (int)(i - row * chunks);
+  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < n; base += (int64_t)gridDim.x * kThreads) {
+    const int64_t row0 = base / chunks, i = base + threadIdx.x;
+    if (i >= n) break;
+    const Spot spot = spot_of(row0, (unsigned)(base - row0 * chunks), threadIdx.x, chunks);
+    const int64_t row = spot.row;
+    const int c = spot.chunk;
     if (row >= count) {
       store8<DT, true>(h, i * 8, 8, zero8<DT>());
       continue;
@@ -47,9 +61,15 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_fwd(const uint8_t* __restri
     if constexpr (KEEP) {
       const int kg = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(g)));
       const int ku = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(u)));
-      *reinterpret_cast<u32x2_any*>(codes + at * 8) = encode_fp8(g, pow2f(kg));
-      *reinterpret_cast<u32x2_any*>(codes + (at + chunks) * 8) = encode_fp8(u, pow2f(ku));
-      if ((c & 3) == 0) {
+      store_8<true>(codes + at * 8, encode_fp8(g, pow2f(kg)));
+      store_8<true>(codes + (at + chunks) * 8, encode_fp8(u, pow2f(ku)));
+      if ((chunks & 15) == 0) {        // 16 lanes hold four blocks: one store of four bytes
+        const uint32_t bg = scale_bytes(kg, c), bu = scale_bytes(ku, c);
+        if ((c & 15) == 0) {
+          store4<false>(scales + (at >> 2), bg);
+          store4<false>(scales + ((at + chunks) >> 2), bu);
+        }
+      } else if ((c & 3) == 0) {
         scales[at >> 2] = (uint8_t)(kg + 127);
         scales[(at + chunks) >> 2] = (uint8_t)(ku + 127);
       }
@@ -65,9 +85,12 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const uint8_t* __restri
                                                          const int32_t* __restrict__ total,
                                                          uint8_t* __restrict__ grad) {
   const int64_t count = rows_that_count(total, rows), n = rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / chunks;
-    const int c = (int)(i - row * chunks);
+  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < n; base += (int64_t)gridDim.x * kThreads) {
+    const int64_t row0 = base / chunks, i = base + threadIdx.x;
+    if (i >= n) break;
+    const Spot spot = spot_of(row0, (unsigned)(base - row0 * chunks), threadIdx.x, chunks);
+    const int64_t row = spot.row;
+    const int c = spot.chunk;
     const int64_t at = row * 2 * chunks + c;
     if (row >= count) {
       store8<DT, true>(grad, at * 8, 8, zero8<DT>());
