@@ -46,15 +46,22 @@ class MoEPlan(NamedTuple):
     slots: torch.Tensor
 
 
+_entries = {}
+
+
 def _call(name, device, *args):
     """Run entry point ``name`` on ``device``'s current stream (appended as the last argument).
 
-    A decoding step makes these calls one after another, so the host's part of
-    each counts: the raw stream handle costs 0.1 us against 1.9 us for a Stream
-    object, and the device is only switched where it has to be (1.3 us)."""
-    fn = getattr(_lib.moe_lib(), name)
+    A decoding step makes these calls one after another, and a backward makes
+    them on a thread that has just woken, so the host's part of each counts: the
+    raw stream handle costs 0.1 us against 1.9 us for a Stream object (8 us on
+    autograd's thread), and the device is only switched where it has to be
+    (1.3 us)."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(_lib.moe_lib(), name)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -102,11 +109,14 @@ class _MoERoute(torch.autograd.Function):
         ctx.save_for_backward(logits, experts)
         ctx.how = score, renormalize, scale
         ctx.mark_non_differentiable(experts)
+        ctx.set_materialize_grads(False)      # no zeros for the experts' missing gradient
         return weights, experts
 
     @staticmethod
     @_first_order
     def backward(ctx, grad_weights, _):
+        if grad_weights is None:
+            return (None,) * 10
         logits, experts = ctx.saved_tensors
         score, renormalize, scale = ctx.how
         g = grad_weights.contiguous()
