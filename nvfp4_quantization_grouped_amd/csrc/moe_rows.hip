@@ -14,7 +14,11 @@
 // columns of one token, so the token's rows and weights are scalars, and visits
 // its top_k rows: a token's row is read once (dispatch) or written once
 // (combine) whatever top_k is, and the combine has the loads of 8 rows in
-// flight.
+// flight.  Rows of the grouped order are read and written past the caches (they
+// are top_k times what fits): bf16 [8192, 7168] x top-8, 1.06 GB, dispatch 197
+// -> 176 us (6.0 TB/s; with the tokens' loads past the caches too, 208), combine
+// 203 -> 182 us and 173 with smaller workgroups (6.1 TB/s), the combine's
+// gradient, 2.0 GB, 391 -> 360 us (5.6 TB/s).
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -23,6 +27,11 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256;
+// The combine reads top_k bytes for one that it writes; with half as large
+// workgroups its read streams ran 5% faster (bf16 [8192, 7168] x top-8: 182 ->
+// 173 us; 64 threads 175), where the dispatch measured the same and the
+// quantized dispatch 1-5% slower.
+constexpr int kCombineThreads = 128;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int64_t kPlanRecount = 16384;
@@ -169,8 +178,9 @@ struct Place {
   int64_t token;
   int chunk;
 };
+template <int THREADS>
 __device__ __forceinline__ Place place_of(unsigned segs) {
-  const unsigned w = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned w = blockIdx.x * (THREADS / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned token = w / segs;
   return {token, (int)((w - token * segs) * 64 + (threadIdx.x & 63))};
 }
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const uint8_t* __rest
                                                            int chunks, unsigned segs, int top_k,
                                                            const int32_t* __restrict__ rows,
                                                            uint8_t* __restrict__ out) {
-  const Place p = place_of(segs);
+  const Place p = place_of<kThreads>(segs);
   if (p.token >= tokens || p.chunk >= chunks) return;
   const Columns c = columns_of<NARROW>(p.chunk, hidden);
   const int64_t rb = hidden * kElemBytes<DT>, n = tokens * top_k;
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch_quantized(const uint8
                                                                      int top_k, const int32_t* __restrict__ rows,
                                                                      uint8_t* __restrict__ codes,
                                                                      uint8_t* __restrict__ scales) {
-  const Place p = place_of(segs);
+  const Place p = place_of<kThreads>(segs);
   if (p.token >= tokens || p.chunk >= chunks) return;   // whole groups of four lanes: chunks is a multiple of 4
   float v[8];
   to_f32<DT>(load8<DT>(x + p.token * hidden * kElemBytes<DT>, (int64_t)p.chunk * 8, 8), v);
@@ -255,12 +265,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch_quantized(const uint8
 // WEIGHTED false: weights of 1.  A slot that is not served reads row 0, which
 // the caches hold, and adds nothing of it.
 template <int DT, bool WEIGHTED, bool NARROW>
-__global__ void __launch_bounds__(kThreads) k_moe_combine(const uint8_t* __restrict__ y, int64_t tokens, int64_t hidden,
+__global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const uint8_t* __restrict__ y, int64_t tokens, int64_t hidden,
                                                           int chunks, unsigned segs, int top_k,
                                                           const int32_t* __restrict__ rows,
                                                           const float* __restrict__ weights,
                                                           uint8_t* __restrict__ out) {
-  const Place p = place_of(segs);
+  const Place p = place_of<kCombineThreads>(segs);
   if (p.token >= tokens || p.chunk >= chunks) return;
   const Columns c = columns_of<NARROW>(p.chunk, hidden);
   const int64_t rb = hidden * kElemBytes<DT>, n = tokens * top_k;
@@ -370,9 +380,9 @@ __global__ void __launch_bounds__(kBwdWaves * 64) k_moe_combine_bwd(const uint8_
 
 // Waves a token of the row streams, and their workgroups (0: more than a launch takes).
 unsigned segs_of(int chunks) { return (unsigned)(chunks + 63) / 64; }
-unsigned stream_blocks(int64_t tokens, int chunks) {
-  const int64_t waves = tokens * segs_of(chunks);
-  return waves > 0x7FFFFFF0 ? 0u : (unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64));
+unsigned stream_blocks(int64_t tokens, int chunks, int threads) {
+  const int64_t waves = tokens * segs_of(chunks), per = threads / 64;
+  return waves > 0x7FFFFFF0 ? 0u : (unsigned)((waves + per - 1) / per);
 }
 
 }  // namespace
@@ -410,7 +420,7 @@ hipError_t launch_moe_plan(const int32_t* index, int64_t slots, int first, int l
 hipError_t launch_moe_dispatch(const void* x, int dt, int64_t tokens, int64_t hidden, int top_k, const int32_t* rows,
                                void* out, hipStream_t st) {
   const int chunks = (int)((hidden + 7) / 8);
-  const unsigned blocks = stream_blocks(tokens, chunks), segs = segs_of(chunks);
+  const unsigned blocks = stream_blocks(tokens, chunks, kThreads), segs = segs_of(chunks);
   if (blocks == 0) return hipErrorInvalidValue;
 #define LAUNCH(DT, NARROW)                                                                                          \
   k_moe_dispatch<DT, NARROW><<<blocks, kThreads, 0, st>>>((const uint8_t*)x, tokens, hidden, chunks, segs, top_k, \
@@ -428,7 +438,7 @@ hipError_t launch_moe_dispatch_quantized(const void* x, int dt, int64_t tokens, 
                                          const int32_t* rows, int fmt, uint8_t* codes, uint8_t* scales,
                                          hipStream_t st) {
   const int chunks = (int)(hidden / 8);
-  const unsigned blocks = stream_blocks(tokens, chunks), segs = segs_of(chunks);
+  const unsigned blocks = stream_blocks(tokens, chunks, kThreads), segs = segs_of(chunks);
   if (blocks == 0) return hipErrorInvalidValue;
 #define CALL(DT)                                                                                                    \
   if (fmt == FMT_MXFP4)                                                                                             \
@@ -445,10 +455,10 @@ hipError_t launch_moe_dispatch_quantized(const void* x, int dt, int64_t tokens, 
 hipError_t launch_moe_combine(const void* y, int dt, int64_t tokens, int64_t hidden, int top_k, const int32_t* rows,
                               const float* weights, void* out, hipStream_t st) {
   const int chunks = (int)((hidden + 7) / 8);
-  const unsigned blocks = stream_blocks(tokens, chunks), segs = segs_of(chunks);
+  const unsigned blocks = stream_blocks(tokens, chunks, kCombineThreads), segs = segs_of(chunks);
   if (blocks == 0) return hipErrorInvalidValue;
 #define LAUNCH(DT, WEIGHTED, NARROW)                                                                              \
-  k_moe_combine<DT, WEIGHTED, NARROW><<<blocks, kThreads, 0, st>>>((const uint8_t*)y, tokens, hidden, chunks,    \
+  k_moe_combine<DT, WEIGHTED, NARROW><<<blocks, kCombineThreads, 0, st>>>((const uint8_t*)y, tokens, hidden, chunks,    \
                                                                    segs, top_k, rows, weights, (uint8_t*)out)
 #define CALL(DT)                                        \
   if (hidden < 8) {                                     \
