@@ -54,7 +54,8 @@ typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score;
  * Ties go to the lower group or expert.  Keys are compared as in fp64: where
  * fp32 keys lie too near each other to tell, the token is decided in fp64.
  * An expert whose logit or bias is -inf or NaN is never chosen (nor counted
- * in a softmax or a group's value).  A token with token_mask[t] == 0
+ * in a softmax or a group's value); softmax logits must be below +inf.  A token
+ * with token_mask[t] == 0
  * (uint8 [tokens], NULL = none) chooses none, whatever its logits hold.
  * A place without an expert has index -1 and weight 0.
  * Outputs: weights fp32 and index int32, both [tokens, top_k].
@@ -165,6 +166,7 @@ int moe_combine_bwd(const void* grad_out, const void* y, int t, int64_t tokens, 
  * 8 bits: E4M3 codes uint8 [rows, 2 * inter] and one E8M0 scale byte per 32
  * columns, uint8 [rows, 2 * inter / 32], as quantize_cache_packed writes them
  * for fp8 and block_size 32.  Rows that do not count are left as they were.
+ * What is kept must be finite, as wherever an operation takes an amax.
  * swiglu_bwd -- grad_gate_up [rows, 2 * inter] of grad_h [rows, inter]:
  *   grad_gate = grad_h * up * s (1 + gate (1 - s)), grad_up = grad_h * gate *
  *   s, s = sigmoid(gate), fp32, with gate and up read from codes and scales

@@ -138,6 +138,41 @@ def test_layer_in_a_graph():
             assert torch.equal(a, c) and torch.equal(b, c)
 
 
+def test_rows_in_a_graph():
+    """The two-launch order of many slots, the streams and their gradients captured; replays between eager passes over
+    other assignments, every replay against the eager result."""
+    g = np.random.default_rng(8)
+    T, k, n, F = 5000, 5, 40, 192
+    e = torch.from_numpy(g.integers(-1, n, (T, k)).astype(np.int32)).to(dev())
+    x, w, go = values(g, (T, F), "bf16"), values(g, (T, k), "f32"), values(g, (T, F // 2), "bf16")
+
+    def step(e, x, w):
+        x, w = x.detach().requires_grad_(True), w.detach().requires_grad_(True)
+        plan = mxq.moe_plan(e, n)
+        codes, scales = mxq.moe_dispatch_quantized(x, plan, "fp8")
+        out = mxq.moe_combine(mxq.swiglu(mxq.moe_dispatch(x, plan), plan.offs), w, plan)
+        return (*plan, codes, scales, out, *torch.autograd.grad(out, (x, w), go))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(e, x, w)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step(e, x, w)
+    for seed in range(4):
+        r = np.random.default_rng(200 + seed)
+        e.copy_(torch.from_numpy(r.integers(-1, n, (T, k)).astype(np.int32)))
+        x.copy_(values(r, (T, F), "bf16"))
+        w.copy_(values(r, (T, k), "f32"))
+        graph.replay()
+        want = step(e, x, w)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_layer_on_two_streams_at_once():
     """Two plans and their rows at the same time, each on its own stream with its own workspace."""
     g = np.random.default_rng(5)

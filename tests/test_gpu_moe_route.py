@@ -90,7 +90,8 @@ def test_route_near_ties_are_decided_in_fp64():
 
 
 GROUPS = [(64, 4, 2, 8, 2), (256, 8, 4, 8, 2), (160, 8, 3, 6, 1), (256, 8, 1, 8, 2), (60, 12, 5, 4, 2), (64, 64, 8, 8, 2),
-          (1024, 64, 4, 8, 2), (21, 3, 2, 5, 2), (256, 4, 4, 8, 2), (12, 6, 1, 4, 2), (512, 16, 3, 8, 1)]
+          (1024, 64, 4, 8, 2), (21, 3, 2, 5, 2), (256, 4, 4, 8, 2), (12, 6, 1, 4, 2), (512, 16, 3, 8, 1),
+          (130, 13, 4, 8, 2), (1000, 8, 3, 8, 2), (130, 13, 2, 32, 1)]
 
 
 @pytest.mark.parametrize("E,groups,top_groups,k,best", GROUPS)
@@ -143,7 +144,7 @@ def many(g, T, E, dtype="f32", distinct=40):
 MANY = [(4096, 256, 8, dict(groups=8, top_groups=4)), (5001, 256, 8, dict()), (2050, 60, 4, dict()), (3000, 64, 16, dict()),
         (2048, 128, 1, dict(groups=4, top_groups=1)), (2049, 17, 3, dict()), (2500, 96, 6, dict(groups=12, top_groups=5)),
         (2500, 240, 8, dict(groups=5, top_groups=2)), (2300, 256, 16, dict(groups=2, top_groups=1, group_best=1)),
-        (2100, 384, 8, dict(groups=8, top_groups=3)), (2100, 200, 17, dict())]
+        (2100, 384, 8, dict(groups=8, top_groups=3)), (2100, 200, 17, dict()), (2100, 130, 8, dict(groups=13, top_groups=4))]
 
 
 @pytest.mark.parametrize("T,E,k,kw", MANY)
@@ -195,6 +196,52 @@ def test_route_gradient_with_out_of_range_index():
     assert st == 0
     want = moe.route_grad(f64(x), idx, gw.astype(np.float64), "sigmoid", True, 1.0)
     assert_rounded(out, want, "f32", 8 * U * np.abs(gw).max() * 8, "grad")
+
+
+def test_route_near_ties_among_many_tokens():
+    """The near ties above where four tokens share a wave, in every third token, the others far from ties."""
+    g = np.random.default_rng(21)
+    distinct = 12
+    x = (1.5 * g.standard_normal((distinct, 256))).astype(np.float32)
+    for r in range(0, distinct, 3):                      # within two ulps of each other
+        x[r] = (np.full(256, 2.0, np.float32).view(np.int32) + g.integers(0, 3, 256).astype(np.int32)).view(np.float32)
+    x[1] = g.standard_normal(256)
+    bias = (1.5 - moe.sigmoid(x[1].astype(np.float64))).astype(np.float32)
+    order = g.integers(0, distinct, 2304)
+    at = torch.from_numpy(x[order]).to(dev())
+    for b in (bias, np.full(256, 0.5, np.float32)):
+        for kw in (dict(), dict(groups=8, top_groups=4), dict(groups=8, top_groups=4, group_best=1)):
+            for score in ("sigmoid", "softmax"):
+                w, e = mxq.moe_route(at, 8, score=score, bias=torch.from_numpy(b).to(dev()), **kw)
+                want_w, want_e = moe.route(x.astype(np.float64), 8, score, bias=b.astype(np.float64), **kw)
+                assert np.array_equal(e.cpu().numpy(), want_e[order])
+                assert_rounded(w, want_w[order], "f32", 4 * U * want_w[order], "weights")
+
+
+@pytest.mark.parametrize("T", [3, 2050])
+def test_route_infinite_logits(T):
+    """A logit of +inf is a sigmoid score of 1 and comes before every finite logit."""
+    g = np.random.default_rng(22)
+    x = g.standard_normal((5, 64)).astype(np.float32)
+    x[0, 7], x[1, [3, 60]] = np.inf, np.inf
+    x[2] = np.inf
+    order = np.arange(T) % 5
+    at = torch.from_numpy(x[order]).to(dev())
+    for kw in (dict(), dict(bias=(0.1 * g.standard_normal(64)).astype(np.float32))):
+        want_w, want_e = moe.route(x.astype(np.float64), 6, "sigmoid", **kw)
+        w, e = mxq.moe_route(at, 6, score="sigmoid", **{k: torch.from_numpy(v).to(dev()) for k, v in kw.items()})
+        assert np.array_equal(e.cpu().numpy(), want_e[order])
+        assert_rounded(w, want_w[order], "f32", 4 * U * want_w[order], "weights")
+
+
+def test_route_second_derivatives_are_refused():
+    x = torch.randn(4, 16, device=dev(), requires_grad=True)
+    w, _ = mxq.moe_route(x, 4)
+    g, = torch.autograd.grad(w.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+    w, e = mxq.moe_route(x, 4)
+    assert torch.autograd.grad(w.sum() * 0 + x.sum(), x)[0].shape == x.shape
 
 
 def test_route_refusals():
