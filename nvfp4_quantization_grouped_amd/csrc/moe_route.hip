@@ -301,6 +301,20 @@ __device__ __forceinline__ void load_logits(const uint8_t* row, int e0, int mine
   }
 }
 
+// A point between lo and hi to count at: their mean, or in every other step the
+// middle of the floats between them, which comes near whatever lies far below
+// hi (logits masked with the lowest value of their type) in a few steps and
+// ends the halving after 64 of them.
+__device__ __forceinline__ float halfway(float lo, float hi, int step) {
+  if ((step & 1) == 0) return 0.5f * lo + 0.5f * hi;
+  auto order = [](float f) {
+    const uint32_t b = as_u32(f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+  };
+  const uint32_t a = order(lo), m = a + (order(hi) - a) / 2;
+  return as_f32(m & 0x80000000u ? m & 0x7FFFFFFFu : ~m);
+}
+
 struct Candidate {
   int expert;
   float logit;
@@ -399,8 +413,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
     lo = wave_all(lo, [](float p, float q) { return fminf(p, q); });
     hi = wave_all(hi, [](float p, float q) { return fmaxf(p, q); });
     cut = lo;
-    for (int i = 0; i < 40; ++i) {
-      const float mid = 0.5f * lo + 0.5f * hi;
+    for (int i = 0; i < 64; ++i) {
+      const float mid = halfway(lo, hi, i);
       const int n = count(mid);
       if (n >= a.top_k) {
         cut = lo = mid;
@@ -634,7 +648,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     const bool enough = n >= k;
     if (enough) cut = lo;
     for (int i = 0; i < 24 && __any(enough && n > k + 1); ++i) {
-      const float mid = 0.5f * lo + 0.5f * hi;
+      const float mid = halfway(lo, hi, i);
       const int m = row_count(__ballot(two.best >= mid)) + row_count(__ballot(two.next >= mid));
       if (m >= k) { lo = mid; n = m; if (enough) cut = mid; }
       else hi = mid;
@@ -663,8 +677,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     lo = row_all(lo, [](float p, float q) { return fminf(p, q); });
     hi = row_all(hi, [](float p, float q) { return fmaxf(p, q); });
     lo = fmaxf(lo, cut);
-    for (int i = 0; i < 40 && __any(n > 16); ++i) {
-      const float mid = 0.5f * lo + 0.5f * hi;
+    for (int i = 0; i < 64 && __any(n > 16); ++i) {
+      const float mid = halfway(lo, hi, i);
       if (row_total(in_reach(mid)) >= k) {
         lo = mid;
         if (n > 16) {

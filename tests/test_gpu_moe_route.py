@@ -117,6 +117,8 @@ def test_route_masked_and_empty(score):
     x[2, 5:] = float("-inf")
     x[:, 7] = float("-inf")
     x[3, 9] = float("nan")
+    x[4, ::2] = torch.finfo(torch.float32).min
+    x[5, 2:] = torch.finfo(torch.float32).min
     bias = (0.1 * g.standard_normal(64)).astype(np.float32)
     bias[20:30] = -np.inf
     for kw in (dict(), dict(bias=bias), dict(bias=bias, groups=8, top_groups=2), dict(groups=8, top_groups=8)):
@@ -161,6 +163,9 @@ def test_route_many_tokens(T, E, k, kw, score, dtype):
     x[6] = float("-inf")
     x[7, 5] = float("nan")
     x[8] = torch.round(x[8])
+    x[9, ::2] = torch.finfo(x.dtype).min                 # masked with the type's lowest value: still finite logits
+    x[10, : E - min(k, E) + 1] = torch.finfo(x.dtype).min
+    x[11, 1:] = -1e9
     for bias in (None, (0.1 * g.standard_normal(E)).astype(np.float32), np.zeros(E, np.float32)):
         args = dict(score=score, renormalize=bias is not None, **kw)
         want_w, want_e = moe.route(f64(x), k, bias=None if bias is None else bias.astype(np.float64), **args)
