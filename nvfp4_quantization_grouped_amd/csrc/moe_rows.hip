@@ -14,11 +14,13 @@
 // columns of one token, so the token's rows and weights are scalars, and visits
 // its top_k rows: a token's row is read once (dispatch) or written once
 // (combine) whatever top_k is, and the combine has the loads of 8 rows in
-// flight.  Rows of the grouped order are read and written past the caches (they
-// are top_k times what fits): bf16 [8192, 7168] x top-8, 1.06 GB, dispatch 197
-// -> 176 us (6.0 TB/s; with the tokens' loads past the caches too, 208), combine
-// 203 -> 182 us and 173 with smaller workgroups (6.1 TB/s), the combine's
-// gradient, 2.0 GB, 391 -> 360 us (5.6 TB/s).
+// flight.  Rows of the grouped order are read past the caches, and the
+// combine's outputs and gradients written past them (they are top_k times what
+// fits): bf16 [8192, 7168] x top-8, 1.06 GB, combine 203 -> 182 us and 173 with
+// smaller workgroups (6.1 TB/s), its gradient, 2.0 GB, 391 -> 360 us (5.6
+// TB/s).  The dispatch writes through the caches: its last rows are there for
+// whoever reads them next.  Repeated alone it runs 197 us that way and 176 past
+// the caches, but followed by its gradient the two take 371 us against 379.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const uint8_t* __rest
   for (int j = 0; j < top_k; ++j) {
     bool served;
     const int64_t r = row_of(rows[p.token * top_k + j], n, served);
-    if (r >= 0) store8<DT, true>(out + r * rb, c.first, c.live, served ? v : zero8<DT>());
+    if (r >= 0) store8<DT>(out + r * rb, c.first, c.live, served ? v : zero8<DT>());
   }
 }
 
