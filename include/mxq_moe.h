@@ -53,8 +53,9 @@ typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score;
  *     renormalize (0 where that sum is 0).
  * Ties go to the lower group or expert.  Keys are compared as in fp64: where
  * fp32 keys lie too near each other to tell, the token is decided in fp64.
- * An expert whose logit or bias is -inf or NaN is never chosen (nor counted
- * in a softmax or a group's value); softmax logits must be below +inf.  A token
+ * An expert whose logit or bias is -inf or NaN is never chosen nor counted in a
+ * group's value; one whose logit is -inf or NaN is not counted in a softmax
+ * either.  Softmax logits must be below +inf.  A token
  * with token_mask[t] == 0
  * (uint8 [tokens], NULL = none) chooses none, whatever its logits hold.
  * A place without an expert has index -1 and weight 0.

@@ -1,15 +1,22 @@
 // The router: scores, balance bias, expert groups, top-k and weights
 // (moe_route), and the weights' gradient with respect to the logits.
 //
-// One wave per token.  Which expert comes next may hang on keys that fp32 does
-// not tell apart, so the choice is made on fp64 keys, ties to the lower index
-// -- but an fp64 exponential for every expert costs more than all the rest, so
-// k_moe_route computes fp32 keys, whose error is bounded (kKeyError), takes as
-// candidates every expert that the bound leaves in the running for the top_k
-// (a few more than top_k), and gives each candidate a lane, an fp64 key and a
-// rank: the number of candidates before it.  k_moe_route_general works with
-// fp64 keys in LDS throughout; it serves the group sizes that do not fit the
-// lanes of the other.
+// Which expert comes next may hang on keys that fp32 does not tell apart, so the
+// choice is made on fp64 keys, ties to the lower index -- but an fp64
+// exponential for every expert costs more than all the rest.  So the kernels
+// compute fp32 keys, whose error is bounded (key_error), take as candidates
+// every expert that the bound leaves in the running for the top_k (a few more
+// than top_k), and give each candidate a lane, an fp64 key and a rank: the
+// number of candidates before it.  Three kernels, chosen by what fits:
+//   k_moe_route_rows     16 lanes a token: up to 512 experts, 16 places, groups
+//                        of whole lanes (of 4, 8, 16 or 32 experts);
+//   k_moe_route          a wave a token: up to 1024 experts, 32 places, groups of
+//                        whole lanes (of 1, 2, 4, 8 or 16 experts);
+//   k_moe_route_general  a wave a token with fp64 keys in LDS throughout: any
+//                        group size.
+// 16384 tokens x 256 experts, 8 of 256 in 4 of 8 groups, sigmoid and bias, fp32:
+// 11.6, 23.6 and 55.3 us.  All are bound by instructions, not by the 16.8 MB of
+// logits (3.4 us): 828 vector instructions for four tokens in the first.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -19,8 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = kThreads / 64;   // per workgroup
-// From this many tokens on four share a wave.
-constexpr int64_t kRowTokens = 2048;
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -146,15 +151,17 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_general(RouteArgs a) {
 
 // ------------------------------------------------- fp32 keys, fp64 candidates
 // fp32 score: of an exponential at full rate, as its error is bounded, not
-// small.  In units of u = 2^-24 (half an ulp of 1), with scores of at most 1:
-// sigmoid 1 / (1 + e), e = 2^(-x log2 e): e is off by |x| u (two roundings of
-// the exponent) and 2 u, which moves the score by s (1 - s) times that, at
-// most u; the sum adds u and the reciprocal 2 u.  softmax p = e / z, e = 2^((x
-// - top) log2 e): p |x - top| 3 u <= 2 u, the exponential 2 u, z in fp64, its
-// reciprocal and the product 3 u.  A bias adds half an ulp of the key.
+// small.  In units of u = 2^-24 (half an ulp of 1) times the largest score there
+// can be (sigmoid 1, softmax 1 / z):
+// sigmoid 1 / (1 + e), e = 2^(-x log2 e): e is off by 1.4 |x| u (the product and
+// the constant) and 2 u, which moves the score by s (1 - s) times that, at most
+// u; the sum adds u and the reciprocal 2 u.  softmax p = e / z, e = 2^((x - top)
+// log2 e): p |x - top| 2.4 u <= u and 2 u, or 4 u by exp_neg; z in fp64 or a sum
+// of such exponentials, 4 u; its reciprocal and the product 2 u.  A bias adds
+// half an ulp of the key.
 constexpr float kUlp = 0x1p-24f;
 constexpr float kLog2e = 0x1.715476p+0f;
-__device__ __forceinline__ float key_error(float key) { return kUlp * (16.0f + 2.0f * fabsf(key)); }
+__device__ __forceinline__ float key_error(float key, float most) { return kUlp * (16.0f * most + 2.0f * fabsf(key)); }
 __device__ __forceinline__ float sigmoid_key(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
 }
@@ -231,9 +238,10 @@ union GroupPairs {
 // Value of the group that this lane's experts belong to, the same in every
 // lane of the group: its `best` (1 or 2) largest keys summed.  t: the two
 // largest of this lane's keys; lanes: lanes of a group; lds: the wave's own;
-// the token's lanes are those from `base` to `end`.
+// the token's lanes are those from `base` to `end`; most: the largest score there can be.
 template <typename T>
-__device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int best, T* lds, int base, int end) {
+__device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int best, T* lds, int base, int end,
+                                                     float most) {
   const int lane = threadIdx.x & 63;
   if ((lanes & (lanes - 1)) == 0) {
     auto meet = [&](T b, T n) { t.add(b); t.add(n); };
@@ -257,8 +265,8 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
   }
   if (!(t.best > -INFINITY)) return {t.best, 0.0f};
   if (best == 2 && t.next > -INFINITY)
-    return {t.best + t.next, kUlp * (32.0f + 4.0f * (fabsf((float)t.best) + fabsf((float)t.next)))};
-  return {t.best, kUlp * (32.0f + 4.0f * fabsf((float)t.best))};
+    return {t.best + t.next, kUlp * (32.0f * most + 4.0f * (fabsf((float)t.best) + fabsf((float)t.next)))};
+  return {t.best, kUlp * (32.0f * most + 4.0f * fabsf((float)t.best))};
 }
 
 // Whether this lane's group is among the `top` groups of largest value; near:
@@ -378,7 +386,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) t.add(key[v]);
     bool near;
-    kept = group_kept(group_value<float>(t, lanes, a.group_best, pairs[wave].f, 0, 64), a.groups, lanes, a.top_groups, near);
+    kept = group_kept(group_value<float>(t, lanes, a.group_best, pairs[wave].f, 0, 64, rz), a.groups, lanes,
+                      a.top_groups, near);
     if (near) {
       Two<double> t64;
 #pragma unroll 1
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
         float l;
         t64.add(key64(v, l));
       }
-      kept = group_kept(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, 0, 64), a.groups, lanes,
+      kept = group_kept(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, 0, 64, rz), a.groups, lanes,
                         a.top_groups, near);
     }
 #pragma unroll
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
         hi = mid;
       }
     }
-    if (!by_logit) cut -= 2.0f * key_error(cut);
+    if (!by_logit) cut -= 2.0f * key_error(cut, rz);
   }
   const int n = count(cut);
 
@@ -492,11 +501,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 }
 
 // ------------------------------------------------------ four tokens a wave
-// The same for up to 256 experts and 16 places with 16 lanes a token: one
+// The same for up to 512 experts and 16 places with 16 lanes a token: one
 // instruction serves four tokens in what is done once a token (the fp64 scores
-// of the candidates, their ranks, the groups), which is most of the work.  The
-// wave-wide kernel above keeps fewer steps one after another, which counts
-// where there are few tokens.
+// of the candidates, their ranks, the groups), which is most of the work.
+// Grouped sigmoid router with a bias, 256 experts, here and wave-wide: 4 tokens
+// 4.6 and 5.1 us, 1024 tokens 5.2 and 5.7, 16384 tokens 11.6 and 23.6, 65536
+// tokens 28 and 81; 512 experts, 16384 tokens 19 and 32.
 
 // Number of set lanes of `m` in this lane's row of 16.
 __device__ __forceinline__ int row_count(uint64_t m) {
@@ -533,6 +543,13 @@ __device__ __forceinline__ int row_rank(double key) {
   }
 }
 
+// Whether another lane's key is within `error` of this one's, which is finite.
+template <int N>
+__device__ __forceinline__ bool row_close(float key, float error) {
+  if constexpr (N == 0) return false;
+  else return (int)(fabsf(dpp_value<0x120 + N>(key) - key) <= error) | (int)row_close<N - 1>(key, error);
+}
+
 // Experts l * V .. l * V + V - 1 in lane l of a token's row; experts <= 16 V,
 // top_k <= 16, a group (if there are groups) is whole lanes.
 template <int DT, int V, bool SIGMOID>
@@ -549,31 +566,52 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   float x[V], key[V];
   load_logits<DT, V>(row, e0, mine, x);
   const bool by_logit = !a.bias && a.groups == 1;
-  float top = kNone;
+  // Softmax: the sum of fp32 exponentials, each off by 4 u, is enough for the
+  // weights and for keys that are clear of each other; where they are not,
+  // exact_z() takes its place for that token.
+  float top = kNone, rz = 1.0f;
   double z = 1.0;
-  if (!SIGMOID) {
+  if (by_logit) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = x[v];           // where x is NaN the key is too, and no comparison takes it
+  }
+  if (SIGMOID) {
+    if (!by_logit) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = x[v] == kNone ? kNone : sigmoid_key(x[v]);
+    }
+  } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
     top = row_all(top, [](float p, float q) { return fmaxf(p, q); });
     if (!by_logit || !a.renormalize) {
-      double s = 0.0;
+      float e[V];
+      double sum = 0.0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) s += x[v] > kNone ? exp((double)x[v] - (double)top) : 0.0;
-      z = row_all(s, [](double p, double q) { return p + q; });
+      for (int v = 0; v < V; ++v) {
+        e[v] = x[v] > kNone ? exp_neg(top - x[v]) : 0.0f;
+        sum += (double)e[v];
+      }
+      z = row_all(sum, [](double p, double q) { return p + q; });
+      rz = (float)(1.0 / z);
+      if (!by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = x[v] > kNone ? e[v] * rz : kNone;
+      }
     }
   }
-  auto score64 = [&](float v) { return SIGMOID ? sigmoid_f64((double)v) : exp((double)v - (double)top) / z; };
-  // fp32 keys; where x is NaN the key is too, and no comparison takes it
-  if (by_logit) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = x[v];
-  } else {
-    const float rz = SIGMOID ? 1.0f : (float)(1.0 / z);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float s = SIGMOID ? sigmoid_key(x[v]) : softmax_key(x[v], top, rz);
-      key[v] = x[v] == kNone ? kNone : s;
+  auto exact_z = [&]() {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int v = 0; v < mine; ++v) {
+      const float logit = elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>));
+      sum += eligible(logit) ? exp((double)logit - (double)top) : 0.0;
     }
+    return row_all(sum, [](double p, double q) { return p + q; });
+  };
+  bool sure = SIGMOID || by_logit;     // whether z is exact, or moves no key
+  auto score64 = [&](float v) { return SIGMOID ? sigmoid_f64((double)v) : exp((double)v - (double)top) / z; };
+  if (!by_logit) {
     if (a.bias) {
       if (e0 + V <= E) {
 #pragma unroll
@@ -616,15 +654,23 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       return rank < a.top_groups;
     };
     bool near;
-    kept = keep(group_value<float>(two, lanes, a.group_best, pairs[wave].f, base, base + 16), near);
+    kept = keep(group_value<float>(two, lanes, a.group_best, pairs[wave].f, base, base + 16, rz), near);
     if (__any(near)) {
+      if (!sure) {
+        const double exact = exact_z();
+        const bool mine_near = row_count(__ballot(near)) > 0;   // this token's, not its neighbours' in the wave
+        z = mine_near ? exact : z;
+        sure = mine_near;
+      }
       Two<double> t64;
 #pragma unroll 1
       for (int v = 0; v < mine; ++v) {
         double unused;
         t64.add(key64(e0 + v, unused));
       }
-      kept = keep(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, base, base + 16), near);
+      const bool kept64 =
+          keep(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, base, base + 16, rz), near);
+      kept = sure ? kept64 : kept;
     }
     if (!kept) {
       two = Two<float>();
@@ -654,7 +700,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       else hi = mid;
     }
   }
-  auto slack = [&](float c) { return by_logit || c == kLowest ? c : c - 2.0f * key_error(c); };
+  auto slack = [&](float c) { return by_logit || c == kLowest ? c : c - 2.0f * key_error(c, rz); };
   // this lane's experts at or above c, bit v for expert e0 + v
   auto in_reach = [&](float c) {
     uint32_t m = 0;
@@ -706,6 +752,16 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     if (fits && l < n) {
       expert = found[wave][lane];
       k64 = key64(expert, s);
+    }
+    if (!SIGMOID && __any(!sure)) {
+      const float k32 = (float)k64;
+      const bool close = row_close<15>(k32, 2.0f * key_error(k32, rz)) && !sure && fits && l < n;
+      const bool retry = !sure && (n > 16 || row_count(__ballot(close)) > 0);
+      if (__any(retry)) {
+        const double exact = exact_z();
+        z = retry ? exact : z;
+        if (retry && fits && l < n) k64 = key64(expert, s);
+      }
     }
     // candidates stand in expert order, so equal keys go by lane
     const int r = row_rank<15>(k64);
@@ -783,18 +839,23 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __res
     if (mine >= 0) g = (double)grad_weights[token * top_k + l];
   }
   const bool any = all(mine, [](int p, int q) { return max(p, q); }) >= 0;
+  float x = -INFINITY;
+  if (mine >= 0) x = elem_value<DT>(load_bits<DT>(row + mine * kElemBytes<DT>));
   float out[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) out[v] = 0.0f;
   float top = 0.0f;
   double z = 1.0;
   if constexpr (!SIGMOID) {
-    load_logits<DT, V>(row, e0, on && any ? min(V, max(0, E - e0)) : 0, out);
-    float most = -INFINITY;
+    auto larger = [](float p, float q) { return fmaxf(p, q); };
+    if (renormalize) {
+      top = all(x, larger);            // a common factor of the scores drops out: the chosen logits are enough
+    } else {
+      load_logits<DT, V>(row, e0, on && any ? min(V, max(0, E - e0)) : 0, out);
+      float most = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v) most = fmaxf(most, out[v]);
-    top = all(most, [](float p, float q) { return fmaxf(p, q); });
-    if (!renormalize) {
+      for (int v = 0; v < V; ++v) most = fmaxf(most, out[v]);
+      top = all(most, larger);
       float sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -804,10 +865,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __res
       z = all((double)sum, add);
     }
   }
-  if (mine >= 0) {
-    const double x = (double)elem_value<DT>(load_bits<DT>(row + mine * kElemBytes<DT>));
-    s = SIGMOID ? sigmoid_f64(x) : exp(x - (double)top) / z;
-  }
+  if (mine >= 0) s = SIGMOID ? sigmoid_f64((double)x) : exp((double)x - (double)top) / z;
   double du = scale * g;
   if (renormalize) {
     const double sum = all(s, add), mean = all(g * s, add);
@@ -851,14 +909,14 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   while (v * 64 < a.experts) v *= 2;
   const bool whole = a.groups == 1 || (a.experts / a.groups) % v == 0;
   // 16 lanes a token
-  const int v16 = a.experts <= 64 ? 4 : a.experts <= 128 ? 8 : 16;
-  if (a.tokens >= kRowTokens && a.experts <= 256 && a.top_k <= 16 &&
-      (a.groups == 1 || (a.experts / a.groups) % v16 == 0)) {
-    const unsigned grid = (unsigned)((a.tokens + 4 * kTokens - 1) / (4 * kTokens));
+  const int v16 = a.experts <= 64 ? 4 : a.experts <= 128 ? 8 : a.experts <= 256 ? 16 : 32;
+  if (a.experts <= 512 && a.top_k <= 16 && (a.groups == 1 || (a.experts / a.groups) % v16 == 0)) {
+    const int64_t grid = (a.tokens + 4 * kTokens - 1) / (4 * kTokens);
 #define LAUNCH(DT, SIGMOID)                                                               \
-  if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<grid, kThreads, 0, st>>>(a);           \
-  else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<grid, kThreads, 0, st>>>(a);      \
-  else k_moe_route_rows<DT, 16, SIGMOID><<<grid, kThreads, 0, st>>>(a)
+  if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a);      \
+  else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
+  else if (v16 == 16) k_moe_route_rows<DT, 16, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
+  else k_moe_route_rows<DT, 32, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a)
 #define CALL(DT)                            \
   if (a.sigmoid) { LAUNCH(DT, true); }      \
   else { LAUNCH(DT, false); }

@@ -45,7 +45,8 @@ def check(x, k, dtype="f32", bias=None, mask=None, grad=True, **kw):
 
 
 SIZES = [(1, 8, 2), (3, 60, 4), (5, 64, 8), (64, 256, 8), (65, 256, 1), (7, 384, 6), (4, 1024, 32), (2, 33, 32),
-         (9, 1, 1), (6, 17, 17), (1, 512, 9), (130, 128, 8), (5, 1000, 3)]
+         (9, 1, 1), (6, 17, 17), (1, 512, 9), (130, 128, 8), (5, 1000, 3), (7, 100, 20),
+         (5, 300, 8), (6, 512, 16), (3, 500, 24)]
 
 
 @pytest.mark.parametrize("T,E,k", SIZES)
@@ -90,7 +91,7 @@ def test_route_near_ties_are_decided_in_fp64():
 
 
 GROUPS = [(64, 4, 2, 8, 2), (256, 8, 4, 8, 2), (160, 8, 3, 6, 1), (256, 8, 1, 8, 2), (60, 12, 5, 4, 2), (64, 64, 8, 8, 2),
-          (1024, 64, 4, 8, 2), (21, 3, 2, 5, 2), (256, 4, 4, 8, 2), (12, 6, 1, 4, 2), (512, 16, 3, 8, 1),
+          (1024, 64, 4, 8, 2), (21, 3, 2, 5, 2), (256, 4, 4, 8, 2), (12, 6, 1, 4, 2), (512, 16, 3, 8, 1), (512, 4, 2, 8, 2), (384, 8, 4, 8, 2), (320, 5, 2, 6, 2),
           (130, 13, 4, 8, 2), (1000, 8, 3, 8, 2), (130, 13, 2, 32, 1)]
 
 
@@ -146,7 +147,8 @@ def many(g, T, E, dtype="f32", distinct=40):
 MANY = [(4096, 256, 8, dict(groups=8, top_groups=4)), (5001, 256, 8, dict()), (2050, 60, 4, dict()), (3000, 64, 16, dict()),
         (2048, 128, 1, dict(groups=4, top_groups=1)), (2049, 17, 3, dict()), (2500, 96, 6, dict(groups=12, top_groups=5)),
         (2500, 240, 8, dict(groups=5, top_groups=2)), (2300, 256, 16, dict(groups=2, top_groups=1, group_best=1)),
-        (2100, 384, 8, dict(groups=8, top_groups=3)), (2100, 200, 17, dict()), (2100, 130, 8, dict(groups=13, top_groups=4))]
+        (2100, 384, 8, dict(groups=8, top_groups=3)), (2100, 200, 17, dict()), (2100, 130, 8, dict(groups=13, top_groups=4)),
+        (2100, 512, 8, dict(groups=16, top_groups=5)), (2100, 500, 10, dict())]
 
 
 @pytest.mark.parametrize("T,E,k,kw", MANY)
