@@ -9,14 +9,14 @@
 // than top_k), and give each candidate a lane, an fp64 key and a rank: the
 // number of candidates before it.  Three kernels, chosen by what fits:
 //   k_moe_route_rows     16 lanes a token: up to 512 experts, 16 places, groups
-//                        of whole lanes (of 4, 8, 16 or 32 experts);
+//                        of whole lanes (of 4, 8, 16, 24 or 32 experts);
 //   k_moe_route          a wave a token: up to 1024 experts, 32 places, groups of
 //                        whole lanes (of 1, 2, 4, 8 or 16 experts);
 //   k_moe_route_general  a wave a token with fp64 keys in LDS throughout: any
 //                        group size.
 // 16384 tokens x 256 experts, 8 of 256 in 4 of 8 groups, sigmoid and bias, fp32:
-// 11.6, 23.6 and 55.3 us.  All are bound by instructions, not by the 16.8 MB of
-// logits (3.4 us): 828 vector instructions for four tokens in the first.
+// 10.1, 23.6 and 55.3 us.  All are bound by instructions, not by the 16.8 MB of
+// logits (3.4 us): some 850 vector instructions for four tokens in the first.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -155,13 +155,14 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_general(RouteArgs a) {
 // can be (sigmoid 1, softmax 1 / z):
 // sigmoid 1 / (1 + e), e = 2^(-x log2 e): e is off by 1.4 |x| u (the product and
 // the constant) and 2 u, which moves the score by s (1 - s) times that, at most
-// u; the sum adds u and the reciprocal 2 u.  softmax p = e / z, e = 2^((x - top)
-// log2 e): p |x - top| 2.4 u <= u and 2 u, or 4 u by exp_neg; z in fp64 or a sum
-// of such exponentials, 4 u; its reciprocal and the product 2 u.  A bias adds
-// half an ulp of the key.
+// u; the sum adds u and the reciprocal 2 u: 4.  softmax p = e / z, e = 2^((x -
+// top) log2 e): p |x - top| 2.4 u <= u and 2 u, or 4 u by exp_neg; z in fp64 or a
+// sum of such exponentials, 4 u; its reciprocal and the product 3 u: 11.  A bias
+// adds half an ulp of the key, u times its size.
 constexpr float kUlp = 0x1p-24f;
+constexpr float kScoreError = 12.0f;
 constexpr float kLog2e = 0x1.715476p+0f;
-__device__ __forceinline__ float key_error(float key, float most) { return kUlp * (16.0f * most + 2.0f * fabsf(key)); }
+__device__ __forceinline__ float key_error(float key, float most) { return kUlp * (kScoreError * most + 1.25f * fabsf(key)); }
 __device__ __forceinline__ float sigmoid_key(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
 }
@@ -223,11 +224,13 @@ struct Two {
   }
 };
 
-// A group's value, and a bound on its error where its keys are fp32 ones.
+// A group's value, a bound on its error where its keys are fp32 ones, and the
+// smallest key in it.
 template <typename T>
 struct GroupValue {
   T value;
   float error;
+  T least;
 };
 
 union GroupPairs {
@@ -263,10 +266,11 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
     }
     wave_sync();
   }
-  if (!(t.best > -INFINITY)) return {t.best, 0.0f};
-  if (best == 2 && t.next > -INFINITY)
-    return {t.best + t.next, kUlp * (32.0f * most + 4.0f * (fabsf((float)t.best) + fabsf((float)t.next)))};
-  return {t.best, kUlp * (32.0f * most + 4.0f * fabsf((float)t.best))};
+  if (!(t.best > -INFINITY)) return {t.best, 0.0f, t.best};
+  if (best == 2 && t.next > -INFINITY)       // two keys' errors, and the sum's rounding
+    return {t.best + t.next,
+            kUlp * (2.0f * kScoreError * most + 2.5f * (fabsf((float)t.best) + fabsf((float)t.next))), t.next};
+  return {t.best, key_error((float)t.best, most), t.best};
 }
 
 // Whether this lane's group is among the `top` groups of largest value; near:
@@ -307,6 +311,15 @@ __device__ __forceinline__ void load_logits(const uint8_t* row, int e0, int mine
     for (int v = 0; v < V; ++v)
       x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : -INFINITY;
   }
+}
+
+// The keys at or above c among this lane's, bit v for key v.
+template <int V>
+__device__ __forceinline__ uint32_t in_reach(const float (&key)[V], float c) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int v = V - 1; v >= 0; --v) m = m + m + (key[v] >= c ? 1u : 0u);
+  return m;
 }
 
 // A point between lo and hi to count at: their mean, or in every other step the
@@ -386,14 +399,15 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) t.add(key[v]);
     bool near;
-    kept = group_kept(group_value<float>(t, lanes, a.group_best, pairs[wave].f, 0, 64, rz), a.groups, lanes,
-                      a.top_groups, near);
-    if (near) {
+    const GroupValue<float> value = group_value<float>(t, lanes, a.group_best, pairs[wave].f, 0, 64, rz);
+    kept = group_kept(value, a.groups, lanes, a.top_groups, near);
+    if (near) {                        // again in fp64, from the keys that can be among a group's largest
       Two<double> t64;
+      const float least = value.least > -INFINITY ? value.least - 2.0f * key_error(value.least, rz) : INFINITY;
 #pragma unroll 1
-      for (int v = 0; v < mine; ++v) {
+      for (uint32_t m = in_reach(key, least); m; m &= m - 1) {
         float l;
-        t64.add(key64(v, l));
+        t64.add(key64(__builtin_ctz(m), l));
       }
       kept = group_kept(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, 0, 64, rz), a.groups, lanes,
                         a.top_groups, near);
@@ -505,8 +519,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 // instruction serves four tokens in what is done once a token (the fp64 scores
 // of the candidates, their ranks, the groups), which is most of the work.
 // Grouped sigmoid router with a bias, 256 experts, here and wave-wide: 4 tokens
-// 4.6 and 5.1 us, 1024 tokens 5.2 and 5.7, 16384 tokens 11.6 and 23.6, 65536
-// tokens 28 and 81; 512 experts, 16384 tokens 19 and 32.
+// 4.6 and 5.1 us, 1024 tokens 5.2 and 5.7, 16384 tokens 10.1 and 23.6, 65536
+// tokens 26 and 81; 512 experts, 16384 tokens 15.3 and 31.7.
 
 // Number of set lanes of `m` in this lane's row of 16.
 __device__ __forceinline__ int row_count(uint64_t m) {
@@ -654,7 +668,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       return rank < a.top_groups;
     };
     bool near;
-    kept = keep(group_value<float>(two, lanes, a.group_best, pairs[wave].f, base, base + 16, rz), near);
+    const GroupValue<float> value = group_value<float>(two, lanes, a.group_best, pairs[wave].f, base, base + 16, rz);
+    kept = keep(value, near);
     if (__any(near)) {
       if (!sure) {
         const double exact = exact_z();
@@ -662,11 +677,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
         z = mine_near ? exact : z;
         sure = mine_near;
       }
-      Two<double> t64;
+      Two<double> t64;                 // from the keys that can be among a group's largest
+      const float least = value.least > kNone ? value.least - 2.0f * key_error(value.least, rz) : INFINITY;
 #pragma unroll 1
-      for (int v = 0; v < mine; ++v) {
+      for (uint32_t m = in_reach(key, least); m; m &= m - 1) {
         double unused;
-        t64.add(key64(e0 + v, unused));
+        t64.add(key64(e0 + __builtin_ctz(m), unused));
       }
       const bool kept64 =
           keep(group_value<double>(t64, lanes, a.group_best, pairs[wave].d, base, base + 16, rz), near);
@@ -701,17 +717,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     }
   }
   auto slack = [&](float c) { return by_logit || c == kLowest ? c : c - 2.0f * key_error(c, rz); };
-  // this lane's experts at or above c, bit v for expert e0 + v
-  auto in_reach = [&](float c) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v) m = m + m + (key[v] >= c ? 1u : 0u);
-    return m;
-  };
   auto row_total = [&](uint32_t m) {
     return row_all(__builtin_popcount(m), [](int p, int q) { return p + q; });
   };
-  uint32_t reach = in_reach(slack(cut));
+  uint32_t reach = in_reach(key, slack(cut));
   int n = row_total(reach);
   if (__any(n > 16)) {
     float lo = INFINITY, hi = kNone;
@@ -725,10 +734,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     lo = fmaxf(lo, cut);
     for (int i = 0; i < 64 && __any(n > 16); ++i) {
       const float mid = halfway(lo, hi, i);
-      if (row_total(in_reach(mid)) >= k) {
+      if (row_total(in_reach(key, mid)) >= k) {
         lo = mid;
         if (n > 16) {
-          reach = in_reach(slack(mid));
+          reach = in_reach(key, slack(mid));
           n = row_total(reach);
         }
       } else {
@@ -909,13 +918,14 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   while (v * 64 < a.experts) v *= 2;
   const bool whole = a.groups == 1 || (a.experts / a.groups) % v == 0;
   // 16 lanes a token
-  const int v16 = a.experts <= 64 ? 4 : a.experts <= 128 ? 8 : a.experts <= 256 ? 16 : 32;
+  const int v16 = a.experts <= 64 ? 4 : a.experts <= 128 ? 8 : a.experts <= 256 ? 16 : a.experts <= 384 ? 24 : 32;
   if (a.experts <= 512 && a.top_k <= 16 && (a.groups == 1 || (a.experts / a.groups) % v16 == 0)) {
     const int64_t grid = (a.tokens + 4 * kTokens - 1) / (4 * kTokens);
 #define LAUNCH(DT, SIGMOID)                                                               \
   if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a);      \
   else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
   else if (v16 == 16) k_moe_route_rows<DT, 16, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
+  else if (v16 == 24) k_moe_route_rows<DT, 24, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
   else k_moe_route_rows<DT, 32, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a)
 #define CALL(DT)                            \
   if (a.sigmoid) { LAUNCH(DT, true); }      \
