@@ -13,6 +13,10 @@
  * fixed order and no atomic decides one.  Sums, scores and statistics are
  * held in fp32 or fp64; each output is rounded once, nearest-even.
  *
+ * MXQ_ERR_HIP also means a call of more threads than one launch takes (2^32):
+ * 64 per token and 512 columns in the row operations, 16 or 64 per token in the
+ * router.
+ *
  * Words used below
  * ----------------
  *  slot   one of the tokens * top_k routed places: slot t * top_k + j is

@@ -13,6 +13,9 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxGroups = 64;
 
+// A launch's threads in one dimension are counted in 32 bits.
+inline bool launchable(int64_t blocks, int64_t threads) { return blocks > 0 && blocks <= 0xFFFFFFFFll / threads; }
+
 struct RouteArgs {
   const void* logits;
   const float* bias;          // NULL: none

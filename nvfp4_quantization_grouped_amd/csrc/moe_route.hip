@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __res
 
 hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   const int64_t blocks = (a.tokens + kTokens - 1) / kTokens;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launchable(blocks, kThreads)) return hipErrorInvalidValue;
   // experts of a lane: enough for 64 lanes, and no group cut inside a lane
   int v = 1;
   while (v * 64 < a.experts) v *= 2;
@@ -958,7 +958,7 @@ hipError_t launch_moe_route_bwd(const void* logits, int dt, int64_t tokens, int 
   const bool rows = experts <= 256 && top_k <= 16;
   const int lanes = rows ? 16 : 64, v = (experts + lanes - 1) / lanes;
   const int64_t blocks = (tokens * lanes + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launchable(blocks, kThreads)) return hipErrorInvalidValue;
 #define LAUNCH(DT, G, V, SIGMOID)                                                                             \
   k_moe_route_bwd<DT, G, V, SIGMOID><<<(unsigned)blocks, kThreads, 0, st>>>(                                  \
       (const uint8_t*)logits, tokens, experts, top_k, renormalize, scale, index, grad_weights, (uint8_t*)grad_logits)

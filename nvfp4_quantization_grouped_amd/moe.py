@@ -8,6 +8,10 @@ Tensors must be CUDA (ROCm) tensors on one device; calls are enqueued on the
 current stream of that device, outputs and workspaces are allocated with
 PyTorch's caching allocator.  There is no CPU path.
 
+Everything can be captured into a graph, backward passes too; as with any
+operator, a backward is captured with ``torch.autograd.grad``, or with leaves of
+which no eager graph is alive.
+
 A layer's pass, as :func:`mxfp4_moe` makes it::
 
     weights, experts = moe_route(logits, 8, score="sigmoid", bias=bias, groups=8, top_groups=4)
