@@ -29,7 +29,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .ops import _DT, _E8M0, _FMT, _need_cuda, _ptr
+from .ops import _DT, _E8M0, _FMT, _need_cuda
 from .ops import (MXFP4GroupedMM, mxfp4_grouped_mm_fwd_w4a4, mxfp4_grouped_mm_fwd_w4a4_quantized,
                   mxfp4_grouped_mm_fwd_w4a8, mxfp4_grouped_mm_fwd_w4a8_quantized)
 
@@ -86,23 +86,25 @@ def _first_order(backward):
 
 
 def _float_type(t, name):
-    if t.dtype not in _DT:
+    code = _DT.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return _DT[t.dtype]
+    return code
 
 
-def _grad_wanted(*ts):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+def _ptr(t):
+    """Address of a tensor's first element; 0 (NULL) for None and for an empty tensor."""
+    return 0 if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------------------- router
 def _route(logits, top_k, score, bias, groups, top_groups, group_best, renormalize, scale, mask):
     T, E = logits.shape
-    weights = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
-    experts = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
-    _call("moe_route", logits.device, _ptr(logits), _DT[logits.dtype], T, E, top_k, _SCORE[score],
-          None if bias is None else bias.data_ptr(), groups, top_groups, group_best, int(renormalize), float(scale),
-          None if mask is None else _ptr(mask), _ptr(weights), _ptr(experts))
+    device = logits.device
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=device)
+    experts = torch.empty(T, top_k, dtype=torch.int32, device=device)
+    _call("moe_route", device, logits.data_ptr(), _DT[logits.dtype], T, E, top_k, score, _ptr(bias), groups,
+          top_groups, group_best, renormalize, scale, _ptr(mask), weights.data_ptr(), experts.data_ptr())
     return weights, experts
 
 
@@ -126,8 +128,8 @@ class _MoERoute(torch.autograd.Function):
         g = grad_weights.contiguous()
         grad = torch.empty_like(logits)
         T, E = logits.shape
-        _call("moe_route_bwd", logits.device, _ptr(logits), _DT[logits.dtype], T, E, experts.shape[1], _SCORE[score],
-              int(renormalize), float(scale), _ptr(experts), _ptr(g), _ptr(grad))
+        _call("moe_route_bwd", logits.device, logits.data_ptr(), _DT[logits.dtype], T, E, experts.shape[1], score,
+              renormalize, scale, experts.data_ptr(), g.data_ptr(), grad.data_ptr())
         return (grad,) + (None,) * 9
 
 
@@ -148,23 +150,26 @@ def moe_route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups
     have a gradient with respect to the logits."""
     if score not in _SCORE:
         raise ValueError("moe_route: score must be 'softmax' or 'sigmoid'")
-    _need_cuda(*(t for t in (logits, bias, token_mask) if t is not None))
+    _need_cuda(logits)
     _float_type(logits, "moe_route")
     if logits.dim() != 2:
         raise ValueError("moe_route: logits must be [tokens, experts]")
     if bias is not None:
-        if bias.dtype != torch.float32 or tuple(bias.shape) != (logits.shape[1],):
+        _need_cuda(logits, bias)
+        if bias.dtype != torch.float32 or bias.shape != logits.shape[1:]:
             raise TypeError("moe_route: bias must be float32 [experts]")
         bias = bias.detach().contiguous()
     if token_mask is not None:
-        if token_mask.dtype != torch.bool or tuple(token_mask.shape) != (logits.shape[0],):
+        _need_cuda(logits, token_mask)
+        if token_mask.dtype != torch.bool or token_mask.shape != logits.shape[:1]:
             raise TypeError("moe_route: token_mask must be bool [tokens]")
         token_mask = token_mask.contiguous()
-    args = (logits.contiguous(), int(top_k), score, bias, int(groups), int(top_groups), int(group_best),
-            bool(renormalize), float(scale), token_mask)
-    if not 1 <= args[1] <= min(32, logits.shape[1]):
+    top_k = int(top_k)
+    if not 1 <= top_k <= min(32, logits.shape[1]):
         raise ValueError("moe_route: top_k must be between 1 and 32 and no more than the experts")
-    return _MoERoute.apply(*args) if _grad_wanted(logits) else _route(*args)
+    args = (logits.contiguous(), top_k, _SCORE[score], bias, int(groups), int(top_groups), int(group_best),
+            int(bool(renormalize)), float(scale), token_mask)
+    return _MoERoute.apply(*args) if logits.requires_grad and torch.is_grad_enabled() else _route(*args)
 
 
 # ------------------------------------------------------------ grouped order
@@ -190,8 +195,8 @@ def moe_plan(experts, num_experts, first_expert=0, local_experts=None):
     rows = torch.empty_like(e)
     slots = torch.empty(T * k, dtype=torch.int32, device=e.device)
     work = torch.empty(need // 4, dtype=torch.int32, device=e.device) if need else None
-    _call("moe_plan", e.device, _ptr(e), T, k, first_expert, local, _ptr(offs), _ptr(rows), _ptr(slots),
-          None if work is None else work.data_ptr(), need)
+    _call("moe_plan", e.device, e.data_ptr(), T, k, first_expert, local, offs.data_ptr(), rows.data_ptr(),
+          slots.data_ptr(), _ptr(work), need)
     return MoEPlan(offs, rows, slots)
 
 
@@ -210,7 +215,7 @@ def _plan_rows(rows, tokens, device, name):
 def _dispatch(x, rows):
     (T, H), k = x.shape, rows.shape[1]
     out = torch.empty(T * k, H, dtype=x.dtype, device=x.device)
-    _call("moe_dispatch", x.device, _ptr(x), _DT[x.dtype], T, H, k, _ptr(rows), _ptr(out))
+    _call("moe_dispatch", x.device, x.data_ptr(), _DT[x.dtype], T, H, k, rows.data_ptr(), out.data_ptr())
     return out
 
 
@@ -227,7 +232,7 @@ class _MoEDispatch(torch.autograd.Function):
         g = grad.contiguous()
         (T, k), H = rows.shape, g.shape[1]
         out = torch.empty(T, H, dtype=g.dtype, device=g.device)
-        _call("moe_dispatch_bwd", g.device, _ptr(g), _DT[g.dtype], T, H, k, _ptr(rows), _ptr(out))
+        _call("moe_dispatch_bwd", g.device, g.data_ptr(), _DT[g.dtype], T, H, k, rows.data_ptr(), out.data_ptr())
         return out, None
 
 
@@ -241,7 +246,7 @@ def moe_dispatch(x, plan):
         raise ValueError("moe_dispatch: x must be [tokens, hidden]")
     rows = _plan_rows(plan.rows, x.shape[0], x.device, "moe_dispatch")
     x = x.contiguous()
-    return _MoEDispatch.apply(x, rows) if _grad_wanted(x) else _dispatch(x, rows)
+    return _MoEDispatch.apply(x, rows) if x.requires_grad and torch.is_grad_enabled() else _dispatch(x, rows)
 
 
 def moe_dispatch_quantized(x, plan, format):
@@ -265,8 +270,8 @@ def moe_dispatch_quantized(x, plan, format):
     fp4 = format == "mxfp4"
     codes = torch.empty(T * k, H // 2 if fp4 else H, dtype=torch.int8 if fp4 else torch.uint8, device=x.device)
     scales = torch.empty(T * k, H // 32, dtype=torch.uint8, device=x.device)
-    _call("moe_dispatch_quantized", x.device, _ptr(x), dt, T, H, k, _ptr(rows), _FMT[format], _ptr(codes),
-          _ptr(scales))
+    _call("moe_dispatch_quantized", x.device, x.data_ptr(), dt, T, H, k, rows.data_ptr(), _FMT[format],
+          codes.data_ptr(), scales.data_ptr())
     return codes, (scales.view(_E8M0) if fp4 and _E8M0 is not None else scales)
 
 
@@ -274,7 +279,8 @@ def moe_dispatch_quantized(x, plan, format):
 def _combine(y, weights, rows):
     (T, k), H = rows.shape, y.shape[1]
     out = torch.empty(T, H, dtype=y.dtype, device=y.device)
-    _call("moe_combine", y.device, _ptr(y), _DT[y.dtype], T, H, k, _ptr(rows), _ptr(weights), _ptr(out))
+    _call("moe_combine", y.device, y.data_ptr(), _DT[y.dtype], T, H, k, rows.data_ptr(), weights.data_ptr(),
+          out.data_ptr())
     return out
 
 
@@ -294,8 +300,8 @@ class _MoECombine(torch.autograd.Function):
         (T, k), H = rows.shape, shape[1]
         gy = torch.empty(shape, dtype=dtype, device=g.device) if ctx.needs_input_grad[0] else None
         gw = torch.empty_like(weights) if ctx.needs_input_grad[1] else None
-        _call("moe_combine_bwd", g.device, _ptr(g), None if y is None else _ptr(y), _DT[dtype], T, H, k, _ptr(rows),
-              _ptr(weights), None if gy is None else _ptr(gy), None if gw is None else _ptr(gw))
+        _call("moe_combine_bwd", g.device, g.data_ptr(), _ptr(y), _DT[dtype], T, H, k, rows.data_ptr(),
+              weights.data_ptr(), _ptr(gy), _ptr(gw))
         return gy, gw, None
 
 
@@ -314,7 +320,9 @@ def moe_combine(y, weights, plan):
     if y.dim() != 2 or y.shape[0] != rows.numel():
         raise ValueError("moe_combine: y must be [tokens * top_k, hidden]")
     y, weights = y.contiguous(), weights.contiguous()
-    return _MoECombine.apply(y, weights, rows) if _grad_wanted(y, weights) else _combine(y, weights, rows)
+    if (y.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
+        return _MoECombine.apply(y, weights, rows)
+    return _combine(y, weights, rows)
 
 
 # ------------------------------------------------------------------- swiglu
@@ -325,8 +333,8 @@ def _swiglu(x, offs, keep):
     if keep:
         codes = torch.empty(R, 2 * I, dtype=torch.uint8, device=x.device)
         scales = torch.empty(R, 2 * I // CHECKPOINT_BLOCK, dtype=torch.uint8, device=x.device)
-    _call("swiglu_fwd", x.device, _ptr(x), _DT[x.dtype], R, I, None if offs is None else _ptr(offs),
-          0 if offs is None else offs.numel(), _ptr(h), _ptr(codes) if keep else None, _ptr(scales) if keep else None)
+    _call("swiglu_fwd", x.device, x.data_ptr(), _DT[x.dtype], R, I, _ptr(offs), 0 if offs is None else offs.shape[0],
+          h.data_ptr(), _ptr(codes), _ptr(scales))
     return h, codes, scales
 
 
@@ -344,9 +352,8 @@ class _SwiGLU(torch.autograd.Function):
         g = grad.contiguous()
         R, I = g.shape
         out = torch.empty(R, 2 * I, dtype=g.dtype, device=g.device)
-        _call("swiglu_bwd", g.device, _ptr(g), None if x is None else _ptr(x), None if codes is None else _ptr(codes),
-              None if scales is None else _ptr(scales), _DT[g.dtype], R, I, None if offs is None else _ptr(offs),
-              0 if offs is None else offs.numel(), _ptr(out))
+        _call("swiglu_bwd", g.device, g.data_ptr(), _ptr(x), _ptr(codes), _ptr(scales), _DT[g.dtype], R, I, _ptr(offs),
+              0 if offs is None else offs.shape[0], out.data_ptr())
         return out, None, None
 
 
@@ -361,18 +368,21 @@ def swiglu(gate_up, offs=None, checkpoint="fp8"):
     ``quantize_cache_packed(gate_up, "fp8", 32)`` gives), and the gradient is
     that of silu(gate) * up at the kept values; ``checkpoint=None`` keeps
     gate_up itself."""
-    _need_cuda(*(t for t in (gate_up, offs) if t is not None))
+    _need_cuda(gate_up)
     _float_type(gate_up, "swiglu")
     if checkpoint not in ("fp8", None):
         raise ValueError("swiglu: checkpoint must be 'fp8' or None")
     if gate_up.dim() != 2 or gate_up.shape[1] % 64:
         raise ValueError("swiglu: gate_up must be [rows, 2 * inter] with inter a multiple of 32")
     if offs is not None:
-        if offs.dtype != torch.int32 or offs.dim() != 1 or offs.numel() == 0:
+        _need_cuda(gate_up, offs)
+        if offs.dtype != torch.int32 or offs.dim() != 1 or offs.shape[0] == 0:
             raise TypeError("swiglu: offs must be int32 [experts]")
         offs = offs.contiguous()
     x = gate_up.contiguous()
-    return _SwiGLU.apply(x, offs, checkpoint) if _grad_wanted(x) else _swiglu(x, offs, False)[0]
+    if x.requires_grad and torch.is_grad_enabled():
+        return _SwiGLU.apply(x, offs, checkpoint)
+    return _swiglu(x, offs, False)[0]
 
 
 # -------------------------------------------------------------------- layer
@@ -394,7 +404,7 @@ def mxfp4_moe(x, weights, experts, gate_up, gate_up_scales, down, down_scales, *
         raise ValueError("mxfp4_moe: activations must be 'bf16', 'fp8' or 'mxfp4'")
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise TypeError("mxfp4_moe: x must be bfloat16 [tokens, hidden]")
-    if activations != "bf16" and _grad_wanted(x, weights):
+    if activations != "bf16" and (x.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
         raise ValueError("mxfp4_moe: low-bit activations have no gradient")
     local = gate_up.shape[0]
     plan = moe_plan(experts, first_expert + local if num_experts is None else num_experts, first_expert, local)
