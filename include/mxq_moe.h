@@ -186,6 +186,17 @@ int swiglu_fwd(const void* gate_up, int t, int64_t rows, int64_t inter, const in
 int swiglu_bwd(const void* grad_h, const void* gate_up, const uint8_t* codes, const uint8_t* scales, int t,
                int64_t rows, int64_t inter, const int32_t* offs, int64_t experts, void* grad_gate_up, void* stream);
 
+/*
+ * swiglu_quantized -- h as swiglu_fwd writes it, rounded to t, and then quantized
+ * on the way out: the operand of the low-bit down product.  What quantizing
+ * swiglu_fwd's h would give, bit for bit, without writing h.  fmt, codes and
+ * scales as in moe_dispatch_quantized, with inter for hidden; rows that do not
+ * count get what a row of zeros gives.  h must be finite.
+ * Errors: as swiglu_fwd, and MXQ_ERR_FORMAT.
+ */
+int swiglu_quantized(const void* gate_up, int t, int64_t rows, int64_t inter, const int32_t* offs, int64_t experts,
+                     int fmt, uint8_t* codes, uint8_t* scales, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,6 +39,7 @@ from .moe import (
     moe_route,
     mxfp4_moe,
     swiglu,
+    swiglu_quantized,
 )
 
 __all__ = [
@@ -51,4 +52,5 @@ __all__ = [
     "quantize_nvfp4", "dequantize_nvfp4", "quantize_cache_packed", "dequantize_cache_packed",
     "quantize_nvfp4_mse", "validate_offs",
     "MoEPlan", "moe_combine", "moe_dispatch", "moe_dispatch_quantized", "moe_plan", "moe_route", "mxfp4_moe", "swiglu",
+    "swiglu_quantized",
 ]

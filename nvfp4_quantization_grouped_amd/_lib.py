@@ -26,7 +26,7 @@ EXPORTS = (
 # include/mxq_moe.h
 MOE_EXPORTS = (
     "moe_route", "moe_route_bwd", "moe_plan_workspace", "moe_plan", "moe_dispatch", "moe_dispatch_bwd",
-    "moe_dispatch_quantized", "moe_combine", "moe_combine_bwd", "swiglu_fwd", "swiglu_bwd",
+    "moe_dispatch_quantized", "moe_combine", "moe_combine_bwd", "swiglu_fwd", "swiglu_bwd", "swiglu_quantized",
 )
 
 _lib = None
@@ -63,6 +63,7 @@ _MOE_SIGS = {
     "moe_combine_bwd": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp], _int),
     "swiglu_fwd": ([_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp], _int),
     "swiglu_bwd": ([_vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _i64, _vp, _vp], _int),
+    "swiglu_quantized": ([_vp, _int, _i64, _i64, _vp, _i64, _int, _vp, _vp, _vp], _int),
 }
 
 

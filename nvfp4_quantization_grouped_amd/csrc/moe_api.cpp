@@ -208,6 +208,21 @@ int swiglu_fwd(const void* gate_up, int t, int64_t rows, int64_t inter, const in
                                          scales, (hipStream_t)stream));
 }
 
+int swiglu_quantized(const void* gate_up, int t, int64_t rows, int64_t inter, const int32_t* offs, int64_t experts,
+                     int fmt, uint8_t* codes, uint8_t* scales, void* stream) {
+  const int st = swiglu_shape(t, rows, inter, offs, experts);
+  if (st != MXQ_OK) return st;
+  if (fmt != MXQ_FMT_FP8 && fmt != MXQ_FMT_MXFP4) return MXQ_ERR_FORMAT;
+  if (rows == 0 || inter == 0) return MXQ_OK;
+  if (!gate_up || !codes || !scales) return MXQ_ERR_NULL;
+  if (misaligned4(offs)) return MXQ_ERR_ALIGN;
+  const int64_t n = rows * inter, nc = fmt == MXQ_FMT_FP8 ? n : n / 2;
+  const Span in[] = {{gate_up, 2 * n * dtype_bytes(t)}, {offs, experts * 4}, {codes, nc}};
+  if (overlaps_any({codes, nc}, in, 2) || overlaps_any({scales, n / 32}, in, 3)) return MXQ_ERR_ALIAS;
+  return from_hip(mxq::launch_swiglu_quantized(gate_up, t, rows, inter, offs ? offs + experts - 1 : nullptr, fmt, codes,
+                                               scales, (hipStream_t)stream));
+}
+
 int swiglu_bwd(const void* grad_h, const void* gate_up, const uint8_t* codes, const uint8_t* scales, int t,
                int64_t rows, int64_t inter, const int32_t* offs, int64_t experts, void* grad_gate_up, void* stream) {
   const int st = swiglu_shape(t, rows, inter, offs, experts);

@@ -50,6 +50,8 @@ hipError_t launch_moe_combine_bwd(const void* grad_out, const void* y, int dt, i
 // total: the count of rows that count, in device memory (NULL: all of them).
 hipError_t launch_swiglu_fwd(const void* gate_up, int dt, int64_t rows, int64_t inter, const int32_t* total, void* h,
                              uint8_t* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_swiglu_quantized(const void* gate_up, int dt, int64_t rows, int64_t inter, const int32_t* total,
+                                   int fmt, uint8_t* codes, uint8_t* scales, hipStream_t st);
 hipError_t launch_swiglu_bwd(const void* grad_h, const void* gate_up, const uint8_t* codes, const uint8_t* scales,
                              int dt, int64_t rows, int64_t inter, const int32_t* total, void* grad_gate_up,
                              hipStream_t st);

@@ -30,8 +30,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .ops import _DT, _E8M0, _FMT, _need_cuda
-from .ops import (MXFP4GroupedMM, mxfp4_grouped_mm_fwd_w4a4, mxfp4_grouped_mm_fwd_w4a4_quantized,
-                  mxfp4_grouped_mm_fwd_w4a8, mxfp4_grouped_mm_fwd_w4a8_quantized)
+from .ops import MXFP4GroupedMM, mxfp4_grouped_mm_fwd_w4a4_quantized, mxfp4_grouped_mm_fwd_w4a8_quantized
 
 CHECKPOINT_BLOCK = 32
 _SCORE = {"softmax": 0, "sigmoid": 1}
@@ -249,6 +248,19 @@ def moe_dispatch(x, plan):
     return _MoEDispatch.apply(x, rows) if x.requires_grad and torch.is_grad_enabled() else _dispatch(x, rows)
 
 
+def _quantized_rows(rows, width, format, device):
+    """Codes and scale bytes of rows in the form that the products with low-bit activations take."""
+    if format == "mxfp4":
+        codes = torch.empty(rows, width // 2, dtype=torch.int8, device=device)
+    else:
+        codes = torch.empty(rows, width, dtype=torch.uint8, device=device)
+    return codes, torch.empty(rows, width // 32, dtype=torch.uint8, device=device)
+
+
+def _scale_view(scales, format):
+    return scales.view(_E8M0) if format == "mxfp4" and _E8M0 is not None else scales
+
+
 def moe_dispatch_quantized(x, plan, format):
     """``moe_dispatch`` with the rows quantized on the way, in the form that a
     grouped GEMM with low-bit activations takes (no gradient).
@@ -267,12 +279,10 @@ def moe_dispatch_quantized(x, plan, format):
     rows = _plan_rows(plan.rows, x.shape[0], x.device, "moe_dispatch_quantized")
     x = x.detach().contiguous()
     (T, H), k = x.shape, rows.shape[1]
-    fp4 = format == "mxfp4"
-    codes = torch.empty(T * k, H // 2 if fp4 else H, dtype=torch.int8 if fp4 else torch.uint8, device=x.device)
-    scales = torch.empty(T * k, H // 32, dtype=torch.uint8, device=x.device)
+    codes, scales = _quantized_rows(T * k, H, format, x.device)
     _call("moe_dispatch_quantized", x.device, x.data_ptr(), dt, T, H, k, rows.data_ptr(), _FMT[format],
           codes.data_ptr(), scales.data_ptr())
-    return codes, (scales.view(_E8M0) if fp4 and _E8M0 is not None else scales)
+    return codes, _scale_view(scales, format)
 
 
 # ------------------------------------------------------------------ combine
@@ -326,6 +336,17 @@ def moe_combine(y, weights, plan):
 
 
 # ------------------------------------------------------------------- swiglu
+def _gate_up_args(gate_up, offs, name):
+    if gate_up.dim() != 2 or gate_up.shape[1] % 64:
+        raise ValueError(f"{name}: gate_up must be [rows, 2 * inter] with inter a multiple of 32")
+    if offs is not None:
+        _need_cuda(gate_up, offs)
+        if offs.dtype != torch.int32 or offs.dim() != 1 or offs.shape[0] == 0:
+            raise TypeError(f"{name}: offs must be int32 [experts]")
+        offs = offs.contiguous()
+    return gate_up.contiguous(), offs
+
+
 def _swiglu(x, offs, keep):
     R, I = x.shape[0], x.shape[1] // 2
     h = torch.empty(R, I, dtype=x.dtype, device=x.device)
@@ -372,17 +393,27 @@ def swiglu(gate_up, offs=None, checkpoint="fp8"):
     _float_type(gate_up, "swiglu")
     if checkpoint not in ("fp8", None):
         raise ValueError("swiglu: checkpoint must be 'fp8' or None")
-    if gate_up.dim() != 2 or gate_up.shape[1] % 64:
-        raise ValueError("swiglu: gate_up must be [rows, 2 * inter] with inter a multiple of 32")
-    if offs is not None:
-        _need_cuda(gate_up, offs)
-        if offs.dtype != torch.int32 or offs.dim() != 1 or offs.shape[0] == 0:
-            raise TypeError("swiglu: offs must be int32 [experts]")
-        offs = offs.contiguous()
-    x = gate_up.contiguous()
+    x, offs = _gate_up_args(gate_up, offs, "swiglu")
     if x.requires_grad and torch.is_grad_enabled():
         return _SwiGLU.apply(x, offs, checkpoint)
     return _swiglu(x, offs, False)[0]
+
+
+def swiglu_quantized(gate_up, format, offs=None):
+    """``swiglu`` with h quantized on its way out, in the form that a grouped
+    GEMM with low-bit activations takes (no gradient): the codes and scales that
+    quantizing swiglu's output gives, bit for bit, as ``moe_dispatch_quantized``
+    returns them for "fp8" and "mxfp4"."""
+    _need_cuda(gate_up)
+    dt = _float_type(gate_up, "swiglu_quantized")
+    if format not in ("fp8", "mxfp4"):
+        raise ValueError("swiglu_quantized: format must be 'fp8' or 'mxfp4'")
+    x, offs = _gate_up_args(gate_up.detach(), offs, "swiglu_quantized")
+    R, I = x.shape[0], x.shape[1] // 2
+    codes, scales = _quantized_rows(R, I, format, x.device)
+    _call("swiglu_quantized", x.device, x.data_ptr(), dt, R, I, _ptr(offs), 0 if offs is None else offs.shape[0],
+          _FMT[format], codes.data_ptr(), scales.data_ptr())
+    return codes, _scale_view(scales, format)
 
 
 # -------------------------------------------------------------------- layer
@@ -411,12 +442,8 @@ def mxfp4_moe(x, weights, experts, gate_up, gate_up_scales, down, down_scales, *
     if activations == "bf16":
         rows = MXFP4GroupedMM.apply(moe_dispatch(x, plan), gate_up, gate_up_scales, plan.offs)
         rows = MXFP4GroupedMM.apply(swiglu(rows, plan.offs, checkpoint), down, down_scales, plan.offs)
-    elif activations == "fp8":
-        q, s = moe_dispatch_quantized(x, plan, "fp8")
-        rows = mxfp4_grouped_mm_fwd_w4a8_quantized(q, s, gate_up, gate_up_scales, plan.offs)
-        rows = mxfp4_grouped_mm_fwd_w4a8(swiglu(rows, plan.offs), down, down_scales, plan.offs)
     else:
-        q, s = moe_dispatch_quantized(x, plan, "mxfp4")
-        rows = mxfp4_grouped_mm_fwd_w4a4_quantized(q, s, gate_up, gate_up_scales, plan.offs)
-        rows = mxfp4_grouped_mm_fwd_w4a4(swiglu(rows, plan.offs), down, down_scales, plan.offs)
+        mm = mxfp4_grouped_mm_fwd_w4a8_quantized if activations == "fp8" else mxfp4_grouped_mm_fwd_w4a4_quantized
+        rows = mm(*moe_dispatch_quantized(x, plan, activations), gate_up, gate_up_scales, plan.offs)
+        rows = mm(*swiglu_quantized(rows, activations, plan.offs), down, down_scales, plan.offs)
     return moe_combine(rows, weights, plan)

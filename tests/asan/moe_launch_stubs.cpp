@@ -37,6 +37,10 @@ hipError_t launch_swiglu_fwd(const void*, int, int64_t, int64_t, const int32_t*,
                              hipStream_t) {
   return reached();
 }
+hipError_t launch_swiglu_quantized(const void*, int, int64_t, int64_t, const int32_t*, int, uint8_t*, uint8_t*,
+                                   hipStream_t) {
+  return reached();
+}
 hipError_t launch_swiglu_bwd(const void*, const void*, const uint8_t*, const uint8_t*, int, int64_t, int64_t,
                              const int32_t*, void*, hipStream_t) {
   return reached();

@@ -125,12 +125,22 @@ def test_swiglu(L):
     assert call(rows=0) == 0
 
 
+def test_swiglu_quantized(L):
+    call = caller(L.swiglu_quantized, "x t rows inter offs experts fmt codes scales stream",
+                  (A[0], 1, 16, 64, A[1], 8, 1, A[2], A[3], None))
+    assert call(rows=-1) == call(inter=40) == call(experts=0) == SHAPE and call(t=5) == DTYPE
+    assert call(fmt=2) == call(fmt=-1) == FORMAT
+    assert call(x=None) == call(codes=None) == call(scales=None) == NULL and call(offs=A[1] + 1) == ALIGN
+    assert call(codes=A[0] + 32) == call(scales=A[2] + 8) == call(codes=A[1]) == ALIAS
+    assert call(rows=0) == call(inter=0) == 0
+
+
 def test_operators_refuse_cpu_tensors():
     x, e = torch.zeros(2, 64), torch.zeros(2, 1, dtype=torch.int32)
     plan = mxq.MoEPlan(torch.zeros(1, dtype=torch.int32), e, torch.zeros(2, dtype=torch.int32))
     for call in (lambda: mxq.moe_route(x, 1), lambda: mxq.moe_plan(e, 1), lambda: mxq.moe_dispatch(x, plan),
                  lambda: mxq.moe_dispatch_quantized(x, plan, "fp8"), lambda: mxq.moe_combine(x, x, plan),
-                 lambda: mxq.swiglu(x)):
+                 lambda: mxq.swiglu(x), lambda: mxq.swiglu_quantized(x, "fp8")):
         with pytest.raises(ValueError, match="GPU tensors"):
             call()
     with pytest.raises(ValueError):

@@ -102,6 +102,23 @@ def test_swiglu_keeps_what_the_packed_cache_form_keeps():
         assert (codes[R - 2:] == 77).all() and (scales[R - 2:] == 78).all()
 
 
+@pytest.mark.parametrize("R,I", [(1, 32), (5, 96), (64, 2048), (33, 1408), (1000, 64), (2, 32 * 513)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("format", ["fp8", "mxfp4"])
+def test_swiglu_quantized(R, I, dtype, format):
+    """Bit for bit what quantizing swiglu's output gives, rows behind the last expert (which hold NaN) included."""
+    x = values(np.random.default_rng(R + I + 1), (R, 2 * I), dtype, 2.0)
+    x[0] = 0.0
+    for offs in (None, i32([R // 2, max(0, R - 3)])):
+        if offs is not None:
+            x[max(0, R - 3):] = float("nan")
+        codes, scales = mxq.swiglu_quantized(x, format, offs)
+        h = mxq.swiglu(x, offs)
+        want = mxq.quantize_cache_packed(h, "fp8", 32) if format == "fp8" else mxq.quantize_mxfp4(h)
+        assert codes.dtype == want[0].dtype and scales.dtype == want[1].dtype
+        assert torch.equal(codes, want[0]) and torch.equal(scales.view(torch.uint8), want[1].view(torch.uint8))
+
+
 def test_swiglu_holds_what_it_says():
     """With a gradient wanted, the graph keeps 8 bits an element (and a scale per 32), not the input."""
     x = values(np.random.default_rng(4), (4096, 4096), "bf16").requires_grad_(True)
@@ -128,7 +145,8 @@ def test_swiglu_strided_misaligned_and_empty():
 def test_swiglu_refusals():
     x = torch.zeros(4, 128, device=dev())
     for call in (lambda: mxq.swiglu(x[:, :96]), lambda: mxq.swiglu(x, checkpoint="int8"),
-                 lambda: mxq.swiglu(x.view(-1)), lambda: mxq.swiglu(x, torch.zeros(2, dtype=torch.int32))):
+                 lambda: mxq.swiglu(x.view(-1)), lambda: mxq.swiglu(x, torch.zeros(2, dtype=torch.int32)),
+                 lambda: mxq.swiglu_quantized(x[:, :96], "fp8"), lambda: mxq.swiglu_quantized(x, "nvfp4")):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: mxq.swiglu(x.double()), lambda: mxq.swiglu(x, torch.zeros(2, device=dev())),
