@@ -178,7 +178,8 @@ def moe_plan(experts, num_experts, first_expert=0, local_experts=None):
     ``first_expert`` on (default: all ``num_experts``): a stable sort by
     expert.  Every other value, -1 among them, is a slot that is not served."""
     _need_cuda(experts)
-    local = num_experts - first_expert if local_experts is None else local_experts
+    num_experts, first_expert = int(num_experts), int(first_expert)
+    local = num_experts - first_expert if local_experts is None else int(local_experts)
     if experts.dtype != torch.int32:
         raise TypeError("moe_plan: experts must be int32")
     if experts.dim() != 2:
