@@ -213,7 +213,7 @@ __device__ __forceinline__ T wave_all(T v, Op op) {
 template <typename T>
 struct Two {
   T best = -INFINITY, next = -INFINITY;
-  __device__ __forceinline__ void add(T k) {       // a NaN changes nothing
+  __device__ __forceinline__ void add(T k) {       // not NaN
     if constexpr (sizeof(T) == 4) {
       next = __builtin_amdgcn_fmed3f(best, next, k);
       best = fmaxf(best, k);
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   double z = 1.0;
   if (by_logit) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = x[v];           // where x is NaN the key is too, and no comparison takes it
+    for (int v = 0; v < V; ++v) key[v] = x[v];
   }
   if (SIGMOID) {
     if (!by_logit) {
@@ -639,6 +639,9 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       }
     }
   }
+  // A NaN (of a logit or a bias) is no key: the median of three that Two takes is not defined for it.
+#pragma unroll
+  for (int v = 0; v < V; ++v) key[v] = fmaxf(key[v], kNone);
   // fp64 score s of expert e of this token, and its key
   auto key64 = [&](int e, double& s) {
     const float logit = elem_value<DT>(load_bits<DT>(row + e * kElemBytes<DT>));

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_moe_plan_place(const int32_t* 
     s += kPlanThreads;
     expert = s < t1 ? index[s] : -1;
     __syncthreads();
-    for (int i = threadIdx.x; i < nb; i += kPlanThreads) {              // this round's slots lie before the next's
+    for (int i = threadIdx.x; i < nb; i += kPlanThreads) {              // these slots lie before the next 1024
       int c = 0;
       for (int w = 0; w < kPlanWaves; ++w) {
         c += in_wave[w * nb + i];

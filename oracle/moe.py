@@ -73,6 +73,8 @@ def route_grad(logits, experts, grad_weights, score="softmax", renormalize=True,
         s = scores(logits[t], score)
         total = sum(s[e] for _, e in places)
         u = np.zeros(logits.shape[1])
+        if renormalize and total == 0:                    # the weights are 0, whatever the logits do
+            continue
         for j, e in places:
             if renormalize:
                 mean = sum(grad_weights[t, i] * s[f] for i, f in places) / total

@@ -129,6 +129,25 @@ def test_route_masked_and_empty(score):
     check(x, 8, score=score, mask=none)
 
 
+@pytest.mark.parametrize("E,k,kw", [(5, 2, dict()), (60, 5, dict()), (128, 6, dict(groups=8, top_groups=3)), (256, 8, dict()),
+                                    (256, 7, dict(groups=8, top_groups=4)), (384, 5, dict()), (512, 8, dict()),
+                                    (700, 9, dict()), (130, 6, dict(groups=13, top_groups=5)), (96, 20, dict())])
+@pytest.mark.parametrize("share", [0.1, 0.6])
+def test_route_nan_logits_and_biases(E, k, kw, share):
+    """NaN in any place of the logits or the bias closes that expert and disturbs no other."""
+    g = np.random.default_rng(E + k)
+    x = values(g, (70, E), "f32")
+    x[torch.from_numpy(g.random((70, E)) < share).to(dev())] = float("nan")
+    bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+    bias[g.random(E) < 0.2] = np.nan
+    for score in ("softmax", "sigmoid"):
+        for b in (None, bias):
+            want_w, want_e = moe.route(f64(x), k, score, bias=None if b is None else b.astype(np.float64), **kw)
+            w, e = mxq.moe_route(x, k, score=score, bias=None if b is None else torch.from_numpy(b).to(dev()), **kw)
+            assert np.array_equal(e.cpu().numpy(), want_e)
+            assert_rounded(w, want_w, "f32", 4 * U * want_w, "weights")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_far_values(score):
     """Logits far from 0: scores that round to 1 or vanish in fp32 keep their order and their weights."""
