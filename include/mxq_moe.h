@@ -54,7 +54,7 @@ typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score;
  *     top_groups groups of largest value are kept.
  *   The top_k experts of largest key are chosen, in falling order.
  *   weights[t, j] = scale * s_j, divided by the sum of the chosen s with
- *     renormalize (0 where that sum is 0).
+ *     renormalize (0 where sigmoid scores all vanish in fp64, below e^-745).
  * Ties go to the lower group or expert.  Keys are compared as in fp64: where
  * fp32 keys lie too near each other to tell, the token is decided in fp64.
  * An expert whose logit or bias is -inf or NaN is never chosen nor counted in a

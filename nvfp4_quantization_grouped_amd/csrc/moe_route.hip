@@ -127,8 +127,15 @@ __device__ void route_token(const RouteArgs& a, int64_t token, double* key) {
       if (lane == 0) key[at] = -INFINITY;
       wave_sync();
     }
+  float logit = -INFINITY;
+  if (mine >= 0) logit = elem_value<DT>(load_bits<DT>(x + mine * kElemBytes<DT>));
   double s = 0.0;
-  if (mine >= 0) s = score(elem_value<DT>(load_bits<DT>(x + mine * kElemBytes<DT>)));
+  if (!a.sigmoid && a.renormalize) {
+    const float most = wave_max(logit);              // the chosen scores up to a common factor, none vanishing
+    if (mine >= 0) s = exp((double)logit - (double)most);
+  } else if (mine >= 0) {
+    s = score(logit);
+  }
   double w = a.scale * s;
   if (a.renormalize) {
     const double sum = wave_sum(s);
@@ -451,7 +458,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
   const int n = count(cut);
 
   int expert = -1;
-  double s = 0.0, k64 = -INFINITY;
+  double k64 = -INFINITY;
+  float logit = -INFINITY;
   int rank = lane;
   bool chosen = false;
   if (n <= 64) {
@@ -466,8 +474,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
     if (lane < n) {
       const Candidate c = found[wave][lane];
       expert = c.expert;
-      s = score64(c.logit);
-      k64 = by_logit ? (double)c.logit : s + (a.bias ? (double)a.bias[expert] : 0.0);
+      logit = c.logit;
+      k64 = by_logit ? (double)logit : score64(logit) + (a.bias ? (double)a.bias[expert] : 0.0);
       rank = 0;
     }
     for (int o = 0; o < n; ++o) {
@@ -497,10 +505,18 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
       wave_argmax(best, at);
       const int from = __ffsll((unsigned long long)__ballot(own == best && best_e == at && at >= 0)) - 1;
       const float l = lane_value(best_x, from);
-      if (lane == j) { expert = at; s = score64(l); chosen = true; }
+      if (lane == j) { expert = at; logit = l; chosen = true; }
       last = best;
       last_e = at;
     }
+  }
+  double s = 0.0;
+  if (!a.sigmoid && a.renormalize) {
+    // the chosen scores up to a common factor, none vanishing
+    const float most = wave_all(chosen ? logit : -INFINITY, [](float p, float q) { return fmaxf(p, q); });
+    if (chosen) s = exp((double)logit - (double)most);
+  } else if (chosen) {
+    s = score64(logit);
   }
   double w = a.scale * s;
   if (a.renormalize) {
@@ -642,13 +658,17 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   // A NaN (of a logit or a bias) is no key: the median of three that Two takes is not defined for it.
 #pragma unroll
   for (int v = 0; v < V; ++v) key[v] = fmaxf(key[v], kNone);
-  // fp64 score s of expert e of this token, and its key
-  auto key64 = [&](int e, double& s) {
-    const float logit = elem_value<DT>(load_bits<DT>(row + e * kElemBytes<DT>));
+  // fp64 key of expert e of this token, its logit, and its score where the key needs that
+  struct Expert {
+    float logit;
+    double score;
+  };
+  auto key64 = [&](int e, Expert& x) {
+    x.logit = elem_value<DT>(load_bits<DT>(row + e * kElemBytes<DT>));
+    x.score = by_logit ? 0.0 : score64(x.logit);
     const float b = a.bias ? a.bias[e] : 0.0f;
-    s = score64(logit);
-    if (!((int)eligible(logit) & (int)eligible(b))) return (double)-INFINITY;
-    return by_logit ? (double)logit : s + (double)b;
+    if (!((int)eligible(x.logit) & (int)eligible(b))) return (double)-INFINITY;
+    return by_logit ? (double)x.logit : x.score + (double)b;
   };
 
   Two<float> two;
@@ -657,15 +677,15 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   bool kept = true;
   if (a.groups > 1) {
     const int lanes = E / a.groups / V, base = lane & 48;
-    auto keep = [&](auto own, bool& near) {
+    auto keep = [&](auto own_group, bool& near) {
       const int g = l / lanes;
       int rank = 0;
       int close = 0;
-      const float error = 2.0f * row_all(own.error, [](float p, float q) { return fmaxf(p, q); });
+      const float error = 2.0f * row_all(own_group.error, [](float p, float q) { return fmaxf(p, q); });
       for (int o = 0; o < a.groups; ++o) {
-        const auto v = row_lane(own.value, o * lanes);
-        rank += (int)(v > own.value) | ((int)(v == own.value) & (int)(o < g));
-        close |= (int)(o != g) & (int)(v <= own.value) & (int)((float)(own.value - v) <= error);
+        const auto v = row_lane(own_group.value, o * lanes);
+        rank += (int)(v > own_group.value) | ((int)(v == own_group.value) & (int)(o < g));
+        close |= (int)(o != g) & (int)(v <= own_group.value) & (int)((float)(own_group.value - v) <= error);
       }
       near = g < a.groups && rank == a.top_groups - 1 && close;
       return rank < a.top_groups;
@@ -684,7 +704,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       const float least = value.least > kNone ? value.least - 2.0f * key_error(value.least, rz) : INFINITY;
 #pragma unroll 1
       for (uint32_t m = in_reach(key, least); m; m &= m - 1) {
-        double unused;
+        Expert unused;
         t64.add(key64(e0 + __builtin_ctz(m), unused));
       }
       const bool kept64 =
@@ -750,7 +770,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   }
 
   int expert = -1, rank = l;
-  double s = 0.0;
+  Expert own = {kNone, 0.0};
   bool chosen = false;
   {
     const bool fits = n <= 16;
@@ -763,7 +783,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     double k64 = -INFINITY;
     if (fits && l < n) {
       expert = found[wave][lane];
-      k64 = key64(expert, s);
+      k64 = key64(expert, own);
     }
     if (!SIGMOID && __any(!sure)) {
       const float k32 = (float)k64;
@@ -772,7 +792,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
       if (__any(retry)) {
         const double exact = exact_z();
         z = retry ? exact : z;
-        if (retry && fits && l < n) k64 = key64(expert, s);
+        if (retry && fits && l < n) k64 = key64(expert, own);
       }
     }
     // candidates stand in expert order, so equal keys go by lane
@@ -791,22 +811,30 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
     for (int j = 0; j < k; ++j) {
       double best = -INFINITY;
       int best_e = -1;
-      double best_s = 0.0;
+      Expert best_x = {0.0f, 0.0};
 #pragma unroll 1
       for (int v = 0; v < (kept && n > 16 ? mine : 0); ++v) {
-        double sv;
-        const double q = key64(e0 + v, sv);
-        if ((q < last || (q == last && e0 + v > last_e)) && q > best) { best = q; best_e = e0 + v; best_s = sv; }
+        Expert xv;
+        const double q = key64(e0 + v, xv);
+        if ((q < last || (q == last && e0 + v > last_e)) && q > best) { best = q; best_e = e0 + v; best_x = xv; }
       }
       const double all = row_all(best, [](double p, double q) { return p > q ? p : q; });
       const int e = row_all(best == all && best_e >= 0 ? best_e : 0x7FFFFFFF, [](int p, int q) { return min(p, q); });
       const uint64_t who = __ballot(best_e == e);
       const int from = __builtin_ctz(((uint32_t)(who >> (lane & 48)) & 0xFFFFu) | 0x10000u) & 15;
-      const double sv = row_lane(best_s, from);
-      if (n > 16 && l == j) { expert = e; s = sv; chosen = true; }
+      const Expert x = {row_lane(best_x.logit, from), row_lane(best_x.score, from)};
+      if (n > 16 && l == j) { expert = e; own = x; chosen = true; }
       last = all;
       last_e = e;
     }
+  }
+  double s = 0.0;
+  if (!SIGMOID && a.renormalize) {
+    // the chosen scores up to a common factor, none vanishing
+    const float most = row_all(chosen ? own.logit : kNone, [](float p, float q) { return fmaxf(p, q); });
+    if (chosen) s = exp((double)own.logit - (double)most);
+  } else if (chosen) {
+    s = by_logit ? score64(own.logit) : own.score;
   }
   double w = a.scale * s;
   if (a.renormalize) {
@@ -868,13 +896,13 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __res
 #pragma unroll
       for (int v = 0; v < V; ++v) most = fmaxf(most, out[v]);
       top = all(most, larger);
-      float sum = 0.0f;
+      double sum = 0.0;                // in fp64: next to the largest, 1, the others' sum keeps its own accuracy
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         out[v] = out[v] > -INFINITY ? exp_neg(top - out[v]) : 0.0f;
-        sum += out[v];
+        sum += (double)out[v];
       }
-      z = all((double)sum, add);
+      z = all(sum, add);
     }
   }
   if (mine >= 0) s = SIGMOID ? sigmoid_f64((double)x) : exp((double)x - (double)top) / z;

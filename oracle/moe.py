@@ -33,6 +33,15 @@ def scores(x, score):
     return s
 
 
+def chosen_scores(x, s, chosen, score, renormalize):
+    """Scores to renormalize over: a softmax's up to a common factor, so that logits far below the largest of all do
+    not vanish beside it."""
+    if score == "softmax" and renormalize and len(chosen):
+        with np.errstate(over="ignore"):                  # of experts that were not chosen
+            s = np.exp(np.asarray(x, np.float64) - max(x[e] for e in chosen))
+    return s
+
+
 def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=1, group_best=2, renormalize=True, scale=1.0,
           token_mask=None):
     """(weights float64 [T, k], experts int32 [T, k]) of logits [T, E]."""
@@ -55,6 +64,7 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=1, gro
             kept = sorted(value, key=lambda g: (-value[g], g))[:top_groups]
             able = [e for e in able if e // size in kept]
         chosen = sorted(able, key=lambda e: (-key[e], e))[:top_k]
+        s = chosen_scores(logits[t], s, chosen, score, renormalize)
         total = sum(s[e] for e in chosen)
         for j, e in enumerate(chosen):
             experts[t, j] = e
@@ -70,7 +80,7 @@ def route_grad(logits, experts, grad_weights, score="softmax", renormalize=True,
         places = [(j, int(e)) for j, e in enumerate(experts[t]) if 0 <= e < logits.shape[1]]
         if not places:
             continue
-        s = scores(logits[t], score)
+        s = chosen_scores(logits[t], scores(logits[t], score), [e for _, e in places], score, renormalize)
         total = sum(s[e] for _, e in places)
         u = np.zeros(logits.shape[1])
         if renormalize and total == 0:                    # the weights are 0, whatever the logits do
@@ -81,7 +91,7 @@ def route_grad(logits, experts, grad_weights, score="softmax", renormalize=True,
                 u[e] = scale * (grad_weights[t, j] - mean) / total
             else:
                 u[e] = scale * grad_weights[t, j]
-        s0 = np.nan_to_num(s, nan=0.0)
+        s0 = np.where(u != 0, np.nan_to_num(s, nan=0.0), 0.0) if renormalize else np.nan_to_num(s, nan=0.0)
         out[t] = u * s0 * (1 - s0) if score == "sigmoid" else s0 * (u - (u * s0).sum())
     return out
 

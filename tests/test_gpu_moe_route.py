@@ -155,6 +155,31 @@ def test_route_far_values(score):
                       [-300.0, -301.0, -302.0, -303.0, -304.0, -305.0, -306.0, -307.0]], device=dev())
     check(x, 3, score=score, grad=False)
     check(x, 8, score=score, renormalize=False, grad=False)
+    bias = np.array([0, 0, 3, 0, 0, 3, 3, 0], np.float32)        # the choice falls on logits far below the largest
+    check(x, 3, score=score, bias=bias)
+    wide = torch.cat([x, x - 1, x - 2], 1)
+    check(wide, 20, score=score, bias=np.concatenate([bias] * 3))
+    low = torch.full((3, 130), torch.finfo(torch.float16).min, device=dev()).half()
+    low[:, 7] = 0.0
+    check(low, 5, "f16", score=score, bias=(np.arange(130) == 90).astype(np.float32) * 9, groups=13, top_groups=2)
+
+
+def test_route_gradient_of_a_peaked_softmax():
+    """One score near 1: the gradient s (1 - s) of its logit keeps the accuracy of the others' sum.  Exponentials off by
+    4 u, their sum by as much, the products' and the result's roundings: 16 u, relative.  Absolute: z, s and u s are fp64
+    values next to 1, here and in the oracle alike: each of the E - 1 additions in z, the quotient, the product and the
+    difference round by up to 2^-53, on both sides."""
+    x = torch.zeros(30, 60, device=dev())
+    x[:, 11] = torch.linspace(2, 30, 30, device=dev())
+    x.requires_grad_(True)
+    for E in (60, 300):
+        leaf = torch.nn.functional.pad(x.detach(), (0, E - 60)).requires_grad_(True)
+        w, e = mxq.moe_route(leaf, 1, renormalize=False)
+        assert (e == 11).all()
+        g, = torch.autograd.grad(w.sum(), leaf)
+        want = moe.route_grad(f64(leaf), e.cpu().numpy(), np.ones((30, 1)), "softmax", False, 1.0)
+        off = np.abs(f64(g) - want)
+        assert (off <= 16 * U * np.abs(want) + 2 * (E + 2) * 2.0 ** -53).all(), (off / np.abs(want)).max()
 
 
 def many(g, T, E, dtype="f32", distinct=40):
