@@ -41,6 +41,19 @@ __device__ __forceinline__ Spot spot_of(int64_t row0, unsigned first, unsigned i
   return {row0 + d, (int)(at - d * chunks)};
 }
 
+// silu(gate) * up of eight columns in fp32, before its rounding to DT.  The
+// compiler may fold the last product and the rounding to fp16 into one
+// instruction that rounds once, and does it in some places and not in others:
+// kept apart, so that every caller gets the same bits.
+template <int DT>
+__device__ __forceinline__ void silu_mul(const float (&g)[8], const float (&u)[8], float (&o)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    o[k] = g[k] * sigmoid_f32(g[k]) * u[k];
+    if constexpr (DT == DT_F16) asm("" : "+v"(o[k]));
+  }
+}
+
 template <int DT, bool KEEP>
 __global__ void __launch_bounds__(kThreads) k_swiglu_fwd(const uint8_t* __restrict__ gate_up, int64_t rows, int chunks,
                                                          const int32_t* __restrict__ total, uint8_t* __restrict__ h,
@@ -60,8 +73,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_fwd(const uint8_t* __restri
     float g[8], u[8], o[8];
     to_f32<DT>(load8<DT, true>(gate_up, at * 8, 8), g);
     to_f32<DT>(load8<DT, true>(gate_up, (at + chunks) * 8, 8), u);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = g[k] * sigmoid_f32(g[k]) * u[k];
+    silu_mul<DT>(g, u, o);
     store8<DT, true>(h, i * 8, 8, from_f32<DT>(o));
     if constexpr (KEEP) {
       const int kg = ceil_rule_exponent<FMT_FP8>(group_max_u32<4>(amax_bits(g)));
@@ -103,8 +115,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_quantized(const uint8_t* __
       float g[8], u[8];
       to_f32<DT>(load8<DT, true>(gate_up, at * 8, 8), g);
       to_f32<DT>(load8<DT, true>(gate_up, (at + chunks) * 8, 8), u);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = g[k] * sigmoid_f32(g[k]) * u[k];
+      silu_mul<DT>(g, u, o);
       to_f32<DT>(from_f32<DT>(o), o);
     }
     const uint32_t amax = group_max_u32<4>(amax_bits(o));

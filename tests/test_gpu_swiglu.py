@@ -119,6 +119,16 @@ def test_swiglu_quantized(R, I, dtype, format):
         assert torch.equal(codes, want[0]) and torch.equal(scales.view(torch.uint8), want[1].view(torch.uint8))
 
 
+@pytest.mark.parametrize("format", ["fp8", "mxfp4"])
+def test_swiglu_quantized_over_many_values(format):
+    """One rounding of h more or less shows in about one code of ten million: 268 million of them."""
+    x = torch.randn(32768, 2 * 8192, device=dev(), generator=torch.Generator(dev()).manual_seed(7)).mul_(3).half()
+    codes, scales = mxq.swiglu_quantized(x, format)
+    h = mxq.swiglu(x)
+    want = mxq.quantize_cache_packed(h, "fp8", 32) if format == "fp8" else mxq.quantize_mxfp4(h)
+    assert torch.equal(codes, want[0]) and torch.equal(scales.view(torch.uint8), want[1].view(torch.uint8))
+
+
 def test_swiglu_holds_what_it_says():
     """With a gradient wanted, the graph keeps 8 bits an element (and a scale per 32), not the input."""
     x = values(np.random.default_rng(4), (4096, 4096), "bf16").requires_grad_(True)
