@@ -15,7 +15,7 @@
 //   k_moe_route_general  a wave a token with fp64 keys in LDS throughout: any
 //                        group size.
 // 16384 tokens x 256 experts, 8 of 256 in 4 of 8 groups, sigmoid and bias, fp32:
-// 10.1, 23.6 and 55.3 us.  All are bound by instructions, not by the 16.8 MB of
+// 10.2, 23.8 and 50.6 us.  All are bound by instructions, not by the 16.8 MB of
 // logits (3.4 us): some 850 vector instructions for four tokens in the first.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 // instruction serves four tokens in what is done once a token (the fp64 scores
 // of the candidates, their ranks, the groups), which is most of the work.
 // Grouped sigmoid router with a bias, 256 experts, here and wave-wide: 4 tokens
-// 4.6 and 5.1 us, 1024 tokens 5.2 and 5.7, 16384 tokens 10.1 and 23.6, 65536
-// tokens 26 and 81; 512 experts, 16384 tokens 15.3 and 31.7.
+// 4.7 and 5.4 us, 1024 tokens 5.3 and 6.0, 16384 tokens 10.2 and 23.8, 65536
+// tokens 27 and 82; 512 experts, 16384 tokens 15.5 and 31.8.
 
 // Number of set lanes of `m` in this lane's row of 16.
 __device__ __forceinline__ int row_count(uint64_t m) {

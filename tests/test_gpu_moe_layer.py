@@ -87,6 +87,21 @@ def test_layer_forward_and_gradients(T, first, local):
         assert (out[3] == 0).all() and (gl[3] == 0).all() and (gx[3] == 0).all()
 
 
+@pytest.mark.parametrize("activations", ["bf16", "fp8", "mxfp4"])
+@pytest.mark.parametrize("T", [0, 5])
+def test_layer_with_no_row_to_serve(T, activations):
+    """No token, or tokens that go nowhere: zeros, and zero gradients."""
+    (gp, gs), (dp, ds) = (on_gpu(w) for w in layer())
+    x = torch.ones(T, H, dtype=torch.bfloat16, device=dev(), requires_grad=activations == "bf16")
+    w = torch.full((T, K), float("nan"), device=dev(), requires_grad=activations == "bf16")
+    e = torch.full((T, K), -1, dtype=torch.int32, device=dev())
+    out = mxq.mxfp4_moe(x, w, e, gp, gs, dp, ds, activations=activations)
+    assert out.shape == (T, H) and not out.any()
+    if activations == "bf16":
+        gx, gw = torch.autograd.grad(out, (x, w), torch.ones_like(out))
+        assert gx.shape == x.shape and gw.shape == w.shape and not gx.any() and not gw.any()
+
+
 @pytest.mark.parametrize("activations", ["fp8", "mxfp4"])
 def test_layer_with_low_bit_activations(activations):
     """Equal, bit for bit, to the layer put together from dispatch and the products that quantize themselves."""

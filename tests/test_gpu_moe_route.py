@@ -224,6 +224,22 @@ def test_route_many_tokens(T, E, k, kw, score, dtype):
         assert_rounded(w, want, "f32", 4 * U * np.abs(want), "weights")
 
 
+@pytest.mark.parametrize("E,k,kw", [(256, 8, {}), (1000, 24, {}), (300, 6, {"groups": 60, "top_groups": 3})])
+def test_route_past_32_bit_offsets(E, k, kw):
+    """Tokens whose logits lie past 2^31 elements and 2^32 bytes: what the same tokens give alone."""
+    T = 2 ** 31 // E + 70_000
+    x = torch.randn(T, E, device=dev(), dtype=torch.bfloat16, generator=torch.Generator(dev()).manual_seed(9))
+    at = torch.tensor([0, T // 2, T - 70_000, T - 69_999, T - 2, T - 1], device=dev())
+    leaf, few = x.requires_grad_(True), x.detach()[at].requires_grad_(True)
+    w, e = mxq.moe_route(leaf, k, **kw)
+    want_w, want_e = mxq.moe_route(few, k, **kw)
+    assert torch.equal(w[at], want_w) and torch.equal(e[at], want_e)
+    gw = torch.randn(T, k, device=dev())
+    got, = torch.autograd.grad(w, leaf, gw)
+    want, = torch.autograd.grad(want_w, few, gw[at])
+    assert torch.equal(got[at], want)
+
+
 def test_route_strided_and_misaligned_logits():
     g = np.random.default_rng(14)
     base = values(g, (33, 2 * 60 + 1), "bf16")

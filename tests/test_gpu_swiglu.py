@@ -129,6 +129,28 @@ def test_swiglu_quantized_over_many_values(format):
     assert torch.equal(codes, want[0]) and torch.equal(scales.view(torch.uint8), want[1].view(torch.uint8))
 
 
+def test_swiglu_past_32_bit_offsets():
+    """Rows whose element offsets pass 2^31 and whose byte offsets pass 2^32: what the same rows give alone."""
+    R, I = 600_000, 2048
+    x = torch.randn(R, 2 * I, device=dev(), dtype=torch.bfloat16, generator=torch.Generator(dev()).manual_seed(8))
+    offs = i32([R // 2, R - 5])
+    at = torch.tensor([0, 1, 262143, 262144, 524287, 524288, R - 7, R - 6], device=dev())
+    for checkpoint in ("fp8", None):
+        leaf, few = x.detach().requires_grad_(True), x[at].requires_grad_(True)
+        h = mxq.swiglu(leaf, offs, checkpoint)
+        want = mxq.swiglu(few, None, checkpoint)
+        assert torch.equal(h[at], want) and not h[R - 5:].any()
+        go = x[:, :I].contiguous()
+        got, = torch.autograd.grad(h, leaf, go)
+        want, = torch.autograd.grad(want, few, go[at])
+        assert torch.equal(got[at], want) and not got[R - 5:].any()
+        del h, got, leaf
+    for format in ("fp8", "mxfp4"):
+        got, want = mxq.swiglu_quantized(x, format, offs), mxq.swiglu_quantized(x[at], format)
+        assert torch.equal(got[0][at], want[0])
+        assert torch.equal(got[1].view(torch.uint8)[at], want[1].view(torch.uint8))
+
+
 def test_swiglu_holds_what_it_says():
     """With a gradient wanted, the graph keeps 8 bits an element (and a scale per 32), not the input."""
     x = values(np.random.default_rng(4), (4096, 4096), "bf16").requires_grad_(True)
