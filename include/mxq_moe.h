@@ -177,9 +177,9 @@ int moe_combine_bwd(const void* grad_out, const void* y, int t, int64_t tokens, 
  *   s, s = sigmoid(gate), fp32, with gate and up read from codes and scales
  *   (gate_up NULL) or from gate_up (codes and scales NULL).  Rows that do not
  *   count get zeros.
- * Errors: MXQ_ERR_SHAPE (negative sizes, inter % 32 != 0, rows * inter >=
- * 2^40, experts < 1 with offs), MXQ_ERR_DTYPE, MXQ_ERR_NULL, MXQ_ERR_ALIAS,
- * MXQ_ERR_HIP.
+ * Errors: MXQ_ERR_SHAPE (negative sizes, inter % 32 != 0, inter > 2^20, rows *
+ * inter >= 2^40, experts < 1 with offs), MXQ_ERR_DTYPE, MXQ_ERR_NULL,
+ * MXQ_ERR_ALIAS, MXQ_ERR_HIP.
  */
 int swiglu_fwd(const void* gate_up, int t, int64_t rows, int64_t inter, const int32_t* offs, int64_t experts, void* h,
                uint8_t* codes, uint8_t* scales, void* stream);
