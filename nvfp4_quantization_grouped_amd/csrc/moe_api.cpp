@@ -72,7 +72,8 @@ int moe_route(const void* logits, int t, int64_t tokens, int64_t experts, int64_
   if (overlaps_any({weights, tokens * top_k * 4}, in, 3) || overlaps_any({index, tokens * top_k * 4}, in, 4))
     return MXQ_ERR_ALIAS;
   const mxq::RouteArgs a = {logits, bias, token_mask, weights, index, tokens, (int)experts, (int)top_k, (int)groups,
-                            (int)top_groups, group_best, score == MXQ_SCORE_SIGMOID, renormalize != 0, scale};
+                            (int)(experts / groups), (int)top_groups, group_best, score == MXQ_SCORE_SIGMOID,
+                            renormalize != 0, scale};
   return from_hip(mxq::launch_moe_route(a, t, (hipStream_t)stream));
 }
 

@@ -23,7 +23,7 @@ struct RouteArgs {
   float* weights;
   int32_t* index;
   int64_t tokens;
-  int experts, top_k, groups, top_groups, group_best;
+  int experts, top_k, groups, group_size, top_groups, group_best;
   bool sigmoid, renormalize;
   double scale;
 };

@@ -8,8 +8,8 @@
 // every expert that the bound leaves in the running for the top_k (a few more
 // than top_k), and give each candidate a lane, an fp64 key and a rank: the
 // number of candidates before it.  Three kernels, chosen by what fits:
-//   k_moe_route_rows     16 lanes a token: up to 512 experts, 16 places, groups
-//                        of whole lanes (of 4, 8, 16, 24 or 32 experts);
+//   k_moe_route_rows     16 lanes a token: up to 512 experts, 16 places, up to 16
+//                        groups, a group as whole lanes of up to 32 experts;
 //   k_moe_route          a wave a token: up to 1024 experts, 32 places, groups of
 //                        whole lanes (of 1, 2, 4, 8 or 16 experts);
 //   k_moe_route_general  a wave a token with fp64 keys in LDS throughout: any
@@ -298,25 +298,33 @@ __device__ __forceinline__ bool group_kept(const GroupValue<T>& own, int groups,
   return rank < top;
 }
 
-// Logits of experts e0 .. e0 + V - 1 of a row, of which `mine` exist; the others read as -inf.
+// Logits (or biases) of experts e0 .. e0 + V - 1 of a row, of which `mine` exist; the others read as -inf.
 template <int DT, int V>
 __device__ __forceinline__ void load_logits(const uint8_t* row, int e0, int mine, float (&x)[V]) {
+  auto four = [&](int v) {
+    if constexpr (DT == DT_F32) {
+      const u32x4_t w = *reinterpret_cast<const u32x4_any*>(row + (e0 + v) * 4);
+      x[v] = as_f32(w.x); x[v + 1] = as_f32(w.y); x[v + 2] = as_f32(w.z); x[v + 3] = as_f32(w.w);
+    } else {
+      const u32x2_t w = *reinterpret_cast<const u32x2_any*>(row + (e0 + v) * 2);
+      x[v] = elem_value<DT>(w.x & 0xFFFFu); x[v + 1] = elem_value<DT>(w.x >> 16);
+      x[v + 2] = elem_value<DT>(w.y & 0xFFFFu); x[v + 3] = elem_value<DT>(w.y >> 16);
+    }
+  };
   if (V % 4 == 0 && mine == V) {
 #pragma unroll
-    for (int v = 0; v + 3 < V; v += 4) {
-      if constexpr (DT == DT_F32) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_any*>(row + (e0 + v) * 4);
-        x[v] = as_f32(w.x); x[v + 1] = as_f32(w.y); x[v + 2] = as_f32(w.z); x[v + 3] = as_f32(w.w);
-      } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_any*>(row + (e0 + v) * 2);
-        x[v] = elem_value<DT>(w.x & 0xFFFFu); x[v + 1] = elem_value<DT>(w.x >> 16);
-        x[v + 2] = elem_value<DT>(w.y & 0xFFFFu); x[v + 3] = elem_value<DT>(w.y >> 16);
-      }
-    }
-  } else {
+    for (int v = 0; v + 3 < V; v += 4) four(v);
+    return;
+  }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      x[v] = v < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + v) * kElemBytes<DT>)) : -INFINITY;
+  for (int v = 0; v < V; v += 4) {
+    if (V % 4 == 0 && v + 4 <= mine) {
+      four(v);
+    } else {
+#pragma unroll
+      for (int i = v; i < v + 4 && i < V; ++i)
+        x[i] = i < mine ? elem_value<DT>(load_bits<DT>(row + (e0 + i) * kElemBytes<DT>)) : -INFINITY;
+    }
   }
 }
 
@@ -536,7 +544,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
 // of the candidates, their ranks, the groups), which is most of the work.
 // Grouped sigmoid router with a bias, 256 experts, here and wave-wide: 4 tokens
 // 4.7 and 5.4 us, 1024 tokens 5.3 and 6.0, 16384 tokens 10.2 and 23.8, 65536
-// tokens 27 and 82; 512 experts, 16384 tokens 15.5 and 31.8.
+// tokens 25.5 and 82; 512 experts, 16384 tokens 14.8 and 31.8.
 
 // Number of set lanes of `m` in this lane's row of 16.
 __device__ __forceinline__ int row_count(uint64_t m) {
@@ -580,17 +588,23 @@ __device__ __forceinline__ bool row_close(float key, float error) {
   else return (int)(fabsf(dpp_value<0x120 + N>(key) - key) <= error) | (int)row_close<N - 1>(key, error);
 }
 
-// Experts l * V .. l * V + V - 1 in lane l of a token's row; experts <= 16 V,
-// top_k <= 16, a group (if there are groups) is whole lanes.
+// How a token's experts lie in its 16 lanes: `lanes` lanes a group, `each`
+// experts a lane (the last ones of a group fewer), each <= V.
+struct RowLayout {
+  int lanes, each;
+  int inverse;   // l / lanes = l * inverse >> 8 for l < 16
+};
+
 template <int DT, int V, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
+__global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a, RowLayout in) {
   __shared__ int32_t found[kTokens][64];
   __shared__ GroupPairs pairs[kTokens];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, E = a.experts;
   const int64_t token = ((int64_t)blockIdx.x * kTokens + wave) * 4 + (lane >> 4);
   const bool alive = token < a.tokens && (!a.token_mask || a.token_mask[token]);
   const uint8_t* row = (const uint8_t*)a.logits + token * E * kElemBytes<DT>;
-  const int e0 = l * V, mine = alive ? min(V, max(0, E - e0)) : 0;
+  const int g = l * in.inverse >> 8, part = (l - g * in.lanes) * in.each, size = a.group_size;
+  const int e0 = g * size + part, mine = alive && g < a.groups ? min(in.each, max(0, size - part)) : 0;
   constexpr float kNone = -INFINITY, kLowest = -0x1.fffffep+127f;
 
   float x[V], key[V];
@@ -643,16 +657,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   auto score64 = [&](float v) { return SIGMOID ? sigmoid_f64((double)v) : exp((double)v - (double)top) / z; };
   if (!by_logit) {
     if (a.bias) {
-      if (e0 + V <= E) {
+      float b[V];
+      load_logits<DT_F32, V>((const uint8_t*)a.bias, e0, mine, b);
 #pragma unroll
-        for (int v = 0; v < V; v += 4) {
-          const u32x4_t b = *reinterpret_cast<const u32x4_any*>(a.bias + e0 + v);
-          key[v] += as_f32(b.x); key[v + 1] += as_f32(b.y); key[v + 2] += as_f32(b.z); key[v + 3] += as_f32(b.w);
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] += e0 + v < E ? a.bias[e0 + v] : 0.0f;
-      }
+      for (int v = 0; v < V; ++v) key[v] += b[v];
     }
   }
   // A NaN (of a logit or a bias) is no key: the median of three that Two takes is not defined for it.
@@ -676,9 +684,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a) {
   for (int v = 0; v < V; ++v) two.add(key[v]);
   bool kept = true;
   if (a.groups > 1) {
-    const int lanes = E / a.groups / V, base = lane & 48;
+    const int lanes = in.lanes, base = lane & 48;
     auto keep = [&](auto own_group, bool& near) {
-      const int g = l / lanes;
       int rank = 0;
       int close = 0;
       const float error = 2.0f * row_all(own_group.error, [](float p, float q) { return fmaxf(p, q); });
@@ -941,6 +948,32 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_bwd(const uint8_t* __res
 
 }  // namespace
 
+// Keys that a lane of k_moe_route_rows is built for, at least n: 0 if there are none.
+static int row_width(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 24 ? 24 : n <= 32 ? 32 : 0; }
+
+// The layout of a token's experts in 16 lanes, or one of no lanes.  Runs of a
+// whole width, the smallest that holds all experts, where groups are made of
+// those (240 experts in 5 groups, 16384 tokens: 11.2 us, and 13.3 with the other);
+// otherwise every group gets a power of two of lanes, or its share of the 16 if
+// only that holds it, and its experts are dealt out by fours (as they are
+// loaded).  Dealt out so, 160 experts in 8 groups take 9.5 us and wave-wide 23.8
+// (sigmoid; softmax 12.8 and 28.1), 60 in 4 take 7.6 and with fp64 keys
+// throughout 20.9.
+static RowLayout row_layout(int experts, int groups, int size) {
+  const int v = row_width((experts + 15) / 16);
+  int lanes = 16, each = v;
+  if (groups > 16 || v == 0) return {0, 0, 0};
+  if (groups > 1 && size % v == 0) {
+    lanes = size / v;
+  } else if (groups > 1) {
+    while (lanes * groups > 16) lanes /= 2;
+    if (lanes * 32 < size) lanes = 16 / groups;
+    each = ((size + lanes - 1) / lanes + 3) / 4 * 4;
+    if (row_width(each) == 0) return {0, 0, 0};
+  }
+  return {lanes, each, 256 / lanes + 1};
+}
+
 hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   const int64_t blocks = (a.tokens + kTokens - 1) / kTokens;
   if (!launchable(blocks, kThreads)) return hipErrorInvalidValue;
@@ -948,16 +981,16 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   int v = 1;
   while (v * 64 < a.experts) v *= 2;
   const bool whole = a.groups == 1 || (a.experts / a.groups) % v == 0;
-  // 16 lanes a token
-  const int v16 = a.experts <= 64 ? 4 : a.experts <= 128 ? 8 : a.experts <= 256 ? 16 : a.experts <= 384 ? 24 : 32;
-  if (a.experts <= 512 && a.top_k <= 16 && (a.groups == 1 || (a.experts / a.groups) % v16 == 0)) {
+  const RowLayout in = row_layout(a.experts, a.groups, a.group_size);
+  if (in.lanes > 0 && a.top_k <= 16) {
+    const int v16 = row_width(in.each);
     const int64_t grid = (a.tokens + 4 * kTokens - 1) / (4 * kTokens);
-#define LAUNCH(DT, SIGMOID)                                                               \
-  if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a);      \
-  else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
-  else if (v16 == 16) k_moe_route_rows<DT, 16, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
-  else if (v16 == 24) k_moe_route_rows<DT, 24, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a); \
-  else k_moe_route_rows<DT, 32, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a)
+#define LAUNCH(DT, SIGMOID)                                                                    \
+  if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in);        \
+  else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in);   \
+  else if (v16 == 16) k_moe_route_rows<DT, 16, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in); \
+  else if (v16 == 24) k_moe_route_rows<DT, 24, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in); \
+  else k_moe_route_rows<DT, 32, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in)
 #define CALL(DT)                            \
   if (a.sigmoid) { LAUNCH(DT, true); }      \
   else { LAUNCH(DT, false); }

@@ -92,7 +92,8 @@ def test_route_near_ties_are_decided_in_fp64():
 
 GROUPS = [(64, 4, 2, 8, 2), (256, 8, 4, 8, 2), (160, 8, 3, 6, 1), (256, 8, 1, 8, 2), (60, 12, 5, 4, 2), (64, 64, 8, 8, 2),
           (1024, 64, 4, 8, 2), (21, 3, 2, 5, 2), (256, 4, 4, 8, 2), (12, 6, 1, 4, 2), (512, 16, 3, 8, 1), (512, 4, 2, 8, 2), (384, 8, 4, 8, 2), (320, 5, 2, 6, 2),
-          (130, 13, 4, 8, 2), (1000, 8, 3, 8, 2), (130, 13, 2, 32, 1)]
+          (130, 13, 4, 8, 2), (1000, 8, 3, 8, 2), (130, 13, 2, 32, 1), (480, 3, 2, 8, 2), (240, 5, 2, 8, 2), (96, 8, 3, 8, 2),
+          (60, 4, 2, 16, 2), (405, 9, 4, 8, 2), (510, 3, 1, 8, 1), (15, 15, 4, 4, 2), (42, 14, 5, 9, 1), (155, 5, 2, 8, 2)]
 
 
 @pytest.mark.parametrize("E,groups,top_groups,k,best", GROUPS)
@@ -192,7 +193,8 @@ MANY = [(4096, 256, 8, dict(groups=8, top_groups=4)), (5001, 256, 8, dict()), (2
         (2048, 128, 1, dict(groups=4, top_groups=1)), (2049, 17, 3, dict()), (2500, 96, 6, dict(groups=12, top_groups=5)),
         (2500, 240, 8, dict(groups=5, top_groups=2)), (2300, 256, 16, dict(groups=2, top_groups=1, group_best=1)),
         (2100, 384, 8, dict(groups=8, top_groups=3)), (2100, 200, 17, dict()), (2100, 130, 8, dict(groups=13, top_groups=4)),
-        (2100, 512, 8, dict(groups=16, top_groups=5)), (2100, 500, 10, dict())]
+        (2100, 512, 8, dict(groups=16, top_groups=5)), (2100, 500, 10, dict()),
+        (2200, 160, 6, dict(groups=8, top_groups=3, group_best=1)), (2100, 60, 4, dict(groups=4, top_groups=2))]
 
 
 @pytest.mark.parametrize("T,E,k,kw", MANY)
