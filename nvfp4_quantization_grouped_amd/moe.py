@@ -231,7 +231,7 @@ class _MoEDispatch(torch.autograd.Function):
         rows, = ctx.saved_tensors
         g = grad.contiguous()
         (T, k), H = rows.shape, g.shape[1]
-        out = torch.empty(T, H, dtype=g.dtype, device=g.device)
+        out = g.new_empty((T, H))
         _call("moe_dispatch_bwd", g.device, g.data_ptr(), _DT[g.dtype], T, H, k, rows.data_ptr(), out.data_ptr())
         return out, None
 
@@ -299,19 +299,18 @@ class _MoECombine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, rows):
         ctx.save_for_backward(y if ctx.needs_input_grad[1] else None, weights, rows)
-        ctx.kind = y.dtype, y.shape
         return _combine(y, weights, rows)
 
     @staticmethod
     @_first_order
     def backward(ctx, grad):
         y, weights, rows = ctx.saved_tensors
-        dtype, shape = ctx.kind
+        want_y, want_weights, _ = ctx.needs_input_grad
         g = grad.contiguous()
-        (T, k), H = rows.shape, shape[1]
-        gy = torch.empty(shape, dtype=dtype, device=g.device) if ctx.needs_input_grad[0] else None
-        gw = torch.empty_like(weights) if ctx.needs_input_grad[1] else None
-        _call("moe_combine_bwd", g.device, g.data_ptr(), _ptr(y), _DT[dtype], T, H, k, rows.data_ptr(),
+        (T, k), H = rows.shape, g.shape[1]
+        gy = g.new_empty((T * k, H)) if want_y else None
+        gw = torch.empty_like(weights) if want_weights else None
+        _call("moe_combine_bwd", g.device, g.data_ptr(), _ptr(y), _DT[g.dtype], T, H, k, rows.data_ptr(),
               weights.data_ptr(), _ptr(gy), _ptr(gw))
         return gy, gw, None
 
@@ -373,7 +372,7 @@ class _SwiGLU(torch.autograd.Function):
         x, codes, scales, offs = ctx.saved_tensors
         g = grad.contiguous()
         R, I = g.shape
-        out = torch.empty(R, 2 * I, dtype=g.dtype, device=g.device)
+        out = g.new_empty((R, 2 * I))
         _call("swiglu_bwd", g.device, g.data_ptr(), _ptr(x), _ptr(codes), _ptr(scales), _DT[g.dtype], R, I, _ptr(offs),
               0 if offs is None else offs.shape[0], out.data_ptr())
         return out, None, None
