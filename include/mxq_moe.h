@@ -59,9 +59,10 @@ typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score;
  * fp32 keys lie too near each other to tell, the token is decided in fp64.
  * An expert whose logit or bias is -inf or NaN is never chosen nor counted in a
  * group's value; one whose logit is -inf or NaN is not counted in a softmax
- * either.  Softmax logits must be below +inf.  A token
- * with token_mask[t] == 0
- * (uint8 [tokens], NULL = none) chooses none, whatever its logits hold.
+ * either.  A bias of +inf is a key of +inf: such an expert comes before every
+ * other, and a group with one before every group without.  Softmax logits must
+ * be below +inf.  A token with token_mask[t] == 0 (uint8 [tokens], NULL = none)
+ * chooses none, whatever its logits hold.
  * A place without an expert has index -1 and weight 0.
  * Outputs: weights fp32 and index int32, both [tokens, top_k].
  * Errors: MXQ_ERR_SHAPE (tokens < 0, experts not in 1..1024, top_k not in

@@ -170,6 +170,11 @@ constexpr float kUlp = 0x1p-24f;
 constexpr float kScoreError = 12.0f;
 constexpr float kLog2e = 0x1.715476p+0f;
 __device__ __forceinline__ float key_error(float key, float most) { return kUlp * (kScoreError * most + 1.25f * fabsf(key)); }
+// The least fp32 key whose fp64 key may still be as large as that of an fp32 key
+// c.  A key of +inf has no error: only a bias of +inf makes one, in fp64 too.
+__device__ __forceinline__ float reach_of(float c, float most) {
+  return c < INFINITY ? c - 2.0f * key_error(c, most) : c;
+}
 __device__ __forceinline__ float sigmoid_key(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
 }
@@ -274,6 +279,8 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
     wave_sync();
   }
   if (!(t.best > -INFINITY)) return {t.best, 0.0f, t.best};
+  // a key of +inf leaves no doubt about the value: 0 for its error, so that the other groups' places do not hang on it
+  if (!(t.best < INFINITY)) return {t.best, 0.0f, best == 2 && t.next > -INFINITY ? t.next : t.best};
   if (best == 2 && t.next > -INFINITY)       // two keys' errors, and the sum's rounding
     return {t.best + t.next,
             kUlp * (2.0f * kScoreError * most + 2.5f * (fabsf((float)t.best) + fabsf((float)t.next))), t.next};
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
     kept = group_kept(value, a.groups, lanes, a.top_groups, near);
     if (near) {                        // again in fp64, from the keys that can be among a group's largest
       Two<double> t64;
-      const float least = value.least > -INFINITY ? value.least - 2.0f * key_error(value.least, rz) : INFINITY;
+      const float least = value.least > -INFINITY ? reach_of(value.least, rz) : INFINITY;
 #pragma unroll 1
       for (uint32_t m = in_reach(key, least); m; m &= m - 1) {
         float l;
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
         hi = mid;
       }
     }
-    if (!by_logit) cut -= 2.0f * key_error(cut, rz);
+    if (!by_logit) cut = reach_of(cut, rz);
   }
   const int n = count(cut);
 
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a, RowLay
         sure = mine_near;
       }
       Two<double> t64;                 // from the keys that can be among a group's largest
-      const float least = value.least > kNone ? value.least - 2.0f * key_error(value.least, rz) : INFINITY;
+      const float least = value.least > kNone ? reach_of(value.least, rz) : INFINITY;
 #pragma unroll 1
       for (uint32_t m = in_reach(key, least); m; m &= m - 1) {
         Expert unused;
@@ -746,7 +753,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a, RowLay
       else hi = mid;
     }
   }
-  auto slack = [&](float c) { return by_logit || c == kLowest ? c : c - 2.0f * key_error(c, rz); };
+  auto slack = [&](float c) { return by_logit || c == kLowest ? c : reach_of(c, rz); };
   auto row_total = [&](uint32_t m) {
     return row_all(__builtin_popcount(m), [](int p, int q) { return p + q; });
   };
