@@ -169,11 +169,17 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_general(RouteArgs a) {
 constexpr float kUlp = 0x1p-24f;
 constexpr float kScoreError = 12.0f;
 constexpr float kLog2e = 0x1.715476p+0f;
-__device__ __forceinline__ float key_error(float key, float most) { return kUlp * (kScoreError * most + 1.25f * fabsf(key)); }
+constexpr float kLowest = -0x1.fffffep+127f;
+// Finite for every finite key, biases next to the type's lowest value among them.
+__device__ __forceinline__ float key_error(float key, float most) {
+  return kUlp * kScoreError * most + 1.25f * kUlp * fabsf(key);
+}
 // The least fp32 key whose fp64 key may still be as large as that of an fp32 key
-// c.  A key of +inf has no error: only a bias of +inf makes one, in fp64 too.
+// c.  Never below the lowest finite value: -inf stands for an expert that is
+// closed, or for no expert at all, whose logits must not be read.  A key of +inf
+// has no error: only a bias of +inf makes one, in fp64 too.
 __device__ __forceinline__ float reach_of(float c, float most) {
-  return c < INFINITY ? c - 2.0f * key_error(c, most) : c;
+  return c < INFINITY ? fmaxf(c - 2.0f * key_error(c, most), kLowest) : c;
 }
 __device__ __forceinline__ float sigmoid_key(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
@@ -283,7 +289,8 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
   if (!(t.best < INFINITY)) return {t.best, 0.0f, best == 2 && t.next > -INFINITY ? t.next : t.best};
   if (best == 2 && t.next > -INFINITY)       // two keys' errors, and the sum's rounding
     return {t.best + t.next,
-            kUlp * (2.0f * kScoreError * most + 2.5f * (fabsf((float)t.best) + fabsf((float)t.next))), t.next};
+            2.0f * kUlp * kScoreError * most + 2.5f * kUlp * fabsf((float)t.best) + 2.5f * kUlp * fabsf((float)t.next),
+            t.next};
   return {t.best, key_error((float)t.best, most), t.best};
 }
 
@@ -335,7 +342,7 @@ __device__ __forceinline__ void load_logits(const uint8_t* row, int e0, int mine
   }
 }
 
-// The keys at or above c among this lane's, bit v for key v.
+// The keys at or above c (which is not -inf) among this lane's, bit v for key v.
 template <int V>
 __device__ __forceinline__ uint32_t in_reach(const float (&key)[V], float c) {
   uint32_t m = 0;
@@ -446,8 +453,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(RouteArgs a) {
     for (int v = 0; v < V; ++v) n += __popcll(__ballot(key[v] >= at));
     return n;
   };
-  const int able = count(-0x1.fffffep+127f);
-  float cut = -0x1.fffffep+127f;
+  const int able = count(kLowest);
+  float cut = kLowest;
   if (able > a.top_k + 8) {
     float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_route_rows(RouteArgs a, RowLay
   const uint8_t* row = (const uint8_t*)a.logits + token * E * kElemBytes<DT>;
   const int g = l * in.inverse >> 8, part = (l - g * in.lanes) * in.each, size = a.group_size;
   const int e0 = g * size + part, mine = alive && g < a.groups ? min(in.each, max(0, size - part)) : 0;
-  constexpr float kNone = -INFINITY, kLowest = -0x1.fffffep+127f;
+  constexpr float kNone = -INFINITY;
 
   float x[V], key[V];
   load_logits<DT, V>(row, e0, mine, x);
