@@ -242,8 +242,8 @@ struct Two {
   }
 };
 
-// A group's value, a bound on its error where its keys are fp32 ones, and the
-// smallest key in it.
+// A group's value (half of it in fp32: see group_value), a bound on its error
+// where its keys are fp32 ones, and the smallest key in it.
 template <typename T>
 struct GroupValue {
   T value;
@@ -285,13 +285,17 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
     wave_sync();
   }
   if (!(t.best > -INFINITY)) return {t.best, 0.0f, t.best};
+  const bool pair = best == 2 && t.next > -INFINITY;
+  const T least = pair ? t.next : t.best;
   // a key of +inf leaves no doubt about the value: 0 for its error, so that the other groups' places do not hang on it
-  if (!(t.best < INFINITY)) return {t.best, 0.0f, best == 2 && t.next > -INFINITY ? t.next : t.best};
-  if (best == 2 && t.next > -INFINITY)       // two keys' errors, and the sum's rounding
-    return {t.best + t.next,
-            2.0f * kUlp * kScoreError * most + 2.5f * kUlp * fabsf((float)t.best) + 2.5f * kUlp * fabsf((float)t.next),
-            t.next};
-  return {t.best, key_error((float)t.best, most), t.best};
+  if (!(t.best < INFINITY)) return {t.best, 0.0f, least};
+  // The sum of two keys past half of fp32's range would be infinite, and all such groups equal: fp32 values are halved.
+  const T part = sizeof(T) == 4 ? T(0.5) : T(1);
+  // two keys' errors, and the sum's rounding
+  const float error = pair ? 2.0f * kUlp * kScoreError * most + 2.5f * kUlp * fabsf((float)t.best) +
+                                 2.5f * kUlp * fabsf((float)t.next)
+                           : key_error((float)t.best, most);
+  return {pair ? part * t.best + part * t.next : part * t.best, (float)part * error, least};
 }
 
 // Whether this lane's group is among the `top` groups of largest value; near:

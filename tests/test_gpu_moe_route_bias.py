@@ -92,3 +92,24 @@ def test_route_biases_of_the_lowest_values(E, k, kw, score, low):
         bias[which] = low
         check_between_guards(x, k, bias, score, **kw)
         check_between_guards(x, k, bias, score, renormalize=False, **kw)
+
+
+GROUPED = [(256, 8, 8), (160, 6, 8), (60, 4, 4), (256, 20, 8), (1024, 9, 4), (320, 8, 64)]      # experts, places, groups
+
+
+@pytest.mark.parametrize("E,k,groups", GROUPED)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_route_group_values_past_the_range_of_fp32(E, k, groups, score, sign):
+    """Two keys whose sum no fp32 value holds still give their group its place: each group with a bias of its own near
+    either end of the range, some equal, one group without any expert."""
+    g = np.random.default_rng(E + groups)
+    x = values(g, (8, E), "f32", 1.5)
+    size = E // groups
+    x[:, :size] = float("-inf")
+    for top in (1, 2, groups // 2, groups - 1, groups):
+        for steps in (g.permutation(groups), g.integers(0, 3, groups)):
+            bias = np.repeat(sign * (1.8e38 + 1.6e38 * steps / groups), size).astype(np.float32)
+            check_between_guards(x, k, bias, score, groups=groups, top_groups=top)
+            bias[-size:] = 0.5                             # one group of ordinary biases
+            check_between_guards(x, k, bias, score, groups=groups, top_groups=top)
