@@ -10,7 +10,8 @@ PyTorch's caching allocator.  There is no CPU path.
 
 Everything can be captured into a graph, backward passes too; as with any
 operator, a backward is captured with ``torch.autograd.grad``, or with leaves of
-which no eager graph is alive.
+which no eager graph is alive.  Second derivatives and forward-mode derivatives
+are refused.
 
 A layer's pass, as :func:`mxfp4_moe` makes it::
 
@@ -26,6 +27,7 @@ A layer's pass, as :func:`mxfp4_moe` makes it::
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -82,6 +84,16 @@ def _first_order(backward):
     def run(ctx, *grads):
         return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
     return run
+
+
+def _differentiated(*tensors):
+    """Whether autograd has to see a call on these tensors: one wants a gradient, or a forward-mode level is open and one
+    carries a tangent (which the Functions refuse: they have no forward-mode derivative)."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t.requires_grad:
+                return True
+    return forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _float_type(t, name):
@@ -168,7 +180,7 @@ def moe_route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups
         raise ValueError("moe_route: top_k must be between 1 and 32 and no more than the experts")
     args = (logits.contiguous(), top_k, _SCORE[score], bias, int(groups), int(top_groups), int(group_best),
             int(bool(renormalize)), float(scale), token_mask)
-    return _MoERoute.apply(*args) if logits.requires_grad and torch.is_grad_enabled() else _route(*args)
+    return _MoERoute.apply(*args) if _differentiated(logits) else _route(*args)
 
 
 # ------------------------------------------------------------ grouped order
@@ -246,7 +258,7 @@ def moe_dispatch(x, plan):
         raise ValueError("moe_dispatch: x must be [tokens, hidden]")
     rows = _plan_rows(plan.rows, x.shape[0], x.device, "moe_dispatch")
     x = x.contiguous()
-    return _MoEDispatch.apply(x, rows) if x.requires_grad and torch.is_grad_enabled() else _dispatch(x, rows)
+    return _MoEDispatch.apply(x, rows) if _differentiated(x) else _dispatch(x, rows)
 
 
 def _quantized_rows(rows, width, format, device):
@@ -330,7 +342,7 @@ def moe_combine(y, weights, plan):
     if y.dim() != 2 or y.shape[0] != rows.numel():
         raise ValueError("moe_combine: y must be [tokens * top_k, hidden]")
     y, weights = y.contiguous(), weights.contiguous()
-    if (y.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
+    if _differentiated(y, weights):
         return _MoECombine.apply(y, weights, rows)
     return _combine(y, weights, rows)
 
@@ -394,7 +406,7 @@ def swiglu(gate_up, offs=None, checkpoint="fp8"):
     if checkpoint not in ("fp8", None):
         raise ValueError("swiglu: checkpoint must be 'fp8' or None")
     x, offs = _gate_up_args(gate_up, offs, "swiglu")
-    if x.requires_grad and torch.is_grad_enabled():
+    if _differentiated(x):
         return _SwiGLU.apply(x, offs, checkpoint)
     return _swiglu(x, offs, False)[0]
 
@@ -435,7 +447,7 @@ def mxfp4_moe(x, weights, experts, gate_up, gate_up_scales, down, down_scales, *
         raise ValueError("mxfp4_moe: activations must be 'bf16', 'fp8' or 'mxfp4'")
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise TypeError("mxfp4_moe: x must be bfloat16 [tokens, hidden]")
-    if activations != "bf16" and (x.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
+    if activations != "bf16" and _differentiated(x, weights):
         raise ValueError("mxfp4_moe: low-bit activations have no gradient")
     local = gate_up.shape[0]
     plan = moe_plan(experts, first_expert + local if num_experts is None else num_experts, first_expert, local)
