@@ -142,6 +142,16 @@ __device__ __forceinline__ Raw8<DT> zero8() {
   for (int i = 0; i < Raw8<DT>::kWords; ++i) r.w[i] = 0u;
   return r;
 }
+// Elements 0 .. n - 1 (n < 8) become 0.
+template <int DT>
+__device__ __forceinline__ void clear_first(Raw8<DT>& r, int n) {
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) {
+      if constexpr (DT == DT_F32) r.w[i] = 0u;
+      else r.w[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+}
 
 // fp32 bits of the largest magnitude of eight values.
 __device__ __forceinline__ uint32_t amax_bits(const float (&v)[8]) {

@@ -348,6 +348,12 @@ __global__ void __launch_bounds__(kBwdWaves * 64) k_moe_combine_bwd(const uint8_
       float once[8];                   // g where this chunk's columns count for the dots
 #pragma unroll
       for (int i = 0; i < 8; ++i) once[i] = i < at.repeated ? 0.0f : g[i];
+      if constexpr (GW && !NARROW) {
+        if (at.repeated > 0) {         // y's too: 0 times an infinity is no 0
+#pragma unroll
+          for (int u = 0; u < kDeep; ++u) clear_first<DT>(raw[u], at.repeated);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < kDeep; ++u) {
         float v[8];
