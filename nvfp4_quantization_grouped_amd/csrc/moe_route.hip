@@ -993,8 +993,6 @@ static RowLayout row_layout(int experts, int groups, int size) {
 }
 
 hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
-  const int64_t blocks = (a.tokens + kTokens - 1) / kTokens;
-  if (!launchable(blocks, kThreads)) return hipErrorInvalidValue;
   // experts of a lane: enough for 64 lanes, and no group cut inside a lane
   int v = 1;
   while (v * 64 < a.experts) v *= 2;
@@ -1003,6 +1001,7 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
   if (in.lanes > 0 && a.top_k <= 16) {
     const int v16 = row_width(in.each);
     const int64_t grid = (a.tokens + 4 * kTokens - 1) / (4 * kTokens);
+    if (!launchable(grid, kThreads)) return hipErrorInvalidValue;
 #define LAUNCH(DT, SIGMOID)                                                                    \
   if (v16 == 4) k_moe_route_rows<DT, 4, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in);        \
   else if (v16 == 8) k_moe_route_rows<DT, 8, SIGMOID><<<(unsigned)grid, kThreads, 0, st>>>(a, in);   \
@@ -1019,6 +1018,8 @@ hipError_t launch_moe_route(const RouteArgs& a, int dt, hipStream_t st) {
 #undef LAUNCH
     return hipGetLastError();
   }
+  const int64_t blocks = (a.tokens + kTokens - 1) / kTokens;
+  if (!launchable(blocks, kThreads)) return hipErrorInvalidValue;
   const size_t lds = (size_t)kTokens * a.experts * sizeof(double);   // at most 32 KB
 #define CALL(DT)                                                                             \
   if (!whole) k_moe_route_general<DT><<<(unsigned)blocks, kThreads, lds, st>>>(a);           \
