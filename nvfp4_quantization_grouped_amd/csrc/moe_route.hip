@@ -258,7 +258,8 @@ union GroupPairs {
 
 // Value of the group that this lane's experts belong to, the same in every
 // lane of the group: its `best` (1 or 2) largest keys summed.  t: the two
-// largest of this lane's keys; lanes: lanes of a group; lds: the wave's own;
+// largest of this lane's keys; lanes: lanes of a group, 32 at most (there are two
+// groups or more); lds: the wave's own;
 // the token's lanes are those from `base` to `end`; most: the largest score there can be.
 template <typename T>
 __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int best, T* lds, int base, int end,
@@ -271,7 +272,6 @@ __device__ __forceinline__ GroupValue<T> group_value(Two<T> t, int lanes, int be
     if (lanes > 4) meet(dpp_value<0x141>(t.best), dpp_value<0x141>(t.next));
     if (lanes > 8) meet(dpp_value<0x140>(t.best), dpp_value<0x140>(t.next));
     if (lanes > 16) meet(__shfl_xor(t.best, 16), __shfl_xor(t.next, 16));
-    if (lanes > 32) meet(__shfl_xor(t.best, 32), __shfl_xor(t.next, 32));
   } else {
     lds[2 * lane] = t.best;
     lds[2 * lane + 1] = t.next;
