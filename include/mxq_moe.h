@@ -172,7 +172,10 @@ int moe_combine_bwd(const void* grad_out, const void* y, int t, int64_t tokens, 
  * 8 bits: E4M3 codes uint8 [rows, 2 * inter] and one E8M0 scale byte per 32
  * columns, uint8 [rows, 2 * inter / 32], as quantize_cache_packed writes them
  * for fp8 and block_size 32.  Rows that do not count are left as they were.
- * What is kept must be finite, as wherever an operation takes an amax.
+ * An inf or a NaN in gate or up is one in h, and swiglu_bwd's gradients at its
+ * place are inf or NaN too (grad_gate always, grad_up where gate was not
+ * finite); the finite values that share its block of 32 columns are lost to the
+ * block's scale, and their gradients are not those of their values.
  * swiglu_bwd -- grad_gate_up [rows, 2 * inter] of grad_h [rows, inter]:
  *   grad_gate = grad_h * up * s (1 + gate (1 - s)), grad_up = grad_h * gate *
  *   s, s = sigmoid(gate), fp32, with gate and up read from codes and scales

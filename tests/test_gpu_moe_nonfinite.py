@@ -33,3 +33,55 @@ def test_combine_weight_gradient_with_an_infinite_column(H, dtype):
         g[torch.arange(T, device=dev()), at] = bad
         gw, = torch.autograd.grad(mxq.moe_combine(y, w, plan), w, g)
         assert (gw == bad).all(), (gw[:, 0].tolist(), cols)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("checkpoint", ["fp8", None])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_swiglu_overflow_reaches_the_gradients(dtype, checkpoint, bad):
+    """An inf or a NaN in gate or up is one in h and in the gradients at its place, kept in 8 bits or whole (what a loss
+    scaler looks for); other rows, and other blocks of 32 columns, are as without it."""
+    I, R = 96, 40
+    g = np.random.default_rng(1)
+    x = values(g, (R, 2 * I), dtype)
+    gh = values(g, (R, I), dtype)
+    hit = x.clone()
+    cols = g.integers(0, I, R)
+    up = np.arange(R) % 2 == 1
+    put = torch.from_numpy(cols + np.where(up, I, 0)).to(dev())
+    rows = torch.arange(0, R - 4, device=dev())                        # the last four rows stay as they are
+    hit[rows, put[rows]] = bad
+    res = []
+    for t in (x, hit):
+        leaf = t.clone().requires_grad_(True)
+        h = mxq.swiglu(leaf, checkpoint=checkpoint)
+        res.append((h.detach(), torch.autograd.grad(h, leaf, gh)[0]))
+    (h0, g0), (h1, g1) = res
+    at = torch.from_numpy(cols).to(dev())[rows]
+    assert not torch.isfinite(h1[rows, at]).any()
+    assert not torch.isfinite(g1[rows, at]).any()                      # gate's gradient takes both factors
+    gate = torch.from_numpy(~up).to(dev())[rows]
+    assert not torch.isfinite(g1[rows, at + I])[gate].any()            # up's gradient is a multiple of silu(gate)
+    block = torch.zeros(R, I, dtype=torch.bool, device=dev())
+    block.view(R, -1, 32)[rows, at // 32] = True
+    assert torch.equal(h0[~block], h1[~block])
+    both = torch.cat([block, block], 1)
+    assert torch.equal(g0[~both], g1[~both]) and torch.isfinite(g0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_carry_infinities_and_nan(dtype):
+    """Dispatch copies them; combine and the dispatch's gradient pass them on to their token and column alone."""
+    g = np.random.default_rng(2)
+    T, k, H = 6, 2, 21
+    plan = mxq.moe_plan(i32(g.integers(0, 3, (T, k))), 3)
+    x = values(g, (T, H), dtype)
+    x[1, 15], x[2, 20], x[3, 0] = float("inf"), float("nan"), float("-inf")
+    out = mxq.moe_dispatch(x, plan)
+    assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(x[plan.slots.long() // k], 7.0))
+    w = torch.full((T, k), 0.5, device=dev())
+    back = mxq.moe_combine(out, w, plan)
+    assert torch.equal(torch.isfinite(back), torch.isfinite(x)) and back[1, 15] == float("inf") and back[2, 20].isnan()
+    leaf = values(g, (T, H), dtype).requires_grad_(True)
+    gx, = torch.autograd.grad(mxq.moe_dispatch(leaf, plan), leaf, out)
+    assert torch.equal(torch.isfinite(gx), torch.isfinite(x))
