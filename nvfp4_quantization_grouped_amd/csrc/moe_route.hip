@@ -15,8 +15,16 @@
 //   k_moe_route_general  a wave a token with fp64 keys in LDS throughout: any
 //                        group size.
 // 16384 tokens x 256 experts, 8 of 256 in 4 of 8 groups, sigmoid and bias, fp32:
-// 10.2, 23.8 and 50.6 us.  All are bound by instructions, not by the 16.8 MB of
-// logits (3.4 us): some 850 vector instructions for four tokens in the first.
+// 10.2, 23.8 and 50.6 us.  In the first a wave of four tokens runs through some 860
+// vector instructions, most of them waiting for the one before (loads, halvings
+// that count by ballots, the candidates through LDS, fp64 scores, ranks): four
+// tokens alone take 4.6 us, and 65536 take 25.3, 0.31 ns for each one more, where
+// its logits take 0.21 ns at a copy's rate.
+//
+// To close an expert, a bias of -inf costs nothing.  A large finite one (-1e9, the
+// type's lowest) lends its rounding error to the bound that tells groups apart:
+// with a whole group closed so, every token's groups are looked at again in fp64
+// (16384 tokens 21.4 us and 10.0 with -inf; 64 tokens 15.1 and 4.9).
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 

@@ -17,10 +17,11 @@
 // flight.  Rows of the grouped order are read past the caches, and the
 // combine's outputs and gradients written past them (they are top_k times what
 // fits): bf16 [8192, 7168] x top-8, 1.06 GB, combine 203 -> 182 us and 173 with
-// smaller workgroups (6.1 TB/s), its gradient, 2.0 GB, 391 -> 360 us (5.6
-// TB/s).  The dispatch writes through the caches: its last rows are there for
-// whoever reads them next.  Repeated alone it runs 197 us that way and 176 past
-// the caches, but followed by its gradient the two take 371 us against 379.
+// smaller workgroups (6.1 TB/s), its gradient, 2.0 GB, 391 -> 360 us (5.6 TB/s;
+// 381 behind its forward).  The dispatch writes through the caches: its last rows
+// are there for whoever reads them next.  Repeated alone it runs 197 us that way
+// and 176 past the caches, but followed by its gradient the two take 371 us against
+// 379.
 #include "moe_launch.hpp"
 #include "moe_device.hpp"
 
@@ -270,8 +271,13 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch_quantized(const uint8
   }
 }
 
-// WEIGHTED false: weights of 1.  A slot that is not served reads row 0, which
-// the caches hold, and adds nothing of it.
+// WEIGHTED false: weights of 1.  A slot that is not served, and a place past top_k
+// in a round of 8, reads row 0 and adds nothing of it, so that every lane has the
+// same 8 loads in flight.  That is made for top_k of 8 with every expert here; off
+// that the idle loads show: bf16 [8192, 7168], top-1 81 us (its bytes take 29 at 8
+// TB/s), top-4 104 (73), top-8 175 (132), top-9 203 (147), top-8 with a quarter of
+// the experts here 79 (44).  k_moe_combine_bwd loads alike: 117 (44), 198 (132), 360
+// (250), 432 (279), 293 (161).
 template <int DT, bool WEIGHTED, bool NARROW>
 __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const uint8_t* __restrict__ y, int64_t tokens, int64_t hidden,
                                                           int chunks, unsigned segs, int top_k,

@@ -6,7 +6,7 @@
 // each way: forward 185 us (5.9 TB/s), gradient 171 (6.3 TB/s), the two one after
 // the other 334; with the kept codes past the caches too 176, 171 and 349, with
 // every store through them the two take 375.  Without a checkpoint the forward
-// takes 130 us (0.81 GB, 6.2 TB/s).  A lane owns 8 consecutive columns of
+// takes 130-133 us (0.81 GB, 6.2 TB/s).  A lane owns 8 consecutive columns of
 // gate and the same 8 of up, four lanes a block of 32 columns of each, whose
 // largest magnitudes meet by DPP; inter is a multiple of 32, so no block
 // straddles gate and up and every group of four lanes is whole.
