@@ -165,8 +165,9 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const uint8_t* __restri
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float s = sigmoid_f32(g[k]);
-      dg[k] = d[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
-      du[k] = d[k] * g[k] * s;
+      // grad_h last: the factors before it are no larger than gate or up, so that a far gate's s = 0 meets no overflow
+      dg[k] = d[k] * (u[k] * (s * (1.0f + g[k] * (1.0f - s))));
+      du[k] = d[k] * (g[k] * s);
     }
     store8<DT, true>(grad, at * 8, 8, from_f32<DT>(dg));
     store8<DT, true>(grad, (at + chunks) * 8, 8, from_f32<DT>(du));

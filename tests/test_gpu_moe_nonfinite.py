@@ -1,13 +1,15 @@
 """Infinities and NaN in the routed-expert layer's rows: they reach what they
-belong to and nothing else."""
+belong to and nothing else, and finite rows make none."""
 
 import numpy as np
 import pytest
 import torch
 
 import nvfp4_quantization_grouped_amd as mxq
+from oracle import moe
 from tests.gpu_util import dev
-from tests.moe_util import i32, values
+from tests.moe_util import assert_rounded, f64, i32, values
+from tests.test_gpu_swiglu import bound_grad
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +87,26 @@ def test_rows_carry_infinities_and_nan(dtype):
     leaf = values(g, (T, H), dtype).requires_grad_(True)
     gx, = torch.autograd.grad(mxq.moe_dispatch(leaf, plan), leaf, out)
     assert torch.equal(torch.isfinite(gx), torch.isfinite(x))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("checkpoint", ["fp8", None])
+def test_swiglu_gradients_of_far_values_stay_finite(dtype, checkpoint):
+    """A gate far below 0 has a sigmoid of 0: no product of the others is large enough to make its gradients NaN."""
+    far = [-1e38, -2e38, -1e30, -1e20, -200.0, 200.0, 1e20, 1e30]
+    size = [1.0, -1e12, 1e30, -3e37]
+    R, I = len(far) * len(size), 32
+    x, gh = values(np.random.default_rng(3), (R, 2 * I), dtype), values(np.random.default_rng(4), (R, I), dtype)
+    for r in range(R):
+        gate, d = far[r % len(far)], size[r // len(far)]
+        x[r, :I] = gate
+        x[r, I::2] *= 1e30 if gate < 0 else 1.0
+        gh[r] = (gh[r].float().clamp(-2, 2) * (d if gate < 0 else 1e-3)).to(gh.dtype)
+    leaf = x.clone().requires_grad_(True)
+    grad, = torch.autograd.grad(mxq.swiglu(leaf, checkpoint=checkpoint), leaf, gh)
+    at = f64(x) if checkpoint is None else moe.kept(f64(x))
+    want = moe.swiglu_grad(at, f64(gh))
+    assert np.isfinite(want).all() and torch.isfinite(grad).all()
+    for r in range(R):                                       # each row on its own: a bound takes the largest values it sees
+        one = slice(r, r + 1)
+        assert_rounded(grad[one], want[one], dtype, bound_grad(at[one], f64(gh)[one]), "grad")
