@@ -1,8 +1,9 @@
 """MI355X-native block-scaled microscaling quantization and MXFP4 grouped GEMM,
-and the routed-expert layer around it.
+the routed-expert layer around it, and a paged packed KV cache with the
+attention that reads it.
 
 All compute runs in hand-written HIP kernels for gfx950 behind the C ABI in
-``include/mxq.h`` and ``include/mxq_moe.h`` (``libmxq.so``, built by ``python -m
+``include/mxq.h``, ``include/mxq_moe.h`` and ``include/mxq_pages.h`` (``libmxq.so``, built by ``python -m
 nvfp4_quantization_grouped_amd.build``).  This package is the PyTorch-facing
 binding: argument checks, output allocation and the current stream.
 """
@@ -41,6 +42,19 @@ from .moe import (
     swiglu,
     swiglu_quantized,
 )
+from .cache import (
+    PagedCache,
+    PageTable,
+    cache_accept,
+    cache_append,
+    cache_attention,
+    cache_compact,
+    cache_fork,
+    cache_free,
+    cache_reserve,
+    page_table,
+    paged_cache,
+)
 
 __all__ = [
     "LIB_PATH", "EXPORTS", "MxqError", "lib",
@@ -53,4 +67,6 @@ __all__ = [
     "quantize_nvfp4_mse", "validate_offs",
     "MoEPlan", "moe_combine", "moe_dispatch", "moe_dispatch_quantized", "moe_plan", "moe_route", "mxfp4_moe", "swiglu",
     "swiglu_quantized",
+    "PagedCache", "PageTable", "cache_accept", "cache_append", "cache_attention", "cache_compact", "cache_fork",
+    "cache_free", "cache_reserve", "page_table", "paged_cache",
 ]

@@ -1,7 +1,7 @@
 """ctypes loader for libmxq.so, the HIP library behind this package.
 
 Loads the in-tree ``libmxq.so`` and declares the C signatures of
-``include/mxq.h`` and ``include/mxq_moe.h``.  There is no fallback: if the library is missing or cannot
+``include/mxq.h``, ``include/mxq_moe.h`` and ``include/mxq_pages.h``.  There is no fallback: if the library is missing or cannot
 be loaded, using any op raises.
 """
 
@@ -29,8 +29,15 @@ MOE_EXPORTS = (
     "moe_dispatch_quantized", "moe_combine", "moe_combine_bwd", "swiglu_fwd", "swiglu_bwd", "swiglu_quantized",
 )
 
+# include/mxq_pages.h
+CACHE_EXPORTS = (
+    "cache_append", "cache_attention_workspace", "cache_attention", "cache_fork", "cache_reserve_workspace",
+    "cache_reserve", "cache_accept", "cache_compact_workspace", "cache_compact",
+)
+
 _lib = None
 _moe_declared = None
+_cache_declared = None
 
 _vp, _i64, _i32, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
 _f64 = ctypes.c_double
@@ -67,6 +74,27 @@ _MOE_SIGS = {
 }
 
 
+class Cache(ctypes.Structure):
+    """``mxq_cache`` of ``include/mxq_pages.h``."""
+    _fields_ = [("pages", _i64), ("page_size", _i64), ("kv_heads", _i64), ("head_dim", _i64), ("fmt", _i32),
+                ("block", _i32), ("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp)]
+
+
+_cp = ctypes.POINTER(Cache)
+_CACHE_SIGS = {
+    "cache_append": ([_cp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _int, _i64, _vp, _vp], _int),
+    "cache_attention_workspace": ([_cp, _i64, _i64, _int, _i64, _i64], _i64),
+    "cache_attention": ([_cp, _vp, _i64, _i64, _vp, _vp, _int, _i64, _i64, _vp, _int, _vp, _f64, _vp, _vp, _vp, _i64,
+                         _vp], _int),
+    "cache_fork": ([_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp], _int),
+    "cache_reserve_workspace": ([_i64, _i64, _i64], _i64),
+    "cache_reserve": ([_cp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "cache_accept": ([_cp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp], _int),
+    "cache_compact_workspace": ([_i64], _i64),
+    "cache_compact": ([_cp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+}
+
+
 class MxqError(RuntimeError):
     """A libmxq entry point returned a non-zero status."""
 
@@ -99,6 +127,19 @@ def moe_lib():
             f.restype = res
         _moe_declared = l
     return _moe_declared
+
+
+def cache_lib():
+    """The loaded library with the entry points of ``include/mxq_pages.h`` declared too."""
+    global _cache_declared
+    if _cache_declared is None:
+        l = lib()
+        for name, (args, res) in _CACHE_SIGS.items():
+            f = getattr(l, name)
+            f.argtypes = args
+            f.restype = res
+        _cache_declared = l
+    return _cache_declared
 
 
 def check(status, fn):

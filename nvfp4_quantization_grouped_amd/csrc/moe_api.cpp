@@ -3,41 +3,16 @@
 // allocation, no sync.
 #include "../../include/mxq.h"
 #include "../../include/mxq_moe.h"
+#include "abi_checks.hpp"
 #include "moe_launch.hpp"
 
 namespace {
 
-// A buffer of a call: where it starts and how many bytes it holds.
-struct Span {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
-  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && pa < pb + (uintptr_t)b.bytes && pb < pa + (uintptr_t)a.bytes;
-}
-// Does the output `out` overlap any of the `n` others?
-bool overlaps_any(const Span& out, const Span* others, int n) {
-  for (int i = 0; i < n; ++i)
-    if (overlap(out, others[i])) return true;
-  return false;
-}
-
-bool dtype_ok(int t) { return t == MXQ_F32 || t == MXQ_BF16 || t == MXQ_F16; }
-int64_t dtype_bytes(int t) { return t == MXQ_F32 ? 4 : 2; }
-bool misaligned4(const void* p) { return ((uintptr_t)p & 3) != 0; }
-int from_hip(hipError_t e) { return e == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
+using namespace mxq;
 
 constexpr int64_t kMaxSlots = (int64_t(1) << 31) - (1 << 16);   // rows, and a workgroup past them, fit int32
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-
-// a * b for a, b >= 0, or -1 when it reaches `limit`.
-int64_t product_below(int64_t a, int64_t b, int64_t limit) {
-  if (a == 0 || b == 0) return 0;
-  return a > (limit - 1) / b ? -1 : a * b;
-}
 
 int route_shape(int64_t tokens, int64_t experts, int64_t top_k) {
   if (tokens < 0 || experts < 1 || experts > mxq::kMaxExperts || top_k < 1 || top_k > mxq::kMaxTopK || top_k > experts)
