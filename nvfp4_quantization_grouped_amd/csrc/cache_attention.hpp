@@ -1,0 +1,805 @@
+// cache_attention: attention of new tokens over the packed, paged cache.  The
+// kernels; csrc/cache_attention_<format>_<type>.hip instantiate them.
+//
+// Mathematics.  Rows are the (token, head) pairs of one sequence that share a kv
+// head, 16 to a tile and MT tiles to a wave.  A wave takes 32 positions at a
+// time, transposed so that nothing changes lanes between the products:
+//   S^T [32 positions, rows] = K Q^T          (16x16x32 bf16 MFMA, K decoded in registers)
+//   P^T = exp2(S^T * scale * log2(e) - m)
+//   O^T [channels, rows]   += V^T P^T
+// A lane holds four positions of one row of each 16 x 16 tile of S^T, which are
+// exactly the k slots that it feeds as P^T; the order of positions within the
+// sum is free, so V^T takes the same.  The order of channels within K Q^T is
+// free too: a lane's 8 channels of a step are chosen so that a lane loads 16
+// consecutive bytes.  V is decoded two channels at a time for 8 positions and
+// turned by v_perm.  There is no LDS traffic until the four waves' sums join.
+//
+// Softmax.  m is a row's running maximum in units of log2, moved only when a
+// score exceeds it by 2^8 (probabilities stay below 2^8 relative to it, which
+// fp32 and bf16 hold as well as 1), so that most tiles neither exchange maxima
+// nor rescale sums.  Sums are fp32.
+//
+// Roundings.  Codes times scales have at most 6 significant bits and are exact
+// in bf16.  q of fp16 / fp32 enters as 2 / 3 bf16 parts (exact but for what
+// lies 2^-24 below), probabilities as 2 parts (3 for fp32 outputs): one part
+// alone, 2^-8 of each probability, would double the error that rounding the
+// output to bf16 makes.
+#pragma once
+
+#include <type_traits>
+#include <utility>
+
+#include "cache_device.hpp"
+
+namespace mxq {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+
+constexpr int kAttnThreads = 256;
+constexpr int kTile = 32;                    // positions of a wave's tile
+constexpr int kStep = 4 * kTile;             // of a workgroup's step
+constexpr float kLazy = 8.0f;                // log2 units that a score may exceed the running maximum by
+
+struct AttnDims {
+  int sequences, tokens, heads, group, kv_heads, width, page_shift;
+  int row_tiles;        // tiles of 16 * MT rows of a sequence and kv head, all tokens counted
+  int workgroups;       // that share the steps (split), or 0: one workgroup for each problem
+  bool mask_each;
+  int64_t pages;
+  float scale;          // its size, times log2(e)
+  bool negative;        // its sign, which q takes
+};
+struct AttnArgs {
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int32_t *table, *lengths, *counts;
+  const uint8_t *q, *mask;
+  uint8_t* out;
+  float* lse;
+  float* parts;         // two slots for each workgroup: sums [rows][D], then m and l [rows]
+  int block_shift;
+  AttnDims d;
+};
+
+// ------------------------------------------------------------------- shapes
+template <int DT>
+constexpr int kQParts = DT == DT_BF16 ? 1 : DT == DT_F16 ? 2 : 3;
+template <int DT>
+constexpr int kPParts = DT == DT_F32 ? 3 : 2;
+
+template <int FMT, int D>
+struct Shape {
+  static constexpr bool kFp8 = FMT == FMT_FP8;
+  static constexpr int kRowBytes = kFp8 ? D : D / 2;
+  // K: a lane takes KC channels of a unit; four lanes' channels are neighbours
+  static constexpr int KC = kFp8 ? 16 : (D >= 128 ? 32 : 16);
+  static constexpr int KU = D / (4 * KC);                   // units of a row
+  static constexpr int KW = kFp8 ? KC / 4 : KC / 8;         // words of a unit
+  static constexpr int KS = KC / 16;                        // scale bytes of a unit
+  static constexpr int kHalves = KC / 8;                    // MFMA steps of a unit
+  static constexpr int kSteps = D / 32;
+  // V: a lane takes VC channels of a unit; 16 lanes' channels are neighbours
+  static constexpr int VC = D / 16 > 16 && kFp8 ? 16 : D / 16;
+  static constexpr int VU = D / 16 / VC;
+  static constexpr int VB = kFp8 ? VC : VC / 2;             // bytes of a unit
+  static constexpr int VW = VB < 4 ? 1 : VB / 4;
+  static constexpr int VS = VC > 16 ? 2 : 1;                // scale bytes of a unit
+};
+
+template <int N, class F, int... I>
+__device__ __forceinline__ void static_for_(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+// Channels 2 I and 2 I + 1 of a unit's words as a pair of bf16.
+template <int FMT, int I>
+__device__ __forceinline__ uint32_t decode_pair(const uint32_t* w, float s) {
+  if constexpr (FMT == FMT_FP8) return dec_fp8_bf16x2<(I & 1) != 0>(w[I / 2], s);
+  else return dec_fp4_bf16x2<I & 3>(w[I / 4], s);
+}
+// The same for a scale with mantissa bits (nvfp4): the conversion uses the exponent alone.
+template <int FMT, int I>
+__device__ __forceinline__ uint32_t decode_pair_exact(const uint32_t* w, float s) {
+  const uint32_t v = decode_pair<FMT, I>(w, 1.0f);
+  return elem_bits<DT_BF16>(bf16_lo(v) * s) | elem_bits<DT_BF16>(bf16_hi(v) * s) << 16;
+}
+__device__ __forceinline__ bool has_mantissa(float s) { return (as_u32(s) & 0x7FFFFFu) != 0; }
+
+__device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8_t, u32x4_t{a, b, c, d});
+}
+__device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return elem_bits<DT_BF16>(a) | elem_bits<DT_BF16>(b) << 16;
+}
+// The next bf16 part of eight values, which keep what is left.
+__device__ __forceinline__ bf16x8_t take_part(float (&x)[8], bool last) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    if (!last) {
+      x[2 * i] -= bf16_lo(w[i]);
+      x[2 * i + 1] -= bf16_hi(w[i]);
+    }
+  }
+  return as_bf16x8(w[0], w[1], w[2], w[3]);
+}
+// Over the four lanes that hold a row (16 apart).
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// --------------------------------------------------------------- the schedule
+// A problem is a sequence, a kv head and a tile of rows; its work is its steps of kStep positions.
+struct Work {
+  int known, end, count;     // cached positions, those and the drafted ones, tokens that are no padding
+  int steps, tiles;          // of each problem; row tiles that hold such a token
+};
+__device__ __forceinline__ Work work_of(const AttnArgs& a, int b, int rows) {
+  Work w;
+  w.known = cached_positions(a.lengths[b], a.d.width, 1 << a.d.page_shift);
+  w.count = a.counts ? min(max(a.counts[b], 0), a.d.tokens) : a.d.tokens;
+  w.end = w.count > 0 ? min(w.known + w.count, a.d.width << a.d.page_shift) : 0;
+  w.steps = (w.end + kStep - 1) / kStep;
+  w.tiles = (w.count * a.d.group + rows - 1) / rows;
+  return w;
+}
+// Steps [first, last) of all problems' that workgroup w of g takes.
+__device__ __forceinline__ int share_of(int w, int total, int g) { return (int)((int64_t)w * total / g); }
+// The workgroup that takes step u.
+__device__ __forceinline__ int owner_of(int u, int total, int g) { return (int)((((int64_t)u + 1) * g - 1) / total); }
+
+template <int MT, int D>
+constexpr int kSlotFloats = 16 * MT * (D + 2);
+
+// ------------------------------------------------------------------ one piece
+template <int DT, int FMT, int D, int MT>
+struct Attention {
+  using S = Shape<FMT, D>;
+  static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kRows = 16 * MT;
+  static constexpr int kTilesV = D / 16;
+  // q's fragments stay in registers up to 64 of them, else in LDS
+  static constexpr bool kQInRegs = D * QP * MT <= 512;
+  static constexpr int kPad = D + 4;
+  static constexpr int kQBytes = kQInRegs ? 0 : QP * kRows * D * 2;
+  static constexpr int kSumBytes = 4 * kRows * kPad * 4;
+  static constexpr int kLdsBytes = kQBytes > kSumBytes ? kQBytes : kSumBytes;
+
+  struct Shared {
+    __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
+    float m[4][kRows], l[4][kRows];
+    int first[kAttnThreads + 1];                           // prefix sums of the schedule
+    int sums[4];
+  };
+
+  const AttnArgs& a;
+  Shared& sm;
+  const int lane, wave, col, quarter;
+  // the problem
+  int b, kv, tile;
+  Work w;
+
+  __device__ Attention(const AttnArgs& args, Shared& shared)
+      : a(args), sm(shared), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+        col(threadIdx.x & 15), quarter((threadIdx.x & 63) >> 4) {}
+
+  // Element offset of row r of the problem in q and out; r < tokens * group.
+  __device__ int64_t row_at(int r) const {
+    const int i = r / a.d.group, g = r - i * a.d.group;
+    return (((int64_t)b * a.d.tokens + i) * a.d.heads + kv * a.d.group + g);
+  }
+  __device__ int row_of(int mt) const { return tile * kRows + mt * 16 + col; }
+
+  // ----- q
+  __device__ void q_fragment(int mt, int step, bf16x8_t (&part)[QP]) const {
+    const int u = step / S::kHalves, h = step % S::kHalves;
+    const int ch = u * 4 * S::KC + quarter * S::KC + h * 8, r = row_of(mt);
+    float x[8] = {};
+    if (r < a.d.tokens * a.d.group) to_f32<DT>(load8<DT>(a.q, row_at(r) * D + ch, 8), x);
+    if (a.d.negative)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = -x[i];
+#pragma unroll
+    for (int p = 0; p < QP; ++p) part[p] = take_part(x, p == QP - 1);
+  }
+  struct Q {
+    bf16x8_t f[kQInRegs ? MT : 1][kQInRegs ? S::kSteps : 1][QP];
+  };
+  __device__ void load_q(Q& q) const {
+    if constexpr (kQInRegs) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) q_fragment(mt, s, q.f[mt][s]);
+    } else {
+      for (int i = wave; i < MT * S::kSteps; i += 4) {
+        bf16x8_t part[QP];
+        q_fragment(i / S::kSteps, i % S::kSteps, part);
+#pragma unroll
+        for (int p = 0; p < QP; ++p)
+          *reinterpret_cast<bf16x8_t*>(sm.big + (((i * QP + p) * 64) + lane) * 16) = part[p];
+      }
+      __syncthreads();
+    }
+  }
+  __device__ bf16x8_t q_part(const Q& q, int mt, int step, int p) const {
+    if constexpr (kQInRegs) return q.f[mt][step][p];
+    else
+      return *reinterpret_cast<const bf16x8_t*>(sm.big + ((((mt * S::kSteps + step) * QP + p) * 64) + lane) * 16);
+  }
+
+  // ----- rows of a tile
+  struct Pages {
+    int page[2];        // of the tile's halves of 16 positions; 0 where there is none
+    bool there[2];
+  };
+  __device__ Pages pages_of(int t) const {
+    Pages p;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int slot = (t * kTile + h * 16) >> a.d.page_shift;
+      int page = -1;
+      if (slot < a.d.width) page = a.table[(int64_t)b * a.d.width + slot];
+      page = __builtin_amdgcn_readfirstlane(page);
+      p.there[h] = (uint32_t)page < (uint32_t)a.d.pages;
+      p.page[h] = p.there[h] ? page : 0;
+    }
+    return p;
+  }
+  // Row in the pools of the first position of half h of tile t.
+  __device__ int64_t pool_row(const Pages& p, int t, int h) const {
+    const int in_page = (t * kTile + h * 16) & ((1 << a.d.page_shift) - 1);
+    return (((int64_t)p.page[h] * a.d.kv_heads + kv) << a.d.page_shift) + in_page;
+  }
+  struct K {
+    uint32_t w[2][S::KU][S::KW];
+    uint32_t s[2][S::KU][S::KS];
+  };
+  struct V {
+    uint32_t w[8][S::VU][S::VW];
+    uint32_t s[8][S::VU][S::VS];
+  };
+  __device__ void load_k(K& k, const Pages& p, int t) const {
+    const int blocks = D >> a.block_shift;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t row = pool_row(p, t, h);
+      const uint8_t* codes = a.k_codes + row * S::kRowBytes;
+      const uint8_t* scales = a.k_scales + row * blocks;
+#pragma unroll
+      for (int u = 0; u < S::KU; ++u) {
+        const uint8_t* at = codes + col * S::kRowBytes + (u * 4 + quarter) * S::KW * 4;
+        if constexpr (S::KW == 4) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at);
+          k.w[h][u][0] = v.x; k.w[h][u][1] = v.y; k.w[h][u][2] = v.z; k.w[h][u][3] = v.w;
+        } else {
+          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at);
+          k.w[h][u][0] = v.x; k.w[h][u][1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < S::KS; ++i)
+          k.s[h][u][i] = scales[col * blocks + (((u * 4 + quarter) * S::KC + i * 16) >> a.block_shift)];
+      }
+    }
+  }
+  __device__ void load_v(V& v, const Pages& p, int t) const {
+    const int blocks = D >> a.block_shift;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t row = pool_row(p, t, j / 4);
+      const uint8_t* codes = a.v_codes + row * S::kRowBytes;
+      const uint8_t* scales = a.v_scales + row * blocks;
+      const int r = quarter * 4 + j % 4;
+#pragma unroll
+      for (int u = 0; u < S::VU; ++u) {
+        const uint8_t* at = codes + r * S::kRowBytes + u * 16 * S::VB + col * S::VB;
+        if constexpr (S::VB == 2) v.w[j][u][0] = *reinterpret_cast<const uint16_t*>(at);
+        else if constexpr (S::VB == 4) v.w[j][u][0] = *reinterpret_cast<const uint32_t*>(at);
+        else if constexpr (S::VB == 8) {
+          const u32x2_t x = *reinterpret_cast<const u32x2_t*>(at);
+          v.w[j][u][0] = x.x; v.w[j][u][1] = x.y;
+        } else {
+          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(at);
+          v.w[j][u][0] = x.x; v.w[j][u][1] = x.y; v.w[j][u][2] = x.z; v.w[j][u][3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < S::VS; ++i)
+          v.s[j][u][i] = scales[r * blocks + ((u * 16 * S::VC + col * S::VC + i * 16) >> a.block_shift)];
+      }
+    }
+  }
+
+  // ----- products
+  template <bool EXACT>
+  __device__ void scores(const K& k, const Q& q, f32x4_t (&s)[MT][2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      static_for<S::KU>([&](auto U) {
+        constexpr int u = decltype(U)::value;
+        float sc[S::KS];
+#pragma unroll
+        for (int i = 0; i < S::KS; ++i) sc[i] = scale_value<FMT>(k.s[h][u][i]);
+        static_for<S::kHalves>([&](auto H) {
+          constexpr int hf = decltype(H)::value;
+          uint32_t x[4];
+          static_for<4>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            const float f = sc[hf * 8 / 16 < S::KS ? hf * 8 / 16 : 0];
+            x[i] = EXACT ? decode_pair_exact<FMT, hf * 4 + i>(k.w[h][u], f) : decode_pair<FMT, hf * 4 + i>(k.w[h][u], f);
+          });
+          const bf16x8_t key = as_bf16x8(x[0], x[1], x[2], x[3]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int p = 0; p < QP; ++p)
+              s[mt][h] = mfma(key, q_part(q, mt, u * S::kHalves + hf, p), s[mt][h]);
+        });
+      });
+    }
+  }
+  // O^T += V^T P^T.  CAREFUL: scales with mantissa bits, and values that are not finite, which count only for the rows
+  // that attend to them (`seen`: bf16 ones for those, in the probabilities' places).
+  template <bool CAREFUL>
+  __device__ void values(const V& v, const bf16x8_t (&p)[MT][PP], const bf16x8_t (&seen)[MT], f32x4_t (&o)[MT][kTilesV]) const {
+    static_for<S::VU>([&](auto U) {
+      constexpr int u = decltype(U)::value;
+      float sc[8][S::VS];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < S::VS; ++i) sc[j][i] = scale_value<FMT>(v.s[j][u][i]);
+      static_for<S::VC / 2>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float f = sc[j][i / 8 < S::VS ? i / 8 : 0];
+          x[j] = CAREFUL && FMT == FMT_NVFP4 ? decode_pair_exact<FMT, i>(v.w[j][u], f) : decode_pair<FMT, i>(v.w[j][u], f);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t pick = half ? 0x07060302u : 0x05040100u;
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], pick);
+          const int t = u * S::VC + 2 * i + half;
+          uint32_t odd[4] = {0u, 0u, 0u, 0u};
+          bool any = false;
+          if constexpr (CAREFUL) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((y[j] & 0x7F80u) == 0x7F80u) odd[j] |= 0x3F80u;
+              if ((y[j] & 0x7F800000u) == 0x7F800000u) odd[j] |= 0x3F800000u;
+              if (odd[j] & 0x3F80u) y[j] &= 0xFFFF0000u;
+              if (odd[j] & 0x3F800000u) y[j] &= 0xFFFFu;
+            }
+            any = __ballot((odd[0] | odd[1] | odd[2] | odd[3]) != 0) != 0;
+          }
+          const bf16x8_t val = as_bf16x8(y[0], y[1], y[2], y[3]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int part = 0; part < PP; ++part) o[mt][t] = mfma(val, p[mt][part], o[mt][t]);
+            if (CAREFUL && any) {
+              const f32x4_t met = mfma(as_bf16x8(odd[0], odd[1], odd[2], odd[3]), seen[mt], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (met[r] > 0.0f) o[mt][t][r] = __builtin_nanf("");
+            }
+          }
+        }
+      });
+    });
+  }
+
+  // Steps [first, last) of the problem, this wave's tile of each; `whole`: they are all, else the sums go to `slot`.
+  __device__ void piece(int first, int last, bool whole, float* slot) {
+    Q q;
+    load_q(q);
+    f32x4_t o[MT][kTilesV];
+    float m[MT], sub[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int t = 0; t < kTilesV; ++t) o[mt][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      m[mt] = -__builtin_inff();
+      sub[mt] = l[mt] = 0.0f;
+    }
+    int t = first * 4 + wave;
+    const int end = min(last * 4, (w.end + kTile - 1) / kTile);
+    if (t < end) {
+      Pages now = pages_of(t), next = pages_of(t + 4);
+      K k;
+      V v;
+      load_k(k, now, t);
+      load_v(v, now, t);
+      for (; t < end; t += 4) {
+        f32x4_t s[MT][2];
+        bool exact = false;
+        if constexpr (FMT == FMT_NVFP4) {
+          bool odd = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int u = 0; u < S::KU; ++u)
+#pragma unroll
+              for (int i = 0; i < S::KS; ++i) odd |= has_mantissa(scale_value<FMT>(k.s[h][u][i]));
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+              for (int i = 0; i < S::VS; ++i) odd |= has_mantissa(scale_value<FMT>(v.s[j][u][i]));
+          exact = __ballot(odd) != 0;
+        }
+        if (FMT == FMT_NVFP4 && exact) scores<FMT == FMT_NVFP4>(k, q, s);
+        else scores<false>(k, q, s);
+        const bool more = t + 4 < end;
+        const Pages after = pages_of(min(t + 8, a.d.width << a.d.page_shift >> 5));
+        if (more) load_k(k, next, t + 4);
+        // positions that not every row attends to
+        const bool plain = now.there[0] && now.there[1] && (t + 1) * kTile <= w.known;
+        bf16x8_t p[MT][PP], seen[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float x[8];
+          uint32_t may = 0xFF;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = s[mt][i / 4][i % 4];
+          if (!plain) {
+            const int token = row_of(mt) / a.d.group;
+            may = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int pos = t * kTile + (i / 4) * 16 + quarter * 4 + i % 4, j = pos - w.known;
+              bool ok = now.there[i / 4] && pos < w.end && token < w.count;
+              if (ok && j >= 0)
+                ok = a.mask ? a.mask[((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens + token) * a.d.tokens + j] != 0
+                            : j <= token;
+              may |= (uint32_t)ok << i;
+              if (!ok) x[i] = -__builtin_inff();
+            }
+            uint32_t one[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              one[i] = (may >> (2 * i) & 1 ? 0x3F80u : 0u) | (may >> (2 * i + 1) & 1 ? 0x3F800000u : 0u);
+            seen[mt] = as_bf16x8(one[0], one[1], one[2], one[3]);
+          }
+          float top = x[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+          top *= a.d.scale;
+          if (__ballot(top > m[mt] + kLazy) != 0) {
+            const float to = fmaxf(m[mt], row_max(top));
+            const float keep = m[mt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[mt] - to);
+            m[mt] = to;
+            sub[mt] = to == -__builtin_inff() ? 0.0f : to;
+            l[mt] *= keep;
+#pragma unroll
+            for (int c = 0; c < kTilesV; ++c) o[mt][c] *= keep;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.d.scale, -sub[mt]));
+          if (!plain) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = may >> i & 1 ? x[i] : 0.0f;     // -inf times a scale of 0 is NaN
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l[mt] += x[i];
+#pragma unroll
+          for (int part = 0; part < PP; ++part) p[mt][part] = take_part(x, part == PP - 1);
+        }
+        if (plain && !exact) {
+          values<false>(v, p, seen, o);
+        } else {
+          if (plain) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) seen[mt] = as_bf16x8(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+          } else {
+            // rows that are no position: zeros
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
+              if (!now.there[j / 4] || pos >= w.end) {
+#pragma unroll
+                for (int u = 0; u < S::VU; ++u) {
+#pragma unroll
+                  for (int i = 0; i < S::VW; ++i) v.w[j][u][i] = 0u;
+#pragma unroll
+                  for (int i = 0; i < S::VS; ++i) v.s[j][u][i] = FMT == FMT_NVFP4 ? 0x38 : 127;
+                }
+              }
+            }
+          }
+          values<true>(v, p, seen, o);
+        }
+        if (more) load_v(v, next, t + 4);
+        now = next;
+        next = after;
+      }
+    }
+    join(o, m, l, whole, slot);
+  }
+
+  // The four waves' sums joined: written as outputs, or as a part of them.
+  __device__ void join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
+    __syncthreads();      // q's fragments, and the last piece's sums, have been read
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      l[mt] = row_sum(l[mt]);
+      if (quarter == 0) {
+        sm.m[wave][mt * 16 + col] = m[mt];
+        sm.l[wave][mt * 16 + col] = l[mt];
+      }
+    }
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(sm.big);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 16 + col;
+      const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+      const float keep = m[mt] == -__builtin_inff() ? (l[mt] == 0.0f ? 0.0f : l[mt])   // nothing met, or NaN alone
+                                                    : __builtin_amdgcn_exp2f(m[mt] - top);
+      float* row = sums + (wave * kRows + r) * kPad;
+#pragma unroll
+      for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < S::VC; c += 4) {
+            f32x4_t x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = o[mt][u * S::VC + c + e][i] * keep;
+            *reinterpret_cast<f32x4_t*>(row + u * 16 * S::VC + (quarter * 4 + i) * S::VC + c) = x;
+          }
+    }
+    __syncthreads();
+    const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
+    for (int i = threadIdx.x; i < kRows * (D / 8); i += kAttnThreads) {
+      const int r = i / (D / 8), ch = i % (D / 8) * 8, at = tile * kRows + r;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float* from = sums + (s * kRows + r) * kPad + ch;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += from[e];
+      }
+      const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+      float sum = 0.0f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        sum += sm.l[s][r] * (sm.m[s][r] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(sm.m[s][r] - top));
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4)
+          *reinterpret_cast<f32x4_t*>(slot + r * D + ch + e) = f32x4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
+        if (ch == 0) {
+          slot[kRows * D + r] = top;
+          slot[kRows * D + kRows + r] = sum;
+        }
+      } else if (at < rows) {
+        write_row(a, row_at(at), ch, x, top, at < live ? sum : 0.0f);
+      }
+    }
+  }
+
+  // Eight channels of an output row, and with the first of them its lse.
+  static __device__ void write_row(const AttnArgs& a, int64_t row, int ch, float (&x)[8], float top, float sum) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] / sum;
+    store8<DT>(a.out, row * D + ch, 8, from_f32<DT>(x));
+    if (a.lse && ch == 0)
+      a.lse[row] = sum == 0.0f ? -__builtin_inff()
+                   : top == -__builtin_inff() ? sum : __builtin_fmaf(top, 0x1.62e430p-1f, logf(sum));
+  }
+};
+
+// Sum of v over the threads below this one, of kAttnThreads; all of them in `total`.
+__device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
+  int x = v;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const int y = __shfl_up(x, s);
+    if ((int)(threadIdx.x & 63) >= s) x += y;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) sums[threadIdx.x >> 6] = x;
+  __syncthreads();
+  int below = x - v;
+  total = 0;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if (s < (int)(threadIdx.x >> 6)) below += sums[s];
+    total += sums[s];
+  }
+  return below;
+}
+
+// One workgroup for each problem.
+template <int DT, int FMT, int D, int MT>
+__global__ void __launch_bounds__(kAttnThreads) k_cache_attention(AttnArgs a) {
+  using A = Attention<DT, FMT, D, MT>;
+  __shared__ typename A::Shared sm;
+  A x(a, sm);
+  const int each = a.d.kv_heads * a.d.row_tiles;
+  x.b = blockIdx.x / each;
+  x.kv = (blockIdx.x - x.b * each) / a.d.row_tiles;
+  x.tile = blockIdx.x % a.d.row_tiles;
+  x.w = work_of(a, x.b, A::kRows);
+  x.piece(0, x.tile < x.w.tiles ? x.w.steps : 0, true, nullptr);
+}
+
+// The steps of all problems shared out evenly: workgroup w takes those of share_of, a piece of a problem at a time.  A
+// problem that lies within one share is written here, the others' parts are joined by k_cache_attention_join.
+template <int DT, int FMT, int D, int MT>
+__global__ void __launch_bounds__(kAttnThreads) k_cache_attention_split(AttnArgs a) {
+  using A = Attention<DT, FMT, D, MT>;
+  __shared__ typename A::Shared sm;
+  A x(a, sm);
+  int total = 0;
+  for (int b0 = 0; b0 < a.d.sequences; b0 += kAttnThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    int units = 0, sum;
+    if (b < a.d.sequences) {
+      const Work w = work_of(a, b, A::kRows);
+      units = w.steps * w.tiles * a.d.kv_heads;
+    }
+    attn_scan(units, sm.sums, sum);
+    total += sum;
+  }
+  const int g = min(a.d.workgroups, total), me = blockIdx.x;
+  if (me >= g) return;
+  int u = share_of(me, total, g);
+  const int end = share_of(me + 1, total, g);
+  int base = 0;                     // steps of the sequences before b0
+  for (int b0 = 0; u < end; b0 += kAttnThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    int units = 0, sum;
+    if (b < a.d.sequences) {
+      const Work w = work_of(a, b, A::kRows);
+      units = w.steps * w.tiles * a.d.kv_heads;
+    }
+    const int below = attn_scan(units, sm.sums, sum);
+    sm.first[threadIdx.x] = base + below;
+    __syncthreads();
+    while (u < min(end, base + sum)) {
+      int lo = 0;                   // the last sequence of the chunk that starts at or before u, and is not empty
+      for (int s = kAttnThreads / 2; s > 0; s /= 2)
+        if (sm.first[lo + s] <= u) lo += s;
+      x.b = __builtin_amdgcn_readfirstlane(b0 + lo);
+      x.w = work_of(a, x.b, A::kRows);
+      const int local = u - sm.first[lo], problem = local / x.w.steps, step = local - problem * x.w.steps;
+      x.kv = problem / x.w.tiles;
+      x.tile = problem - x.kv * x.w.tiles;
+      const int n = min(x.w.steps - step, end - u);
+      const bool whole = n == x.w.steps;
+      x.piece(step, step + n, whole, a.parts + (int64_t)(2 * me + (step == 0)) * kSlotFloats<MT, D>);
+      u += n;
+      __syncthreads();
+    }
+    base += sum;
+    __syncthreads();
+  }
+}
+
+// The parts of problems that several workgroups worked on, four rows to a workgroup; and zeros for those that none did.
+template <int DT, int FMT, int D, int MT>
+__global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs a) {
+  using A = Attention<DT, FMT, D, MT>;
+  __shared__ int sums[4];
+  const int each = a.d.kv_heads * a.d.row_tiles;
+  const int b = blockIdx.x / each, kv = (blockIdx.x - b * each) / a.d.row_tiles, tile = blockIdx.x % a.d.row_tiles;
+  int before = 0, all = 0;
+  for (int s = threadIdx.x; s < a.d.sequences; s += kAttnThreads) {
+    const Work w = work_of(a, s, A::kRows);
+    const int units = w.steps * w.tiles * a.d.kv_heads;
+    all += units;
+    if (s < b) before += units;
+  }
+  int total, first;
+  attn_scan(all, sums, total);
+  attn_scan(before, sums, first);
+  const Work w = work_of(a, b, A::kRows);
+  const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
+  const bool none = w.steps == 0 || tile >= w.tiles;
+  int w0 = 0, w1 = 0;
+  const int g = min(a.d.workgroups, total);
+  if (!none) {
+    first += (kv * w.tiles + tile) * w.steps;
+    w0 = owner_of(first, total, g);
+    w1 = owner_of(first + w.steps - 1, total, g);
+    if (w0 == w1) return;
+  }
+  for (int i = threadIdx.x; i < 4 * (D / 8); i += kAttnThreads) {
+    const int r = blockIdx.y * 4 + i / (D / 8), ch = i % (D / 8) * 8, at = tile * A::kRows + r;
+    if (at >= rows) continue;
+    float x[8] = {}, top = -__builtin_inff(), sum = 0.0f;
+    if (!none && at < live) {
+      for (int s = w0; s <= w1; ++s) {
+        const float* slot = a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<MT, D>;
+        top = fmaxf(top, slot[A::kRows * D + r]);
+      }
+      for (int s = w0; s <= w1; ++s) {
+        const float* slot = a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<MT, D>;
+        const float m = slot[A::kRows * D + r], l = slot[A::kRows * D + A::kRows + r];
+        const float keep = m == -__builtin_inff() ? (l == 0.0f ? 0.0f : l) : __builtin_amdgcn_exp2f(m - top);
+        sum += m == -__builtin_inff() ? l : l * keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += slot[r * D + ch + e] * keep;
+      }
+    }
+    const int t = at / a.d.group;
+    A::write_row(a, ((int64_t)b * a.d.tokens + t) * a.d.heads + kv * a.d.group + (at - t * a.d.group), ch, x, top, sum);
+  }
+}
+
+// Rows of a wave's tile, in 16s: as many as the problem has, while the sums fit the registers.
+inline int attention_row_tiles(int dt, int dim, int64_t rows) {
+  const int most = dim <= 128 ? (dt == DT_BF16 ? 4 : 2) : dim == 256 ? 2 : 1;
+  const int want = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  return want < most ? want : most;
+}
+
+template <int DT, int FMT, int D, int MT>
+hipError_t launch_attention_of(const AttnArgs& a, int64_t problems, hipStream_t st) {
+  if (a.d.workgroups == 0) {
+    k_cache_attention<DT, FMT, D, MT><<<(unsigned)problems, kAttnThreads, 0, st>>>(a);
+  } else {
+    k_cache_attention_split<DT, FMT, D, MT><<<(unsigned)a.d.workgroups, kAttnThreads, 0, st>>>(a);
+    k_cache_attention_join<DT, FMT, D, MT><<<dim3((unsigned)problems, 4 * MT), kAttnThreads, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <int DT, int FMT>
+hipError_t launch_attention_dim(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st) {
+#define CASE(D, MT) \
+  if (dim == D && tiles == MT) return launch_attention_of<DT, FMT, D, MT>(a, problems, st)
+  CASE(64, 1);
+  CASE(64, 2);
+  CASE(128, 1);
+  CASE(128, 2);
+  if constexpr (DT == DT_BF16) {
+    CASE(64, 4);
+    CASE(128, 4);
+  }
+  CASE(256, 1);
+  CASE(256, 2);
+  CASE(512, 1);
+#undef CASE
+  return hipErrorInvalidValue;
+}
+
+// The kernels of one type and format (csrc/cache_attention_<format>_<type>.hip).
+template <int DT, int FMT>
+hipError_t launch_attention_kernels(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st);
+#define DECLARE(DT, FMT) \
+  template <>            \
+  hipError_t launch_attention_kernels<DT, FMT>(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st)
+#define DECLARE_FORMATS(DT) \
+  DECLARE(DT, FMT_FP8);     \
+  DECLARE(DT, FMT_MXFP4);   \
+  DECLARE(DT, FMT_NVFP4)
+DECLARE_FORMATS(DT_F32);
+DECLARE_FORMATS(DT_BF16);
+DECLARE_FORMATS(DT_F16);
+#undef DECLARE_FORMATS
+#undef DECLARE
+
+}  // namespace mxq
