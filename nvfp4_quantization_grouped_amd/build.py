@@ -29,6 +29,10 @@ HIPCC_FLAGS = [
     "-Wall", "-Wno-unused-function",
     "-I", os.path.join(ROOT, "include"),
 ]
+# Flags of some files (by the start of their names).  The attention kernels' sums pass through branches and are scaled
+# between products: in VGPRs they stay where they are, in AGPRs each passage copies them (64 of 430 registers at head size
+# 128, and a third of the instructions).
+FILE_FLAGS = {"cache_attention_": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def hipcc():
@@ -41,7 +45,8 @@ def hipcc():
 
 def _compile(src, extra):
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, "-c", src, "-o", obj]
+    own = [f for start, flags in FILE_FLAGS.items() if os.path.basename(src).startswith(start) for f in flags]
+    cmd = [hipcc(), *HIPCC_FLAGS, *own, *extra, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in (r.stderr or "").splitlines() if noise not in l)

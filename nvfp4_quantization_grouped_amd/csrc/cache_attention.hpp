@@ -322,8 +322,7 @@ struct Attention {
   }
 
   // ----- products
-  template <bool EXACT>
-  __device__ void scores(const K& k, const Q& q, f32x4_t (&s)[MT][2]) const {
+  __device__ void scores(const K& k, const Q& q, bool exact, f32x4_t (&s)[MT][2]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -339,7 +338,8 @@ struct Attention {
           static_for<4>([&](auto I) {
             constexpr int i = decltype(I)::value;
             const float f = sc[hf * 8 / 16 < S::KS ? hf * 8 / 16 : 0];
-            x[i] = EXACT ? decode_pair_exact<FMT, hf * 4 + i>(k.w[h][u], f) : decode_pair<FMT, hf * 4 + i>(k.w[h][u], f);
+            x[i] = decode_pair<FMT, hf * 4 + i>(k.w[h][u], f);
+            if (FMT == FMT_NVFP4 && exact) x[i] = decode_pair_exact<FMT, hf * 4 + i>(k.w[h][u], f);
           });
           const bf16x8_t key = as_bf16x8(x[0], x[1], x[2], x[3]);
 #pragma unroll
@@ -351,10 +351,10 @@ struct Attention {
       });
     }
   }
-  // O^T += V^T P^T.  CAREFUL: scales with mantissa bits, and values that are not finite, which count only for the rows
-  // that attend to them (`seen`: bf16 ones for those, in the probabilities' places).
-  template <bool CAREFUL>
-  __device__ void values(const V& v, const bf16x8_t (&p)[MT][PP], const bf16x8_t (&seen)[MT], f32x4_t (&o)[MT][kTilesV]) const {
+  // O^T += V^T P^T.  exact: scales with mantissa bits; careful: values that are not finite count only for the rows that
+  // attend to them (`seen`: bf16 ones for those, in the probabilities' places).
+  __device__ void values(const V& v, const bf16x8_t (&p)[MT][PP], bool exact, bool careful, const bf16x8_t (&seen)[MT],
+                         f32x4_t (&o)[MT][kTilesV]) const {
     static_for<S::VU>([&](auto U) {
       constexpr int u = decltype(U)::value;
       float sc[8][S::VS];
@@ -368,7 +368,11 @@ struct Attention {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float f = sc[j][i / 8 < S::VS ? i / 8 : 0];
-          x[j] = CAREFUL && FMT == FMT_NVFP4 ? decode_pair_exact<FMT, i>(v.w[j][u], f) : decode_pair<FMT, i>(v.w[j][u], f);
+          x[j] = decode_pair<FMT, i>(v.w[j][u], f);
+        }
+        if (FMT == FMT_NVFP4 && exact) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = decode_pair_exact<FMT, i>(v.w[j][u], sc[j][i / 8 < S::VS ? i / 8 : 0]);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -377,9 +381,8 @@ struct Attention {
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], pick);
           const int t = u * S::VC + 2 * i + half;
-          uint32_t odd[4] = {0u, 0u, 0u, 0u};
-          bool any = false;
-          if constexpr (CAREFUL) {
+          if (careful) {
+            uint32_t odd[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               if ((y[j] & 0x7F80u) == 0x7F80u) odd[j] |= 0x3F80u;
@@ -387,20 +390,20 @@ struct Attention {
               if (odd[j] & 0x3F80u) y[j] &= 0xFFFF0000u;
               if (odd[j] & 0x3F800000u) y[j] &= 0xFFFFu;
             }
-            any = __ballot((odd[0] | odd[1] | odd[2] | odd[3]) != 0) != 0;
+            if (__ballot((odd[0] | odd[1] | odd[2] | odd[3]) != 0) != 0) {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                const f32x4_t met = mfma(as_bf16x8(odd[0], odd[1], odd[2], odd[3]), seen[mt], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[mt][t][r] += met[r] > 0.0f ? __builtin_nanf("") : 0.0f;
+              }
+            }
           }
           const bf16x8_t val = as_bf16x8(y[0], y[1], y[2], y[3]);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int part = 0; part < PP; ++part) o[mt][t] = mfma(val, p[mt][part], o[mt][t]);
-            if (CAREFUL && any) {
-              const f32x4_t met = mfma(as_bf16x8(odd[0], odd[1], odd[2], odd[3]), seen[mt], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (met[r] > 0.0f) o[mt][t][r] = __builtin_nanf("");
-            }
-          }
         }
       });
     });
@@ -446,14 +449,13 @@ struct Attention {
               for (int i = 0; i < S::VS; ++i) odd |= has_mantissa(scale_value<FMT>(v.s[j][u][i]));
           exact = __ballot(odd) != 0;
         }
-        if (FMT == FMT_NVFP4 && exact) scores<FMT == FMT_NVFP4>(k, q, s);
-        else scores<false>(k, q, s);
+        scores(k, q, exact, s);
         const bool more = t + 4 < end;
         const Pages after = pages_of(min(t + 8, a.d.width << a.d.page_shift >> 5));
         if (more) load_k(k, next, t + 4);
         // positions that not every row attends to
         const bool plain = now.there[0] && now.there[1] && (t + 1) * kTile <= w.known;
-        bf16x8_t p[MT][PP], seen[MT];
+        bf16x8_t p[MT][PP], seen[MT] = {};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float x[8];
@@ -462,16 +464,17 @@ struct Attention {
           for (int i = 0; i < 8; ++i) x[i] = s[mt][i / 4][i % 4];
           if (!plain) {
             const int token = row_of(mt) / a.d.group;
+            const uint8_t* see = a.mask ? a.mask + ((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens +
+                                                    min(token, a.d.tokens - 1)) * a.d.tokens : nullptr;
             may = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int pos = t * kTile + (i / 4) * 16 + quarter * 4 + i % 4, j = pos - w.known;
-              bool ok = now.there[i / 4] && pos < w.end && token < w.count;
-              if (ok && j >= 0)
-                ok = a.mask ? a.mask[((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens + token) * a.d.tokens + j] != 0
-                            : j <= token;
+              bool ok = j <= token;
+              if (see) ok = j < 0 || see[min(max(j, 0), a.d.tokens - 1)] != 0;
+              ok = ok && now.there[i / 4] && pos < w.end && token < w.count;
               may |= (uint32_t)ok << i;
-              if (!ok) x[i] = -__builtin_inff();
+              x[i] = ok ? x[i] : -__builtin_inff();
             }
             uint32_t one[4];
 #pragma unroll
@@ -503,30 +506,23 @@ struct Attention {
 #pragma unroll
           for (int part = 0; part < PP; ++part) p[mt][part] = take_part(x, part == PP - 1);
         }
-        if (plain && !exact) {
-          values<false>(v, p, seen, o);
-        } else {
-          if (plain) {
+        if (!plain) {
+          // rows that are no position: zeros
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) seen[mt] = as_bf16x8(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-          } else {
-            // rows that are no position: zeros
+          for (int j = 0; j < 8; ++j) {
+            const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
+            if (!now.there[j / 4] || pos >= w.end) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
-              if (!now.there[j / 4] || pos >= w.end) {
+              for (int u = 0; u < S::VU; ++u) {
 #pragma unroll
-                for (int u = 0; u < S::VU; ++u) {
+                for (int i = 0; i < S::VW; ++i) v.w[j][u][i] = 0u;
 #pragma unroll
-                  for (int i = 0; i < S::VW; ++i) v.w[j][u][i] = 0u;
-#pragma unroll
-                  for (int i = 0; i < S::VS; ++i) v.s[j][u][i] = FMT == FMT_NVFP4 ? 0x38 : 127;
-                }
+                for (int i = 0; i < S::VS; ++i) v.s[j][u][i] = FMT == FMT_NVFP4 ? 0x38 : 127;
               }
             }
           }
-          values<true>(v, p, seen, o);
         }
+        values(v, p, exact, !plain, seen, o);
         if (more) load_v(v, next, t + 4);
         now = next;
         next = after;
