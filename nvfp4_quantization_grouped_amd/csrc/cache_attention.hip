@@ -4,8 +4,8 @@
 namespace mxq {
 namespace {
 
-// Steps are shared out among this many workgroups, two for each of 256 CUs.
-constexpr int kWorkgroups = 512;
+// Steps are shared out among as many workgroups as run at a time.
+constexpr int kComputeUnits = 256;
 // From so many problems on each has a workgroup of its own: there are enough of them to keep the card busy.
 constexpr int64_t kManyProblems = 2048;
 // Problems of so many steps at most are not worth sharing.
@@ -25,7 +25,7 @@ Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64
   p.problems = sequences * c.kv_heads * p.row_tiles;
   const int64_t steps = (width * c.page_size + kStep - 1) / kStep;
   const bool split = p.problems < kManyProblems && steps > kFewSteps && p.problems * steps < (int64_t(1) << 31);
-  p.workgroups = split ? kWorkgroups : 0;
+  p.workgroups = split ? kComputeUnits * attention_waves(c.head_dim, p.tiles) : 0;
   return p;
 }
 
@@ -44,7 +44,8 @@ hipError_t launch_cache_attention(const CacheArgs& c, const TableArgs& t, const 
   AttnArgs a = {c.k_codes, c.k_scales, c.v_codes, c.v_scales, t.table, t.lengths, x.counts, (const uint8_t*)x.q, x.mask,
                 (uint8_t*)x.out, x.lse, (float*)workspace, log2_of(c.block), {}};
   a.d = {t.sequences, x.tokens, x.heads, x.heads / c.kv_heads, c.kv_heads, t.width, log2_of(c.page_size), p.row_tiles,
-         p.workgroups, x.mask_each, c.pages, (float)(fabs((double)x.scale) * 1.4426950408889634), x.scale < 0};
+         p.workgroups, x.mask_each, c.pages, fmaxf((float)(fabs((double)x.scale) * 1.4426950408889634), 0x1p-149f),
+         x.scale < 0};
 #define CALL(DT, FMT) return launch_attention_kernels<DT, FMT>(a, c.head_dim, p.tiles, p.problems, st)
 #define FORMATS(DT)                        \
   if (c.fmt == FMT_FP8) CALL(DT, FMT_FP8); \

@@ -47,7 +47,7 @@ struct AttnDims {
   int workgroups;       // that share the steps (split), or 0: one workgroup for each problem
   bool mask_each;
   int64_t pages;
-  float scale;          // its size, times log2(e)
+  float scale;          // its size, times log2(e), no less than 2^-149: -inf times it is -inf
   bool negative;        // its sign, which q takes
 };
 struct AttnArgs {
@@ -101,13 +101,23 @@ __device__ __forceinline__ uint32_t decode_pair(const uint32_t* w, float s) {
   if constexpr (FMT == FMT_FP8) return dec_fp8_bf16x2<(I & 1) != 0>(w[I / 2], s);
   else return dec_fp4_bf16x2<I & 3>(w[I / 4], s);
 }
-// The same for a scale with mantissa bits (nvfp4): the conversion uses the exponent alone.
-template <int FMT, int I>
-__device__ __forceinline__ uint32_t decode_pair_exact(const uint32_t* w, float s) {
-  const uint32_t v = decode_pair<FMT, I>(w, 1.0f);
-  return elem_bits<DT_BF16>(bf16_lo(v) * s) | elem_bits<DT_BF16>(bf16_hi(v) * s) << 16;
+// Scale byte -> scale for the conversions, which take its exponent: for E8M0 that is the byte (0 means 2^-127 and 0xFF NaN
+// there too, bit for bit over every code).
+template <int FMT>
+__device__ __forceinline__ float scale_operand(uint32_t b) {
+  if constexpr (FMT == FMT_NVFP4) return scale_value<FMT>(b);
+  else return as_f32(b << 23);
 }
-__device__ __forceinline__ bool has_mantissa(float s) { return (as_u32(s) & 0x7FFFFFu) != 0; }
+// Whether a scale is more than its exponent (an E4M3 byte that is not what quantize_cache_packed writes): mantissa bits
+// (NaN has some), a sign, or 0.
+__device__ __forceinline__ bool beyond_exponent(float s) { return (as_u32(s) & 0x807FFFFFu) != 0 || s == 0.0f; }
+// Such a scale, 2^e (1 + b1 / 2 + b2 / 4 + b3 / 8), in four passes that each take a power of two: 2^e, then 2^(e - pass)
+// where that bit is set, and next to nothing (2^-127) where it is not.  NaN stays NaN in the first.
+__device__ __forceinline__ float scale_in_pass(float s, int pass) {
+  const uint32_t u = as_u32(s), e = u >> 23 & 0xFFu;
+  if (pass == 0) return e == 255u ? s : as_f32(e << 23);
+  return e != 255u && (u >> (23 - pass) & 1u) ? as_f32((e - pass) << 23) : 0.0f;
+}
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8_t, u32x4_t{a, b, c, d});
@@ -141,25 +151,47 @@ __device__ __forceinline__ float row_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// A value that every lane of a wave reads, through the scalar cache: the wait for it is not a wait for the vector loads
+// before it.  Tables and lengths do not change while a kernel runs.
+__device__ __forceinline__ int uniform_load(const int32_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* Scalar;
+  return ((Scalar)(uintptr_t)p)[i];
+}
+
 // --------------------------------------------------------------- the schedule
 // A problem is a sequence, a kv head and a tile of rows; its work is its steps of kStep positions.
 struct Work {
   int known, end, count;     // cached positions, those and the drafted ones, tokens that are no padding
   int steps, tiles;          // of each problem; row tiles that hold such a token
 };
-__device__ __forceinline__ Work work_of(const AttnArgs& a, int b, int rows) {
+__device__ __forceinline__ Work work_of(const AttnArgs& a, int length, int count, int rows) {
   Work w;
-  w.known = cached_positions(a.lengths[b], a.d.width, 1 << a.d.page_shift);
-  w.count = a.counts ? min(max(a.counts[b], 0), a.d.tokens) : a.d.tokens;
+  w.known = cached_positions(length, a.d.width, 1 << a.d.page_shift);
+  w.count = min(max(count, 0), a.d.tokens);
   w.end = w.count > 0 ? min(w.known + w.count, a.d.width << a.d.page_shift) : 0;
   w.steps = (w.end + kStep - 1) / kStep;
   w.tiles = (w.count * a.d.group + rows - 1) / rows;
   return w;
 }
+// Of a sequence that the whole workgroup works on, in scalar registers.
+__device__ __forceinline__ Work work_of_all(const AttnArgs& a, int b, int rows) {
+  return work_of(a, uniform_load(a.lengths, b), a.counts ? uniform_load(a.counts, b) : a.d.tokens, rows);
+}
+// Steps of a thread's sequence, all its problems together.
+__device__ __forceinline__ int units_of(const AttnArgs& a, int b, int rows) {
+  if (b >= a.d.sequences) return 0;
+  const Work w = work_of(a, a.lengths[b], a.counts ? a.counts[b] : a.d.tokens, rows);
+  return w.steps * w.tiles * a.d.kv_heads;
+}
 // Steps [first, last) of all problems' that workgroup w of g takes.
 __device__ __forceinline__ int share_of(int w, int total, int g) { return (int)((int64_t)w * total / g); }
 // The workgroup that takes step u.
 __device__ __forceinline__ int owner_of(int u, int total, int g) { return (int)((((int64_t)u + 1) * g - 1) / total); }
+
+// Waves of a SIMD that the registers are kept to, which is workgroups of a CU.
+constexpr int attention_waves(int dim, int tiles) { return dim * tiles <= 128 ? 3 : dim * tiles <= 256 ? 2 : 1; }
+template <int D, int MT>
+constexpr int kWaves = attention_waves(D, MT);
 
 template <int MT, int D>
 constexpr int kSlotFloats = 16 * MT * (D + 2);
@@ -179,6 +211,7 @@ struct Attention {
 
   struct Shared {
     __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
+    __attribute__((aligned(16))) uint8_t nan[kRows * D];   // outputs that a value that is not finite reached
     float m[4][kRows], l[4][kRows];
     int first[kAttnThreads + 1];                           // prefix sums of the schedule
     int sums[4];
@@ -186,24 +219,33 @@ struct Attention {
 
   const AttnArgs& a;
   Shared& sm;
-  const int lane, wave, col, quarter;
+  int lane, col, quarter;
+  const int wave;
   // the problem
   int b, kv, tile;
   Work w;
 
-  __device__ Attention(const AttnArgs& args, Shared& shared)
-      : a(args), sm(shared), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
-        col(threadIdx.x & 15), quarter((threadIdx.x & 63) >> 4) {}
+  __device__ __forceinline__ Attention(const AttnArgs& args, Shared& shared)
+      : a(args), sm(shared), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
+    place();
+  }
+  // The lane's place, anew: what is computed from it is not kept across pieces (some 25 registers of addresses).
+  __device__ __forceinline__ void place() {
+    lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    col = lane & 15;
+    quarter = lane >> 4;
+  }
 
   // Element offset of row r of the problem in q and out; r < tokens * group.
-  __device__ int64_t row_at(int r) const {
+  __device__ __forceinline__ int64_t row_at(int r) const {
     const int i = r / a.d.group, g = r - i * a.d.group;
     return (((int64_t)b * a.d.tokens + i) * a.d.heads + kv * a.d.group + g);
   }
-  __device__ int row_of(int mt) const { return tile * kRows + mt * 16 + col; }
+  __device__ __forceinline__ int row_of(int mt) const { return tile * kRows + mt * 16 + col; }
 
   // ----- q
-  __device__ void q_fragment(int mt, int step, bf16x8_t (&part)[QP]) const {
+  __device__ __forceinline__ void q_fragment(int mt, int step, bf16x8_t (&part)[QP]) const {
     const int u = step / S::kHalves, h = step % S::kHalves;
     const int ch = u * 4 * S::KC + quarter * S::KC + h * 8, r = row_of(mt);
     float x[8] = {};
@@ -217,7 +259,7 @@ struct Attention {
   struct Q {
     bf16x8_t f[kQInRegs ? MT : 1][kQInRegs ? S::kSteps : 1][QP];
   };
-  __device__ void load_q(Q& q) const {
+  __device__ __forceinline__ void load_q(Q& q) const {
     if constexpr (kQInRegs) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -234,7 +276,7 @@ struct Attention {
       __syncthreads();
     }
   }
-  __device__ bf16x8_t q_part(const Q& q, int mt, int step, int p) const {
+  __device__ __forceinline__ bf16x8_t q_part(const Q& q, int mt, int step, int p) const {
     if constexpr (kQInRegs) return q.f[mt][step][p];
     else
       return *reinterpret_cast<const bf16x8_t*>(sm.big + ((((mt * S::kSteps + step) * QP + p) * 64) + lane) * 16);
@@ -245,21 +287,19 @@ struct Attention {
     int page[2];        // of the tile's halves of 16 positions; 0 where there is none
     bool there[2];
   };
-  __device__ Pages pages_of(int t) const {
+  __device__ __forceinline__ Pages pages_of(int t) const {
     Pages p;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int slot = (t * kTile + h * 16) >> a.d.page_shift;
-      int page = -1;
-      if (slot < a.d.width) page = a.table[(int64_t)b * a.d.width + slot];
-      page = __builtin_amdgcn_readfirstlane(page);
-      p.there[h] = (uint32_t)page < (uint32_t)a.d.pages;
+      const int page = uniform_load(a.table, (int64_t)b * a.d.width + min(slot, a.d.width - 1));
+      p.there[h] = slot < a.d.width && (uint32_t)page < (uint32_t)a.d.pages;
       p.page[h] = p.there[h] ? page : 0;
     }
     return p;
   }
   // Row in the pools of the first position of half h of tile t.
-  __device__ int64_t pool_row(const Pages& p, int t, int h) const {
+  __device__ __forceinline__ int64_t pool_row(const Pages& p, int t, int h) const {
     const int in_page = (t * kTile + h * 16) & ((1 << a.d.page_shift) - 1);
     return (((int64_t)p.page[h] * a.d.kv_heads + kv) << a.d.page_shift) + in_page;
   }
@@ -271,7 +311,7 @@ struct Attention {
     uint32_t w[8][S::VU][S::VW];
     uint32_t s[8][S::VU][S::VS];
   };
-  __device__ void load_k(K& k, const Pages& p, int t) const {
+  __device__ __forceinline__ void load_k(K& k, const Pages& p, int t) const {
     const int blocks = D >> a.block_shift;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -294,7 +334,7 @@ struct Attention {
       }
     }
   }
-  __device__ void load_v(V& v, const Pages& p, int t) const {
+  __device__ __forceinline__ void load_v(V& v, const Pages& p, int t) const {
     const int blocks = D >> a.block_shift;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -322,95 +362,177 @@ struct Attention {
   }
 
   // ----- products
-  __device__ void scores(const K& k, const Q& q, bool exact, f32x4_t (&s)[MT][2]) const {
+  // Scales that are more than exponents: their sign and zero go into the codes (word by word; a unit's scales each hold
+  // for as many words), and the rest takes four passes.  Returns the number of passes.
+  template <int ROWS, int UNITS, int SCALES, int WORDS>
+  __device__ __forceinline__ static int passes_of(uint32_t (&w)[ROWS][UNITS][WORDS], const uint32_t (&s)[ROWS][UNITS][SCALES]) {
+    if constexpr (FMT != FMT_NVFP4) return 1;
+    bool any = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[mt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      static_for<S::KU>([&](auto U) {
-        constexpr int u = decltype(U)::value;
-        float sc[S::KS];
+      for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-        for (int i = 0; i < S::KS; ++i) sc[i] = scale_value<FMT>(k.s[h][u][i]);
-        static_for<S::kHalves>([&](auto H) {
-          constexpr int hf = decltype(H)::value;
+        for (int i = 0; i < SCALES; ++i) any |= beyond_exponent(scale_value<FMT>(s[r][u][i]));
+    if (__ballot(any) == 0) return 1;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+          const float f = scale_value<FMT>(s[r][u][i * SCALES / WORDS]);
+          w[r][u][i] = f == 0.0f ? 0u : w[r][u][i] ^ (as_u32(f) >> 31) * 0x88888888u;
+        }
+    return 4;
+  }
+  __device__ __forceinline__ static float scale_of(uint32_t byte, int pass, int passes) {
+    const float s = scale_operand<FMT>(byte);
+    if constexpr (FMT != FMT_NVFP4) return s;
+    return passes == 1 ? s : scale_in_pass(s, pass);
+  }
+  // S^T += K Q^T.  The two halves' sums take turns, so that a product seldom waits for the one before it.
+  __device__ __forceinline__ void scores(const K& k, const Q& q, int pass, int passes, f32x4_t (&s)[MT][2]) const {
+    static_for<S::KU>([&](auto U) {
+      constexpr int u = decltype(U)::value;
+      float sc[2][S::KS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < S::KS; ++i) sc[h][i] = scale_of(k.s[h][u][i], pass, passes);
+      static_for<S::kHalves>([&](auto H) {
+        constexpr int hf = decltype(H)::value, is = hf / 2 < S::KS ? hf / 2 : 0;
+        bf16x8_t key[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           uint32_t x[4];
           static_for<4>([&](auto I) {
-            constexpr int i = decltype(I)::value;
-            const float f = sc[hf * 8 / 16 < S::KS ? hf * 8 / 16 : 0];
-            x[i] = decode_pair<FMT, hf * 4 + i>(k.w[h][u], f);
-            if (FMT == FMT_NVFP4 && exact) x[i] = decode_pair_exact<FMT, hf * 4 + i>(k.w[h][u], f);
+            x[decltype(I)::value] = decode_pair<FMT, hf * 4 + decltype(I)::value>(k.w[h][u], sc[h][is]);
           });
-          const bf16x8_t key = as_bf16x8(x[0], x[1], x[2], x[3]);
+          key[h] = as_bf16x8(x[0], x[1], x[2], x[3]);
+        }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+        for (int p = 0; p < QP; ++p)
 #pragma unroll
-            for (int p = 0; p < QP; ++p)
-              s[mt][h] = mfma(key, q_part(q, mt, u * S::kHalves + hf, p), s[mt][h]);
-        });
+          for (int mt = 0; mt < MT; ++mt) {
+            const bf16x8_t f = q_part(q, mt, u * S::kHalves + hf, p);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s[mt][h] = mfma(key[h], f, s[mt][h]);
+          }
       });
-    }
+    });
   }
-  // O^T += V^T P^T.  exact: scales with mantissa bits; careful: values that are not finite count only for the rows that
-  // attend to them (`seen`: bf16 ones for those, in the probabilities' places).
-  __device__ void values(const V& v, const bf16x8_t (&p)[MT][PP], bool exact, bool careful, const bf16x8_t (&seen)[MT],
-                         f32x4_t (&o)[MT][kTilesV]) const {
+  // O^T += V^T P^T.
+  __device__ __forceinline__ void values(const V& v, const bf16x8_t (&p)[MT][PP], int pass, int passes, f32x4_t (&o)[MT][kTilesV]) const {
     static_for<S::VU>([&](auto U) {
       constexpr int u = decltype(U)::value;
       float sc[8][S::VS];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < S::VS; ++i) sc[j][i] = scale_value<FMT>(v.s[j][u][i]);
+        for (int i = 0; i < S::VS; ++i) sc[j][i] = scale_of(v.s[j][u][i], pass, passes);
       static_for<S::VC / 2>([&](auto I) {
-        constexpr int i = decltype(I)::value;
+        constexpr int i = decltype(I)::value, is = i / 8 < S::VS ? i / 8 : 0;
         uint32_t x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float f = sc[j][i / 8 < S::VS ? i / 8 : 0];
-          x[j] = decode_pair<FMT, i>(v.w[j][u], f);
+        for (int j = 0; j < 8; ++j) x[j] = decode_pair<FMT, i>(v.w[j][u], sc[j][is]);
+        uint32_t y[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[0][j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
+          y[1][j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
         }
-        if (FMT == FMT_NVFP4 && exact) {
+        const int t = u * S::VC + 2 * i;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = decode_pair_exact<FMT, i>(v.w[j][u], sc[j][i / 8 < S::VS ? i / 8 : 0]);
-        }
+        for (int part = 0; part < PP; ++part)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t pick = half ? 0x07060302u : 0x05040100u;
-          uint32_t y[4];
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], pick);
-          const int t = u * S::VC + 2 * i + half;
-          if (careful) {
-            uint32_t odd[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((y[j] & 0x7F80u) == 0x7F80u) odd[j] |= 0x3F80u;
-              if ((y[j] & 0x7F800000u) == 0x7F800000u) odd[j] |= 0x3F800000u;
-              if (odd[j] & 0x3F80u) y[j] &= 0xFFFF0000u;
-              if (odd[j] & 0x3F800000u) y[j] &= 0xFFFFu;
-            }
-            if (__ballot((odd[0] | odd[1] | odd[2] | odd[3]) != 0) != 0) {
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const f32x4_t met = mfma(as_bf16x8(odd[0], odd[1], odd[2], odd[3]), seen[mt], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[mt][t][r] += met[r] > 0.0f ? __builtin_nanf("") : 0.0f;
-              }
-            }
-          }
-          const bf16x8_t val = as_bf16x8(y[0], y[1], y[2], y[3]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int part = 0; part < PP; ++part) o[mt][t] = mfma(val, p[mt][part], o[mt][t]);
-        }
+            for (int mt = 0; mt < MT; ++mt)
+              o[mt][t + half] = mfma(as_bf16x8(y[half][0], y[half][1], y[half][2], y[half][3]), p[mt][part], o[mt][t + half]);
       });
     });
   }
 
+  // A tile of which not every row attends to every position: scores of the others become -inf, values of rows that are
+  // no position 0.  A value that is not finite counts for the rows that attend to it alone: it becomes 0 here (0 times
+  // NaN is NaN) and is marked for those rows, whose sums are NaN in the end.
+  __device__ __forceinline__ void mask(const Pages& now, int t, f32x4_t (&s)[MT][2], V& v) const {
+    uint32_t may[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int token = row_of(mt) / a.d.group;
+      const uint8_t* see = a.mask ? a.mask + ((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens +
+                                              min(token, a.d.tokens - 1)) * a.d.tokens : nullptr;
+      may[mt] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pos = t * kTile + (i / 4) * 16 + quarter * 4 + i % 4, j = pos - w.known;
+        bool ok = j <= token;
+        if (see) ok = j < 0 || see[min(max(j, 0), a.d.tokens - 1)] != 0;
+        ok = ok && now.there[i / 4] && pos < w.end && token < w.count;
+        may[mt] |= (uint32_t)ok << i;
+        s[mt][i / 4][i % 4] = ok ? s[mt][i / 4][i % 4] : -__builtin_inff();
+      }
+    }
+    // codes whose value is not finite: from `least` on (by size), which the scale says
+    constexpr uint32_t kOnes = S::kFp8 ? 0x01010101u : 0x11111111u, kTop = S::kFp8 ? 0x80808080u : 0x88888888u;
+    constexpr int kBits = S::kFp8 ? 8 : 4, kHalf = 1 << (kBits - 1);
+    uint32_t bad[8][S::VU][S::VW], any = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
+      const bool none = !now.there[j / 4] || pos >= w.end;
+#pragma unroll
+      for (int u = 0; u < S::VU; ++u) {
+        uint32_t more[S::VS];         // kHalf - least
+#pragma unroll
+        for (int i = 0; i < S::VS; ++i) {
+          const int e = v.s[j][u][i];
+          int least;
+          if constexpr (FMT == FMT_NVFP4) least = (e & 0x7F) == 0x7F ? 0 : 8;
+          else if constexpr (S::kFp8) least = e == 255 ? 0 : min(127, max(262 - e, 0) << 3);   // 0x7F is NaN by itself
+          else least = e == 255 ? 0 : min(8, max(256 - e, 0) << 1);
+          more[i] = none ? 0u : (kHalf - least) * kOnes;
+          v.s[j][u][i] = none || least == 0 ? (FMT == FMT_NVFP4 ? 0x38u : 127u) : v.s[j][u][i];
+        }
+#pragma unroll
+        for (int i = 0; i < S::VW; ++i) {
+          const uint32_t word = none ? 0u : v.w[j][u][i];
+          const uint32_t f = ((word & ~kTop) + more[i * S::VS / S::VW]) & kTop;
+          v.w[j][u][i] = word & ~((f >> (kBits - 1)) * (2 * kHalf - 1));
+          bad[j][u][i] = f;
+          any |= f;
+        }
+      }
+    }
+    if (__ballot(any != 0) == 0) return;
+    // the marks, in loops over words that lie in LDS
+    constexpr int kWords = 8 * S::VU * S::VW, kCodes = S::VC / S::VW;
+    static_assert(kQBytes + kAttnThreads * kWords * 4 <= kLdsBytes, "the marks' words lie behind q's fragments");
+    uint32_t* words = reinterpret_cast<uint32_t*>(sm.big + kQBytes) + (wave * 64 + lane) * kWords;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) words[i] = bad[i / (S::VU * S::VW)][i / S::VW % S::VU][i % S::VW];
+#pragma unroll 1
+    for (int i = 0; i < kWords * kCodes; ++i) {
+      const int word = i / kCodes, code = i - word * kCodes, j = word / (S::VU * S::VW);
+      const uint64_t all = __ballot(words[word] >> (code * kBits + kBits - 1) & 1u);
+      // the quarter's lanes hold this channel of their units, and the rows of the same positions
+      for (uint32_t lanes = (uint32_t)(all >> (quarter * 16)) & 0xFFFFu; lanes != 0; lanes &= lanes - 1) {
+        const int unit = word / S::VW % S::VU, in_unit = (word % S::VW) * kCodes + code;
+        const int channel = unit * 16 * S::VC + __builtin_ctz(lanes) * S::VC + in_unit;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if (may[mt] >> j & 1) sm.nan[(mt * 16 + col) * D + channel] = 1;
+      }
+    }
+  }
+
   // Steps [first, last) of the problem, this wave's tile of each; `whole`: they are all, else the sums go to `slot`.
-  __device__ void piece(int first, int last, bool whole, float* slot) {
+  __device__ __forceinline__ void piece(int first, int last, bool whole, float* slot) {
+    place();
+    for (int i = wave * 64 + lane; i < kRows * D / 16; i += kAttnThreads)
+      *reinterpret_cast<u32x4_t*>(sm.nan + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
     Q q;
     load_q(q);
     f32x4_t o[MT][kTilesV];
@@ -422,69 +544,41 @@ struct Attention {
       m[mt] = -__builtin_inff();
       sub[mt] = l[mt] = 0.0f;
     }
+    __syncthreads();
     int t = first * 4 + wave;
     const int end = min(last * 4, (w.end + kTile - 1) / kTile);
     if (t < end) {
-      Pages now = pages_of(t), next = pages_of(t + 4);
+      Pages now = pages_of(t);
+      int ahead = t + 4 < end ? t + 4 : t;
+      Pages next = pages_of(ahead);
       K k;
       V v;
       load_k(k, now, t);
       load_v(v, now, t);
-      for (; t < end; t += 4) {
+      // One tile, while the next one's rows are on their way: its keys from the scores on, its values from the values on.
+      // (After the last tile that is the same tile again, from the caches.)
+      while (true) {
         f32x4_t s[MT][2];
-        bool exact = false;
-        if constexpr (FMT == FMT_NVFP4) {
-          bool odd = false;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int u = 0; u < S::KU; ++u)
-#pragma unroll
-              for (int i = 0; i < S::KS; ++i) odd |= has_mantissa(scale_value<FMT>(k.s[h][u][i]));
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int u = 0; u < S::VU; ++u)
-#pragma unroll
-              for (int i = 0; i < S::VS; ++i) odd |= has_mantissa(scale_value<FMT>(v.s[j][u][i]));
-          exact = __ballot(odd) != 0;
+        for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        int passes = passes_of(k.w, k.s);
+        for (int pass = 0;;) {
+          scores(k, q, pass, passes, s);
+          if (FMT != FMT_NVFP4 || ++pass >= passes) break;
         }
-        scores(k, q, exact, s);
-        const bool more = t + 4 < end;
-        const Pages after = pages_of(min(t + 8, a.d.width << a.d.page_shift >> 5));
-        if (more) load_k(k, next, t + 4);
-        // positions that not every row attends to
-        const bool plain = now.there[0] && now.there[1] && (t + 1) * kTile <= w.known;
-        bf16x8_t p[MT][PP], seen[MT] = {};
+        load_k(k, next, ahead);
+        const int beyond = ahead + 4 < end ? ahead + 4 : ahead;
+        const Pages after = pages_of(beyond);
+        if (!(now.there[0] && now.there[1] && (t + 1) * kTile <= w.known)) mask(now, t, s, v);
+        bf16x8_t p[MT][PP];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float x[8];
-          uint32_t may = 0xFF;
+          float e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = s[mt][i / 4][i % 4];
-          if (!plain) {
-            const int token = row_of(mt) / a.d.group;
-            const uint8_t* see = a.mask ? a.mask + ((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens +
-                                                    min(token, a.d.tokens - 1)) * a.d.tokens : nullptr;
-            may = 0;
+          for (int i = 0; i < 8; ++i) e[i] = s[mt][i / 4][i % 4];
+          float top = e[0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int pos = t * kTile + (i / 4) * 16 + quarter * 4 + i % 4, j = pos - w.known;
-              bool ok = j <= token;
-              if (see) ok = j < 0 || see[min(max(j, 0), a.d.tokens - 1)] != 0;
-              ok = ok && now.there[i / 4] && pos < w.end && token < w.count;
-              may |= (uint32_t)ok << i;
-              x[i] = ok ? x[i] : -__builtin_inff();
-            }
-            uint32_t one[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              one[i] = (may >> (2 * i) & 1 ? 0x3F80u : 0u) | (may >> (2 * i + 1) & 1 ? 0x3F800000u : 0u);
-            seen[mt] = as_bf16x8(one[0], one[1], one[2], one[3]);
-          }
-          float top = x[0];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+          for (int i = 1; i < 8; ++i) top = fmaxf(top, e[i]);
           top *= a.d.scale;
           if (__ballot(top > m[mt] + kLazy) != 0) {
             const float to = fmaxf(m[mt], row_max(top));
@@ -496,43 +590,32 @@ struct Attention {
             for (int c = 0; c < kTilesV; ++c) o[mt][c] *= keep;
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.d.scale, -sub[mt]));
-          if (!plain) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = may >> i & 1 ? x[i] : 0.0f;     // -inf times a scale of 0 is NaN
+          for (int i = 0; i < 8; ++i) {
+            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[i], a.d.scale, -sub[mt]));
+            l[mt] += e[i];
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) l[mt] += x[i];
-#pragma unroll
-          for (int part = 0; part < PP; ++part) p[mt][part] = take_part(x, part == PP - 1);
+          for (int part = 0; part < PP; ++part) p[mt][part] = take_part(e, part == PP - 1);
         }
-        if (!plain) {
-          // rows that are no position: zeros
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
-            if (!now.there[j / 4] || pos >= w.end) {
-#pragma unroll
-              for (int u = 0; u < S::VU; ++u) {
-#pragma unroll
-                for (int i = 0; i < S::VW; ++i) v.w[j][u][i] = 0u;
-#pragma unroll
-                for (int i = 0; i < S::VS; ++i) v.s[j][u][i] = FMT == FMT_NVFP4 ? 0x38 : 127;
-              }
-            }
-          }
+        passes = passes_of(v.w, v.s);
+        for (int pass = 0;;) {
+          values(v, p, pass, passes, o);
+          if (FMT != FMT_NVFP4 || ++pass >= passes) break;
         }
-        values(v, p, exact, !plain, seen, o);
-        if (more) load_v(v, next, t + 4);
+        t += 4;
+        if (t >= end) break;
+        load_v(v, next, ahead);
         now = next;
         next = after;
+        ahead = beyond;
       }
     }
     join(o, m, l, whole, slot);
   }
 
   // The four waves' sums joined: written as outputs, or as a part of them.
-  __device__ void join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
+  __device__ __forceinline__ void join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
+    place();
     __syncthreads();      // q's fragments, and the last piece's sums, have been read
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -565,7 +648,7 @@ struct Attention {
     }
     __syncthreads();
     const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
-    for (int i = threadIdx.x; i < kRows * (D / 8); i += kAttnThreads) {
+    for (int i = wave * 64 + lane; i < kRows * (D / 8); i += kAttnThreads) {
       const int r = i / (D / 8), ch = i % (D / 8) * 8, at = tile * kRows + r;
       float x[8];
 #pragma unroll
@@ -576,6 +659,9 @@ struct Attention {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += from[e];
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (sm.nan[r * D + ch + e]) x[e] = __builtin_nanf("");
       const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
       float sum = 0.0f;
 #pragma unroll
@@ -596,7 +682,7 @@ struct Attention {
   }
 
   // Eight channels of an output row, and with the first of them its lse.
-  static __device__ void write_row(const AttnArgs& a, int64_t row, int ch, float (&x)[8], float top, float sum) {
+  __device__ __forceinline__ static void write_row(const AttnArgs& a, int64_t row, int ch, float (&x)[8], float top, float sum) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] / sum;
     store8<DT>(a.out, row * D + ch, 8, from_f32<DT>(x));
@@ -629,7 +715,7 @@ __device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
 
 // One workgroup for each problem.
 template <int DT, int FMT, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads) k_cache_attention(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attention(AttnArgs a) {
   using A = Attention<DT, FMT, D, MT>;
   __shared__ typename A::Shared sm;
   A x(a, sm);
@@ -637,50 +723,43 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention(AttnArgs a) {
   x.b = blockIdx.x / each;
   x.kv = (blockIdx.x - x.b * each) / a.d.row_tiles;
   x.tile = blockIdx.x % a.d.row_tiles;
-  x.w = work_of(a, x.b, A::kRows);
+  x.w = work_of_all(a, x.b, A::kRows);
   x.piece(0, x.tile < x.w.tiles ? x.w.steps : 0, true, nullptr);
 }
 
 // The steps of all problems shared out evenly: workgroup w takes those of share_of, a piece of a problem at a time.  A
 // problem that lies within one share is written here, the others' parts are joined by k_cache_attention_join.
 template <int DT, int FMT, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads) k_cache_attention_split(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attention_split(AttnArgs a) {
   using A = Attention<DT, FMT, D, MT>;
   __shared__ typename A::Shared sm;
   A x(a, sm);
   int total = 0;
   for (int b0 = 0; b0 < a.d.sequences; b0 += kAttnThreads) {
-    const int b = b0 + (int)threadIdx.x;
-    int units = 0, sum;
-    if (b < a.d.sequences) {
-      const Work w = work_of(a, b, A::kRows);
-      units = w.steps * w.tiles * a.d.kv_heads;
-    }
-    attn_scan(units, sm.sums, sum);
+    int sum;
+    attn_scan(units_of(a, b0 + (int)threadIdx.x, A::kRows), sm.sums, sum);
     total += sum;
   }
+  total = __builtin_amdgcn_readfirstlane(total);
   const int g = min(a.d.workgroups, total), me = blockIdx.x;
   if (me >= g) return;
   int u = share_of(me, total, g);
   const int end = share_of(me + 1, total, g);
   int base = 0;                     // steps of the sequences before b0
   for (int b0 = 0; u < end; b0 += kAttnThreads) {
-    const int b = b0 + (int)threadIdx.x;
-    int units = 0, sum;
-    if (b < a.d.sequences) {
-      const Work w = work_of(a, b, A::kRows);
-      units = w.steps * w.tiles * a.d.kv_heads;
-    }
-    const int below = attn_scan(units, sm.sums, sum);
+    int sum;
+    const int below = attn_scan(units_of(a, b0 + (int)threadIdx.x, A::kRows), sm.sums, sum);
+    sum = __builtin_amdgcn_readfirstlane(sum);
     sm.first[threadIdx.x] = base + below;
     __syncthreads();
     while (u < min(end, base + sum)) {
       int lo = 0;                   // the last sequence of the chunk that starts at or before u, and is not empty
       for (int s = kAttnThreads / 2; s > 0; s /= 2)
-        if (sm.first[lo + s] <= u) lo += s;
-      x.b = __builtin_amdgcn_readfirstlane(b0 + lo);
-      x.w = work_of(a, x.b, A::kRows);
-      const int local = u - sm.first[lo], problem = local / x.w.steps, step = local - problem * x.w.steps;
+        if (__builtin_amdgcn_readfirstlane(sm.first[lo + s]) <= u) lo += s;
+      x.b = b0 + lo;
+      x.w = work_of_all(a, x.b, A::kRows);
+      const int local = u - __builtin_amdgcn_readfirstlane(sm.first[lo]), problem = local / x.w.steps;
+      const int step = local - problem * x.w.steps;
       x.kv = problem / x.w.tiles;
       x.tile = problem - x.kv * x.w.tiles;
       const int n = min(x.w.steps - step, end - u);
@@ -703,15 +782,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
   const int b = blockIdx.x / each, kv = (blockIdx.x - b * each) / a.d.row_tiles, tile = blockIdx.x % a.d.row_tiles;
   int before = 0, all = 0;
   for (int s = threadIdx.x; s < a.d.sequences; s += kAttnThreads) {
-    const Work w = work_of(a, s, A::kRows);
-    const int units = w.steps * w.tiles * a.d.kv_heads;
+    const int units = units_of(a, s, A::kRows);
     all += units;
     if (s < b) before += units;
   }
   int total, first;
   attn_scan(all, sums, total);
   attn_scan(before, sums, first);
-  const Work w = work_of(a, b, A::kRows);
+  const Work w = work_of_all(a, b, A::kRows);
   const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
   const bool none = w.steps == 0 || tile >= w.tiles;
   int w0 = 0, w1 = 0;
