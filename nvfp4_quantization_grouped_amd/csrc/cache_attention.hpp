@@ -126,7 +126,7 @@ __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  return elem_bits<DT_BF16>(a) | elem_bits<DT_BF16>(b) << 16;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));     // one conversion of two
 }
 // The next bf16 part of eight values, which keep what is left.
 __device__ __forceinline__ bf16x8_t take_part(float (&x)[8], bool last) {
