@@ -128,15 +128,23 @@ __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));     // one conversion of two
 }
-// The next bf16 part of eight values, which keep what is left.
-__device__ __forceinline__ bf16x8_t take_part(float (&x)[8], bool last) {
+// (-1, 0) and (0, -1) in bf16.  Held in registers: the compiler makes 32-bit float constants of such literals, which a
+// dot product then misreads.
+struct MinusOne {
+  uint32_t lo = 0x0000BF80u, hi = 0xBF800000u;
+  __device__ __forceinline__ MinusOne() { asm("" : "+s"(lo), "+s"(hi)); }
+};
+// The next bf16 part of eight values, which keep what is left: exact, and one instruction a value as a dot product of a
+// pair.  (A NaN or an infinity takes its neighbour with it: both are of one row, whose sum is NaN.)
+__device__ __forceinline__ bf16x8_t take_part(float (&x)[8], bool last, const MinusOne& minus) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
     if (!last) {
-      x[2 * i] -= bf16_lo(w[i]);
-      x[2 * i + 1] -= bf16_hi(w[i]);
+      const bf16x2_t part = __builtin_bit_cast(bf16x2_t, w[i]);
+      x[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(part, __builtin_bit_cast(bf16x2_t, minus.lo), x[2 * i], false);
+      x[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(part, __builtin_bit_cast(bf16x2_t, minus.hi), x[2 * i + 1], false);
     }
   }
   return as_bf16x8(w[0], w[1], w[2], w[3]);
@@ -189,7 +197,16 @@ __device__ __forceinline__ int share_of(int w, int total, int g) { return (int)(
 __device__ __forceinline__ int owner_of(int u, int total, int g) { return (int)((((int64_t)u + 1) * g - 1) / total); }
 
 // Waves of a SIMD that the registers are kept to, which is workgroups of a CU.
-constexpr int attention_waves(int dim, int tiles) { return dim * tiles <= 128 ? 3 : dim * tiles <= 256 ? 2 : 1; }
+#ifndef W512
+#define W512 2
+#endif
+#ifndef W256
+#define W256 2
+#endif
+#ifndef W128
+#define W128 3
+#endif
+constexpr int attention_waves(int dim, int tiles) { return dim == 512 ? 1 : dim * tiles <= 128 ? W128 : dim*tiles <= 256 ? W256 : W512; }
 template <int D, int MT>
 constexpr int kWaves = attention_waves(D, MT);
 
@@ -202,12 +219,15 @@ struct Attention {
   using S = Shape<FMT, D>;
   static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kRows = 16 * MT;
   static constexpr int kTilesV = D / 16;
-  // q's fragments stay in registers up to 64 of them, else in LDS
-  static constexpr bool kQInRegs = D * QP * MT <= 512;
+  // q's fragments stay in registers up to 32 of them, else in LDS
+  static constexpr bool kQInRegs = D * QP * MT <= 256;
   static constexpr int kPad = D + 4;
   static constexpr int kQBytes = kQInRegs ? 0 : QP * kRows * D * 2;
-  static constexpr int kSumBytes = 4 * kRows * kPad * 4;
-  static constexpr int kLdsBytes = kQBytes > kSumBytes ? kQBytes : kSumBytes;
+  // the four waves' sums join in as many buffers as 34 KB hold, in turns
+  static constexpr int kBuffers = D * MT <= 128 ? 4 : D * MT <= 256 ? 2 : 1;
+  static constexpr int kSumBytes = kBuffers * kRows * kPad * 4;
+  static constexpr int kMarkBytes = kAttnThreads * S::VU * S::VW * 4;
+  static constexpr int kLdsBytes = kQBytes + kMarkBytes > kSumBytes ? kQBytes + kMarkBytes : kSumBytes;
 
   struct Shared {
     __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
@@ -221,6 +241,7 @@ struct Attention {
   Shared& sm;
   int lane, col, quarter;
   const int wave;
+  const MinusOne minus;
   // the problem
   int b, kv, tile;
   Work w;
@@ -254,7 +275,7 @@ struct Attention {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = -x[i];
 #pragma unroll
-    for (int p = 0; p < QP; ++p) part[p] = take_part(x, p == QP - 1);
+    for (int p = 0; p < QP; ++p) part[p] = take_part(x, p == QP - 1, minus);
   }
   struct Q {
     bf16x8_t f[kQInRegs ? MT : 1][kQInRegs ? S::kSteps : 1][QP];
@@ -320,7 +341,7 @@ struct Attention {
       const uint8_t* scales = a.k_scales + row * blocks;
 #pragma unroll
       for (int u = 0; u < S::KU; ++u) {
-        const uint8_t* at = codes + col * S::kRowBytes + (u * 4 + quarter) * S::KW * 4;
+        const uint8_t* at = codes + (uint32_t)(col * S::kRowBytes + quarter * S::KW * 4) + u * S::KW * 16;
         if constexpr (S::KW == 4) {
           const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at);
           k.w[h][u][0] = v.x; k.w[h][u][1] = v.y; k.w[h][u][2] = v.z; k.w[h][u][3] = v.w;
@@ -330,7 +351,7 @@ struct Attention {
         }
 #pragma unroll
         for (int i = 0; i < S::KS; ++i)
-          k.s[h][u][i] = scales[col * blocks + (((u * 4 + quarter) * S::KC + i * 16) >> a.block_shift)];
+          k.s[h][u][i] = scales[(uint32_t)(col * blocks + (((u * 4 + quarter) * S::KC + i * 16) >> a.block_shift))];
       }
     }
   }
@@ -341,10 +362,9 @@ struct Attention {
       const int64_t row = pool_row(p, t, j / 4);
       const uint8_t* codes = a.v_codes + row * S::kRowBytes;
       const uint8_t* scales = a.v_scales + row * blocks;
-      const int r = quarter * 4 + j % 4;
 #pragma unroll
       for (int u = 0; u < S::VU; ++u) {
-        const uint8_t* at = codes + r * S::kRowBytes + u * 16 * S::VB + col * S::VB;
+        const uint8_t* at = codes + (uint32_t)(quarter * 4 * S::kRowBytes + col * S::VB) + (j % 4 * S::kRowBytes + u * 16 * S::VB);
         if constexpr (S::VB == 2) v.w[j][u][0] = *reinterpret_cast<const uint16_t*>(at);
         else if constexpr (S::VB == 4) v.w[j][u][0] = *reinterpret_cast<const uint32_t*>(at);
         else if constexpr (S::VB == 8) {
@@ -356,7 +376,7 @@ struct Attention {
         }
 #pragma unroll
         for (int i = 0; i < S::VS; ++i)
-          v.s[j][u][i] = scales[r * blocks + ((u * 16 * S::VC + col * S::VC + i * 16) >> a.block_shift)];
+          v.s[j][u][i] = (scales + j % 4 * blocks)[(uint32_t)(quarter * 4 * blocks + ((u * 16 * S::VC + col * S::VC + i * 16) >> a.block_shift))];
       }
     }
   }
@@ -507,23 +527,27 @@ struct Attention {
       }
     }
     if (__ballot(any != 0) == 0) return;
-    // the marks, in loops over words that lie in LDS
-    constexpr int kWords = 8 * S::VU * S::VW, kCodes = S::VC / S::VW;
-    static_assert(kQBytes + kAttnThreads * kWords * 4 <= kLdsBytes, "the marks' words lie behind q's fragments");
+    // the marks, a position at a time, in a loop over its codes, whose words lie in LDS behind q's fragments
+    constexpr int kWords = S::VU * S::VW, kCodes = S::VC / S::VW;
     uint32_t* words = reinterpret_cast<uint32_t*>(sm.big + kQBytes) + (wave * 64 + lane) * kWords;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) words[i] = bad[i / (S::VU * S::VW)][i / S::VW % S::VU][i % S::VW];
-#pragma unroll 1
-    for (int i = 0; i < kWords * kCodes; ++i) {
-      const int word = i / kCodes, code = i - word * kCodes, j = word / (S::VU * S::VW);
-      const uint64_t all = __ballot(words[word] >> (code * kBits + kBits - 1) & 1u);
-      // the quarter's lanes hold this channel of their units, and the rows of the same positions
-      for (uint32_t lanes = (uint32_t)(all >> (quarter * 16)) & 0xFFFFu; lanes != 0; lanes &= lanes - 1) {
-        const int unit = word / S::VW % S::VU, in_unit = (word % S::VW) * kCodes + code;
-        const int channel = unit * 16 * S::VC + __builtin_ctz(lanes) * S::VC + in_unit;
+    for (int j = 0; j < 8; ++j) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          if (may[mt] >> j & 1) sm.nan[(mt * 16 + col) * D + channel] = 1;
+      for (int i = 0; i < kWords; ++i) words[i] = bad[j][i / S::VW][i % S::VW];
+      bool sees[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) sees[mt] = may[mt] >> j & 1;
+#pragma unroll 1
+      for (int i = 0; i < kWords * kCodes; ++i) {
+        const int word = i / kCodes, code = i - word * kCodes;
+        const uint64_t all = __ballot(words[word] >> (code * kBits + kBits - 1) & 1u);
+        // the quarter's lanes hold this channel of their units, and the rows of the same positions
+        for (uint32_t lanes = (uint32_t)(all >> (quarter * 16)) & 0xFFFFu; lanes != 0; lanes &= lanes - 1) {
+          const int channel = word / S::VW * 16 * S::VC + __builtin_ctz(lanes) * S::VC + word % S::VW * kCodes + code;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            if (sees[mt]) sm.nan[(mt * 16 + col) * D + channel] = 1;
+        }
       }
     }
   }
@@ -595,7 +619,7 @@ struct Attention {
             l[mt] += e[i];
           }
 #pragma unroll
-          for (int part = 0; part < PP; ++part) p[mt][part] = take_part(e, part == PP - 1);
+          for (int part = 0; part < PP; ++part) p[mt][part] = take_part(e, part == PP - 1, minus);
         }
         passes = passes_of(v.w, v.s);
         for (int pass = 0;;) {
@@ -627,24 +651,31 @@ struct Attention {
     }
     __syncthreads();
     float* sums = reinterpret_cast<float*>(sm.big);
+#pragma unroll 1
+    for (int turn = 0; turn < 4 / kBuffers; ++turn) {
+      if (turn > 0) __syncthreads();
+      if (wave / kBuffers != turn) continue;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = mt * 16 + col;
-      const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
-      const float keep = m[mt] == -__builtin_inff() ? (l[mt] == 0.0f ? 0.0f : l[mt])   // nothing met, or NaN alone
-                                                    : __builtin_amdgcn_exp2f(m[mt] - top);
-      float* row = sums + (wave * kRows + r) * kPad;
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 16 + col;
+        const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+        const float keep = m[mt] == -__builtin_inff() ? (l[mt] == 0.0f ? 0.0f : l[mt])   // nothing met, or NaN alone
+                                                      : __builtin_amdgcn_exp2f(m[mt] - top);
+        float* row = sums + (wave % kBuffers * kRows + r) * kPad;
 #pragma unroll
-      for (int u = 0; u < S::VU; ++u)
+        for (int u = 0; u < S::VU; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int c = 0; c < S::VC; c += 4) {
-            f32x4_t x;
+            for (int c = 0; c < S::VC; c += 4) {
+              f32x4_t x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = o[mt][u * S::VC + c + e][i] * keep;
-            *reinterpret_cast<f32x4_t*>(row + u * 16 * S::VC + (quarter * 4 + i) * S::VC + c) = x;
-          }
+              for (int e = 0; e < 4; ++e) x[e] = o[mt][u * S::VC + c + e][i] * keep;
+              f32x4_t* at = reinterpret_cast<f32x4_t*>(row + u * 16 * S::VC + (quarter * 4 + i) * S::VC + c);
+              if (turn > 0) x += *at;
+              *at = x;
+            }
+      }
     }
     __syncthreads();
     const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
@@ -654,7 +685,7 @@ struct Attention {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = 0.0f;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < kBuffers; ++s) {
         const float* from = sums + (s * kRows + r) * kPad + ch;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += from[e];
@@ -773,26 +804,39 @@ __global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attenti
   }
 }
 
-// The parts of problems that several workgroups worked on, four rows to a workgroup; and zeros for those that none did.
+// The parts of problems that several workgroups worked on; and zeros for those that none did.  A workgroup takes 64 groups
+// of 8 channels, a lane each, and its waves take turns at the parts, so that a wave has a few parts' loads under way at a
+// time (a lane that took them one after another made 12 us of 16 parts).
 template <int DT, int FMT, int D, int MT>
 __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs a) {
   using A = Attention<DT, FMT, D, MT>;
-  __shared__ int sums[4];
+  __shared__ int counts[4][2];
+  __shared__ float sums[4][64][10];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int each = a.d.kv_heads * a.d.row_tiles;
   const int b = blockIdx.x / each, kv = (blockIdx.x - b * each) / a.d.row_tiles, tile = blockIdx.x % a.d.row_tiles;
   int before = 0, all = 0;
   for (int s = threadIdx.x; s < a.d.sequences; s += kAttnThreads) {
     const int units = units_of(a, s, A::kRows);
     all += units;
-    if (s < b) before += units;
+    before += s < b ? units : 0;
   }
-  int total, first;
-  attn_scan(all, sums, total);
-  attn_scan(before, sums, first);
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    all += __shfl_xor(all, s);
+    before += __shfl_xor(before, s);
+  }
+  if (lane == 0) {
+    counts[wave][0] = all;
+    counts[wave][1] = before;
+  }
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(counts[0][0] + counts[1][0] + counts[2][0] + counts[3][0]);
+  int first = __builtin_amdgcn_readfirstlane(counts[0][1] + counts[1][1] + counts[2][1] + counts[3][1]);
   const Work w = work_of_all(a, b, A::kRows);
   const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
   const bool none = w.steps == 0 || tile >= w.tiles;
-  int w0 = 0, w1 = 0;
+  int w0 = 0, w1 = -1;
   const int g = min(a.d.workgroups, total);
   if (!none) {
     first += (kv * w.tiles + tile) * w.steps;
@@ -800,33 +844,59 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
     w1 = owner_of(first + w.steps - 1, total, g);
     if (w0 == w1) return;
   }
-  for (int i = threadIdx.x; i < 4 * (D / 8); i += kAttnThreads) {
-    const int r = blockIdx.y * 4 + i / (D / 8), ch = i % (D / 8) * 8, at = tile * A::kRows + r;
-    if (at >= rows) continue;
-    float x[8] = {}, top = -__builtin_inff(), sum = 0.0f;
-    if (!none && at < live) {
-      for (int s = w0; s <= w1; ++s) {
-        const float* slot = a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<MT, D>;
-        top = fmaxf(top, slot[A::kRows * D + r]);
-      }
-      for (int s = w0; s <= w1; ++s) {
-        const float* slot = a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<MT, D>;
-        const float m = slot[A::kRows * D + r], l = slot[A::kRows * D + A::kRows + r];
-        const float keep = m == -__builtin_inff() ? (l == 0.0f ? 0.0f : l) : __builtin_amdgcn_exp2f(m - top);
-        sum += m == -__builtin_inff() ? l : l * keep;
+  const int r = blockIdx.y * (512 / D) + lane / (D / 8), ch = lane % (D / 8) * 8, at = tile * A::kRows + r;
+  const bool wanted = at < rows;
+  float x[8] = {}, top = -__builtin_inff(), sum = 0.0f;
+  if (wanted && at < live) {
+    auto slot_of = [&](int s) { return a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<MT, D>; };
+#pragma unroll 4
+    for (int s = w0 + wave; s <= w1; s += 4) top = fmaxf(top, slot_of(s)[A::kRows * D + r]);
+#pragma unroll 2
+    for (int s = w0 + wave; s <= w1; s += 4) {
+      const float* slot = slot_of(s);
+      const float m = slot[A::kRows * D + r], l = slot[A::kRows * D + A::kRows + r];
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(slot + r * D + ch);
+      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(slot + r * D + ch + 4);
+      // nothing met, or NaN alone: l is 0 or NaN
+      const float keep = m == -__builtin_inff() ? l : __builtin_amdgcn_exp2f(m - top);
+      sum += m == -__builtin_inff() ? l : l * keep;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += slot[r * D + ch + e] * keep;
+      for (int e = 0; e < 4; ++e) {
+        x[e] += lo[e] * keep;
+        x[4 + e] += hi[e] * keep;
       }
     }
-    const int t = at / a.d.group;
-    A::write_row(a, ((int64_t)b * a.d.tokens + t) * a.d.heads + kv * a.d.group + (at - t * a.d.group), ch, x, top, sum);
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[wave][lane][e] = x[e];
+  sums[wave][lane][8] = top;
+  sums[wave][lane][9] = sum;
+  __syncthreads();
+  if (wave != 0 || !wanted) return;
+  float best = -__builtin_inff(), whole = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) best = fmaxf(best, sums[s][lane][8]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const float m = sums[s][lane][8], l = sums[s][lane][9];
+    const float keep = m == -__builtin_inff() ? l : __builtin_amdgcn_exp2f(m - best);
+    whole += m == -__builtin_inff() ? l : l * keep;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += sums[s][lane][e] * keep;
+  }
+  const int t = at / a.d.group;
+  A::write_row(a, ((int64_t)b * a.d.tokens + t) * a.d.heads + kv * a.d.group + (at - t * a.d.group), ch, x, best, whole);
 }
 
 // Rows of a wave's tile, in 16s: as many as the problem has, while the sums fit the registers.
 inline int attention_row_tiles(int dt, int dim, int64_t rows) {
   const int most = dim <= 128 ? (dt == DT_BF16 ? 4 : 2) : dim == 256 ? 2 : 1;
-  const int want = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+#ifndef MTMAX
+#define MTMAX 2
+#endif
+  const int want = rows <= 16 ? 1 : rows <= 32 || MTMAX == 2 ? 2 : 4;
   return want < most ? want : most;
 }
 
@@ -836,7 +906,7 @@ hipError_t launch_attention_of(const AttnArgs& a, int64_t problems, hipStream_t 
     k_cache_attention<DT, FMT, D, MT><<<(unsigned)problems, kAttnThreads, 0, st>>>(a);
   } else {
     k_cache_attention_split<DT, FMT, D, MT><<<(unsigned)a.d.workgroups, kAttnThreads, 0, st>>>(a);
-    k_cache_attention_join<DT, FMT, D, MT><<<dim3((unsigned)problems, 4 * MT), kAttnThreads, 0, st>>>(a);
+    k_cache_attention_join<DT, FMT, D, MT><<<dim3((unsigned)problems, 16 * MT * D / 512), kAttnThreads, 0, st>>>(a);
   }
   return hipGetLastError();
 }
