@@ -11,8 +11,20 @@ constexpr int64_t kManyProblems = 2048;
 // Problems of so many steps at most are not worth sharing.
 constexpr int64_t kFewSteps = 4;
 
+hipError_t kernels(const AttnArgs* a, int dt, int fmt, int dim, int rows, int64_t problems, AttnShape* shape,
+                   hipStream_t st) {
+#define FORMATS(DT)                                                                                           \
+  if (fmt == FMT_FP8) return attention_kernels<DT, FMT_FP8>(a, dim, rows, problems, shape, st);               \
+  if (fmt == FMT_MXFP4) return attention_kernels<DT, FMT_MXFP4>(a, dim, rows, problems, shape, st);           \
+  return attention_kernels<DT, FMT_NVFP4>(a, dim, rows, problems, shape, st)
+  if (dt == DT_F32) { FORMATS(DT_F32); }
+  if (dt == DT_BF16) { FORMATS(DT_BF16); }
+  FORMATS(DT_F16);
+#undef FORMATS
+}
+
 struct Plan {
-  int tiles;              // MT
+  int rows;               // of a tile
   int row_tiles;
   int64_t problems;
   int workgroups;         // 0: one for each problem
@@ -20,12 +32,14 @@ struct Plan {
 Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64_t tokens, int64_t heads) {
   const int64_t rows = tokens * (heads / c.kv_heads);
   Plan p;
-  p.tiles = attention_row_tiles(dt, c.head_dim, rows);
-  p.row_tiles = (int)((rows + 16 * p.tiles - 1) / (16 * p.tiles));
+  p.rows = attention_rows(c.head_dim, rows);
+  p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   p.problems = sequences * c.kv_heads * p.row_tiles;
-  const int64_t steps = (width * c.page_size + kStep - 1) / kStep;
+  AttnShape shape = {128, 1};
+  (void)kernels(nullptr, dt, c.fmt, c.head_dim, p.rows, 0, &shape, nullptr);
+  const int64_t steps = (width * c.page_size + shape.step - 1) / shape.step;
   const bool split = p.problems < kManyProblems && steps > kFewSteps && p.problems * steps < (int64_t(1) << 31);
-  p.workgroups = split ? kComputeUnits * attention_waves(c.head_dim, p.tiles) : 0;
+  p.workgroups = split ? kComputeUnits * shape.waves : 0;
   return p;
 }
 
@@ -34,7 +48,7 @@ Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64
 int64_t attention_workspace_bytes(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64_t tokens,
                                   int64_t heads) {
   const Plan p = plan_of(c, sequences, width, dt, tokens, heads);
-  return (int64_t)p.workgroups * 2 * 16 * p.tiles * (c.head_dim + 2) * 4;
+  return (int64_t)p.workgroups * 2 * p.rows * (c.head_dim + 2) * 4;
 }
 
 hipError_t launch_cache_attention(const CacheArgs& c, const TableArgs& t, const AttentionArgs& x, int dt,
@@ -46,16 +60,7 @@ hipError_t launch_cache_attention(const CacheArgs& c, const TableArgs& t, const 
   a.d = {t.sequences, x.tokens, x.heads, x.heads / c.kv_heads, c.kv_heads, t.width, log2_of(c.page_size), p.row_tiles,
          p.workgroups, x.mask_each, c.pages, fmaxf((float)(fabs((double)x.scale) * 1.4426950408889634), 0x1p-149f),
          x.scale < 0};
-#define CALL(DT, FMT) return launch_attention_kernels<DT, FMT>(a, c.head_dim, p.tiles, p.problems, st)
-#define FORMATS(DT)                        \
-  if (c.fmt == FMT_FP8) CALL(DT, FMT_FP8); \
-  if (c.fmt == FMT_MXFP4) CALL(DT, FMT_MXFP4); \
-  CALL(DT, FMT_NVFP4)
-  if (dt == DT_F32) { FORMATS(DT_F32); }
-  if (dt == DT_BF16) { FORMATS(DT_BF16); }
-  FORMATS(DT_F16);
-#undef FORMATS
-#undef CALL
+  return kernels(&a, dt, c.fmt, c.head_dim, p.rows, p.problems, nullptr, st);
 }
 
 }  // namespace mxq

@@ -38,12 +38,11 @@ typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 
 constexpr int kAttnThreads = 256;
 constexpr int kTile = 32;                    // positions of a wave's tile
-constexpr int kStep = 4 * kTile;             // of a workgroup's step
 constexpr float kLazy = 8.0f;                // log2 units that a score may exceed the running maximum by
 
 struct AttnDims {
   int sequences, tokens, heads, group, kv_heads, width, page_shift;
-  int row_tiles;        // tiles of 16 * MT rows of a sequence and kv head, all tokens counted
+  int row_tiles;        // tiles of a kernel's rows of a sequence and kv head, all tokens counted
   int workgroups;       // that share the steps (split), or 0: one workgroup for each problem
   bool mask_each;
   int64_t pages;
@@ -119,6 +118,14 @@ __device__ __forceinline__ float scale_in_pass(float s, int pass) {
   return e != 255u && (u >> (23 - pass) & 1u) ? as_f32((e - pass) << 23) : 0.0f;
 }
 
+// The least code (by size) that is not finite in bf16 under a scale byte; one past the largest where all are.
+template <int FMT>
+__device__ __forceinline__ int least_odd(int e) {
+  if constexpr (FMT == FMT_NVFP4) return (e & 0x7F) == 0x7F ? 0 : 8;
+  else if constexpr (FMT == FMT_FP8) return e == 255 ? 0 : min(127, max(262 - e, 0) << 3);   // code 0x7F is NaN itself
+  else return e == 255 ? 0 : min(8, max(256 - e, 0) << 1);
+}
+
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8_t, u32x4_t{a, b, c, d});
 }
@@ -167,28 +174,31 @@ __device__ __forceinline__ int uniform_load(const int32_t* p, int64_t i) {
 }
 
 // --------------------------------------------------------------- the schedule
-// A problem is a sequence, a kv head and a tile of rows; its work is its steps of kStep positions.
+// A problem is a sequence, a kv head and a tile of A::kRows rows; its work is its steps of A::kStep positions.
 struct Work {
   int known, end, count;     // cached positions, those and the drafted ones, tokens that are no padding
   int steps, tiles;          // of each problem; row tiles that hold such a token
 };
-__device__ __forceinline__ Work work_of(const AttnArgs& a, int length, int count, int rows) {
+template <class A>
+__device__ __forceinline__ Work work_of(const AttnArgs& a, int length, int count) {
   Work w;
   w.known = cached_positions(length, a.d.width, 1 << a.d.page_shift);
   w.count = min(max(count, 0), a.d.tokens);
   w.end = w.count > 0 ? min(w.known + w.count, a.d.width << a.d.page_shift) : 0;
-  w.steps = (w.end + kStep - 1) / kStep;
-  w.tiles = (w.count * a.d.group + rows - 1) / rows;
+  w.steps = (w.end + A::kStep - 1) / A::kStep;
+  w.tiles = (w.count * a.d.group + A::kRows - 1) / A::kRows;
   return w;
 }
 // Of a sequence that the whole workgroup works on, in scalar registers.
-__device__ __forceinline__ Work work_of_all(const AttnArgs& a, int b, int rows) {
-  return work_of(a, uniform_load(a.lengths, b), a.counts ? uniform_load(a.counts, b) : a.d.tokens, rows);
+template <class A>
+__device__ __forceinline__ Work work_of_all(const AttnArgs& a, int b) {
+  return work_of<A>(a, uniform_load(a.lengths, b), a.counts ? uniform_load(a.counts, b) : a.d.tokens);
 }
 // Steps of a thread's sequence, all its problems together.
-__device__ __forceinline__ int units_of(const AttnArgs& a, int b, int rows) {
+template <class A>
+__device__ __forceinline__ int units_of(const AttnArgs& a, int b) {
   if (b >= a.d.sequences) return 0;
-  const Work w = work_of(a, a.lengths[b], a.counts ? a.counts[b] : a.d.tokens, rows);
+  const Work w = work_of<A>(a, a.lengths[b], a.counts ? a.counts[b] : a.d.tokens);
   return w.steps * w.tiles * a.d.kv_heads;
 }
 // Steps [first, last) of all problems' that workgroup w of g takes.
@@ -196,29 +206,90 @@ __device__ __forceinline__ int share_of(int w, int total, int g) { return (int)(
 // The workgroup that takes step u.
 __device__ __forceinline__ int owner_of(int u, int total, int g) { return (int)((((int64_t)u + 1) * g - 1) / total); }
 
-// Waves of a SIMD that the registers are kept to, which is workgroups of a CU.
-#ifndef W512
-#define W512 2
-#endif
-#ifndef W256
-#define W256 2
-#endif
-#ifndef W128
-#define W128 3
-#endif
-constexpr int attention_waves(int dim, int tiles) { return dim == 512 ? 1 : dim * tiles <= 128 ? W128 : dim*tiles <= 256 ? W256 : W512; }
-template <int D, int MT>
-constexpr int kWaves = attention_waves(D, MT);
+// A part of a problem that several workgroups share: sums [rows][D], then m and l [rows].
+template <class A>
+constexpr int64_t kSlotFloats = (int64_t)A::kRows * (A::kDim + 2);
 
-template <int MT, int D>
-constexpr int kSlotFloats = 16 * MT * (D + 2);
+// Eight (or four) channels of an output row, and with the first of them its lse.
+template <int DT, int N>
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t row, int dim, int ch, const float (&sums)[N], float top,
+                                          float sum) {
+  float x[8] = {};
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = sum == 0.0f ? 0.0f : sums[e] / sum;
+  const Raw8<DT> r = from_f32<DT>(x);
+  uint8_t* at = a.out + (row * dim + ch) * kElemBytes<DT>;
+  if constexpr (N == 8) store8<DT>(at, 0, 8, r);
+  else if constexpr (DT == DT_F32) *reinterpret_cast<u32x4_t*>(at) = u32x4_t{r.w[0], r.w[1], r.w[2], r.w[3]};
+  else *reinterpret_cast<u32x2_t*>(at) = u32x2_t{r.w[0], r.w[1]};
+  if (a.lse && ch == 0)
+    a.lse[row] = sum == 0.0f ? -__builtin_inff()
+                 : top == -__builtin_inff() ? sum : __builtin_fmaf(top, 0x1.62e430p-1f, logf(sum));
+}
+
+// Which positions of tile t each row attends to (a bit each, in the lane's order), the scores of the others -inf.
+// row0: this lane's row of the first 16.
+template <int MT>
+__device__ __forceinline__ void mask_scores(const AttnArgs& a, const Work& w, int b, int t, bool there0, bool there1,
+                                            int row0, int quarter, f32x4_t (&s)[MT][2], uint32_t (&may)[MT]) {
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int token = (row0 + mt * 16) / a.d.group;
+    const uint8_t* see = a.mask ? a.mask + ((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens +
+                                            min(token, a.d.tokens - 1)) * a.d.tokens : nullptr;
+    may[mt] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int pos = t * kTile + (i / 4) * 16 + quarter * 4 + i % 4, j = pos - w.known;
+      bool ok = j <= token;
+      if (see) ok = j < 0 || see[min(max(j, 0), a.d.tokens - 1)] != 0;
+      ok = ok && (i < 4 ? there0 : there1) && pos < w.end && token < w.count;
+      may[mt] |= (uint32_t)ok << i;
+      s[mt][i / 4][i % 4] = ok ? s[mt][i / 4][i % 4] : -__builtin_inff();
+    }
+  }
+}
+
+// Probabilities of a tile's scores in bf16 parts, and the rows' running maximum m, sum l and sums o.
+template <int MT, int PP, int NT>
+__device__ __forceinline__ void softmax_step(const f32x4_t (&s)[MT][2], float scale, const MinusOne& minus, float (&m)[MT],
+                                             float (&l)[MT], f32x4_t (&o)[MT][NT], bf16x8_t (&p)[MT][PP]) {
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = s[mt][i / 4][i % 4];
+    float top = e[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, e[i]);
+    top *= scale;
+    if (__ballot(top > m[mt] + kLazy) != 0) {
+      const float to = fmaxf(m[mt], row_max(top));
+      const float keep = m[mt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[mt] - to);
+      m[mt] = to;
+      l[mt] *= keep;
+#pragma unroll
+      for (int c = 0; c < NT; ++c) o[mt][c] *= keep;
+    }
+    const float sub = m[mt] == -__builtin_inff() ? 0.0f : m[mt];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[i], scale, -sub));
+      l[mt] += e[i];
+    }
+#pragma unroll
+    for (int part = 0; part < PP; ++part) p[mt][part] = take_part(e, part == PP - 1, minus);
+  }
+}
 
 // ------------------------------------------------------------------ one piece
 template <int DT, int FMT, int D, int MT>
 struct Attention {
   using S = Shape<FMT, D>;
-  static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kRows = 16 * MT;
-  static constexpr int kTilesV = D / 16;
+  static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
+  static constexpr int kTilesV = D / 16, kType = DT;
+  // waves of a SIMD that the registers are kept to, which is workgroups of a CU
+  static constexpr int kWaves = D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
   // q's fragments stay in registers up to 32 of them, else in LDS
   static constexpr bool kQInRegs = D * QP * MT <= 256;
   static constexpr int kPad = D + 4;
@@ -479,22 +550,7 @@ struct Attention {
   // NaN is NaN) and is marked for those rows, whose sums are NaN in the end.
   __device__ __forceinline__ void mask(const Pages& now, int t, f32x4_t (&s)[MT][2], V& v) const {
     uint32_t may[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int token = row_of(mt) / a.d.group;
-      const uint8_t* see = a.mask ? a.mask + ((int64_t)(a.d.mask_each ? b : 0) * a.d.tokens +
-                                              min(token, a.d.tokens - 1)) * a.d.tokens : nullptr;
-      may[mt] = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int pos = t * kTile + (i / 4) * 16 + quarter * 4 + i % 4, j = pos - w.known;
-        bool ok = j <= token;
-        if (see) ok = j < 0 || see[min(max(j, 0), a.d.tokens - 1)] != 0;
-        ok = ok && now.there[i / 4] && pos < w.end && token < w.count;
-        may[mt] |= (uint32_t)ok << i;
-        s[mt][i / 4][i % 4] = ok ? s[mt][i / 4][i % 4] : -__builtin_inff();
-      }
-    }
+    mask_scores<MT>(a, w, b, t, now.there[0], now.there[1], row_of(0), quarter, s, may);
     // codes whose value is not finite: from `least` on (by size), which the scale says
     constexpr uint32_t kOnes = S::kFp8 ? 0x01010101u : 0x11111111u, kTop = S::kFp8 ? 0x80808080u : 0x88888888u;
     constexpr int kBits = S::kFp8 ? 8 : 4, kHalf = 1 << (kBits - 1);
@@ -508,11 +564,7 @@ struct Attention {
         uint32_t more[S::VS];         // kHalf - least
 #pragma unroll
         for (int i = 0; i < S::VS; ++i) {
-          const int e = v.s[j][u][i];
-          int least;
-          if constexpr (FMT == FMT_NVFP4) least = (e & 0x7F) == 0x7F ? 0 : 8;
-          else if constexpr (S::kFp8) least = e == 255 ? 0 : min(127, max(262 - e, 0) << 3);   // 0x7F is NaN by itself
-          else least = e == 255 ? 0 : min(8, max(256 - e, 0) << 1);
+          const int least = least_odd<FMT>(v.s[j][u][i]);
           more[i] = none ? 0u : (kHalf - least) * kOnes;
           v.s[j][u][i] = none || least == 0 ? (FMT == FMT_NVFP4 ? 0x38u : 127u) : v.s[j][u][i];
         }
@@ -560,13 +612,13 @@ struct Attention {
     Q q;
     load_q(q);
     f32x4_t o[MT][kTilesV];
-    float m[MT], sub[MT], l[MT];
+    float m[MT], l[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int t = 0; t < kTilesV; ++t) o[mt][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       m[mt] = -__builtin_inff();
-      sub[mt] = l[mt] = 0.0f;
+      l[mt] = 0.0f;
     }
     __syncthreads();
     int t = first * 4 + wave;
@@ -595,32 +647,7 @@ struct Attention {
         const Pages after = pages_of(beyond);
         if (!(now.there[0] && now.there[1] && (t + 1) * kTile <= w.known)) mask(now, t, s, v);
         bf16x8_t p[MT][PP];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float e[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = s[mt][i / 4][i % 4];
-          float top = e[0];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) top = fmaxf(top, e[i]);
-          top *= a.d.scale;
-          if (__ballot(top > m[mt] + kLazy) != 0) {
-            const float to = fmaxf(m[mt], row_max(top));
-            const float keep = m[mt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[mt] - to);
-            m[mt] = to;
-            sub[mt] = to == -__builtin_inff() ? 0.0f : to;
-            l[mt] *= keep;
-#pragma unroll
-            for (int c = 0; c < kTilesV; ++c) o[mt][c] *= keep;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[i], a.d.scale, -sub[mt]));
-            l[mt] += e[i];
-          }
-#pragma unroll
-          for (int part = 0; part < PP; ++part) p[mt][part] = take_part(e, part == PP - 1, minus);
-        }
+        softmax_step<MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
         passes = passes_of(v.w, v.s);
         for (int pass = 0;;) {
           values(v, p, pass, passes, o);
@@ -707,19 +734,352 @@ struct Attention {
           slot[kRows * D + kRows + r] = sum;
         }
       } else if (at < rows) {
-        write_row(a, row_at(at), ch, x, top, at < live ? sum : 0.0f);
+        write_row<DT, 8>(a, row_at(at), D, ch, x, top, at < live ? sum : 0.0f);
       }
     }
   }
+};
 
-  // Eight channels of an output row, and with the first of them its lse.
-  __device__ __forceinline__ static void write_row(const AttnArgs& a, int64_t row, int ch, float (&x)[8], float top, float sum) {
+// ------------------------------------------------------- rows of its own to each wave
+// The same products where there are more rows than a wave holds: the workgroup decodes a step's keys and values once, a
+// quarter to each wave, into LDS as the fragments that the products take, and each wave takes all of them for 16 * MT rows
+// of its own.  Decoding costs four times less a row than where each wave decodes what it reads, and needs no registers
+// beside the sums.  LDS holds one step (64 KB); two workgroups of a CU take turns at decoding and products.
+template <int DT, int FMT, int D, int MT>
+struct SharedAttention {
+  using S = Shape<FMT, D>;
+  static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kDim = D, kType = DT;
+  static constexpr int kTilesV = D / 16, kRows = 64 * MT;
+  static constexpr int kStep = D <= 128 ? 128 : 16384 / D, kTiles = kStep / kTile;
+  // two workgroups of a CU where q and the sums leave the registers for it
+  static constexpr int kWaves = MT * (D / 8 * QP + D / 4) <= 192 ? 2 : 1;
+  // a wave's quarter of a step: tile `part`, and of that
+  static constexpr int kPartsOfTile = 4 / kTiles;
+  static constexpr int kHalves = kPartsOfTile > 1 ? 1 : 2;             // halves of its positions for the keys
+  static constexpr int kUnits = kPartsOfTile > 2 ? S::KU / 2 : S::KU;  // units of them
+  static constexpr int VC = D / 16 < 8 ? D / 16 : 8;                   // channels of a lane for the values, of all positions
+  static constexpr int VB = S::kFp8 ? VC : VC / 2, VW = VB < 4 ? 1 : VB / 4;
+  static constexpr int kWords = D / 32;                                // of a row's marks
+
+  struct Shared {
+    __attribute__((aligned(16))) u32x4_t key[kTiles][2][S::kSteps][64];
+    __attribute__((aligned(16))) u32x4_t value[kTiles][kTilesV][64];
+    uint32_t odd[kStep][kWords];          // channels of a position whose value is not finite
+    uint32_t nan[kRows][kWords];          // outputs that one reached
+    int marked;                           // the step that `odd` is of
+    int first[kAttnThreads + 1];
+    int sums[4];
+  };
+
+  const AttnArgs& a;
+  Shared& sm;
+  int lane, col, quarter;
+  const int wave;
+  const MinusOne minus;
+  int b, kv, tile;
+  Work w;
+
+  __device__ __forceinline__ SharedAttention(const AttnArgs& args, Shared& shared)
+      : a(args), sm(shared), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
+    place();
+  }
+  __device__ __forceinline__ void place() {
+    lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    col = lane & 15;
+    quarter = lane >> 4;
+  }
+  __device__ __forceinline__ int row_of(int mt) const { return tile * kRows + (wave * MT + mt) * 16 + col; }
+  __device__ __forceinline__ int64_t row_at(int r) const {
+    const int i = r / a.d.group, g = r - i * a.d.group;
+    return (((int64_t)b * a.d.tokens + i) * a.d.heads + kv * a.d.group + g);
+  }
+
+  // ----- this wave's quarter of a step
+  __device__ __forceinline__ int my_tile(int step) const { return step * kTiles + wave / kPartsOfTile; }
+  __device__ __forceinline__ int my_half() const { return kPartsOfTile > 1 ? wave % 2 : 0; }
+  __device__ __forceinline__ int my_unit() const { return kPartsOfTile > 2 ? wave / 2 * kUnits : 0; }
+  __device__ __forceinline__ int my_channels() const { return kPartsOfTile > 1 ? wave % kPartsOfTile : 0; }   // 128 of them
+  struct Raw {
+    uint32_t k[kHalves][kUnits][S::KW], ks[kHalves][kUnits][S::KS];
+    uint32_t v[8][VW], vs[8];
+    bool there[2];
+  };
+  __device__ __forceinline__ void load(Raw& x, int step) const {
+    const int t = my_tile(step), blocks = D >> a.block_shift;
+    int64_t row[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] / sum;
-    store8<DT>(a.out, row * D + ch, 8, from_f32<DT>(x));
-    if (a.lse && ch == 0)
-      a.lse[row] = sum == 0.0f ? -__builtin_inff()
-                   : top == -__builtin_inff() ? sum : __builtin_fmaf(top, 0x1.62e430p-1f, logf(sum));
+    for (int h = 0; h < 2; ++h) {
+      const int pos = t * kTile + h * 16, slot = pos >> a.d.page_shift;
+      const int page = uniform_load(a.table, (int64_t)b * a.d.width + min(slot, a.d.width - 1));
+      x.there[h] = slot < a.d.width && (uint32_t)page < (uint32_t)a.d.pages;
+      row[h] = (((int64_t)(x.there[h] ? page : 0) * a.d.kv_heads + kv) << a.d.page_shift) +
+               (pos & ((1 << a.d.page_shift) - 1));
+    }
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int64_t r = kHalves == 2 ? row[h] : my_half() ? row[1] : row[0];
+      const uint8_t* codes = a.k_codes + r * S::kRowBytes + my_unit() * S::KW * 16;
+      const uint8_t* scales = a.k_scales + r * blocks;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const uint8_t* at = codes + (uint32_t)(col * S::kRowBytes + quarter * S::KW * 4) + u * S::KW * 16;
+        if constexpr (S::KW == 4) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at);
+          x.k[h][u][0] = v.x; x.k[h][u][1] = v.y; x.k[h][u][2] = v.z; x.k[h][u][3] = v.w;
+        } else {
+          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at);
+          x.k[h][u][0] = v.x; x.k[h][u][1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < S::KS; ++i)
+          x.ks[h][u][i] =
+              scales[(uint32_t)(col * blocks + ((((my_unit() + u) * 4 + quarter) * S::KC + i * 16) >> a.block_shift))];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* codes = a.v_codes + row[j / 4] * S::kRowBytes + my_channels() * 16 * VB;
+      const uint8_t* scales = a.v_scales + (row[j / 4] + j % 4) * blocks;
+      const uint8_t* at = codes + (uint32_t)(quarter * 4 * S::kRowBytes + col * VB) + j % 4 * S::kRowBytes;
+      if constexpr (VB == 2) x.v[j][0] = *reinterpret_cast<const uint16_t*>(at);
+      else if constexpr (VB == 4) x.v[j][0] = *reinterpret_cast<const uint32_t*>(at);
+      else {
+        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at);
+        x.v[j][0] = v.x; x.v[j][1] = v.y;
+      }
+      x.vs[j] = scales[(uint32_t)(quarter * 4 * blocks + ((my_channels() * 128 + col * VC) >> a.block_shift))];
+    }
+  }
+  // Two channels in bf16; a scale that is more than its exponent is multiplied in fp32 (exact, as the product is in bf16).
+  template <int I>
+  __device__ __forceinline__ static uint32_t decode(const uint32_t* words, float s, bool exact) {
+    if (FMT != FMT_NVFP4 || !exact) return decode_pair<FMT, I>(words, s);
+    const uint32_t v = decode_pair<FMT, I>(words, 1.0f);
+    return pack_bf16(bf16_lo(v) * s, bf16_hi(v) * s);
+  }
+  // Raw to LDS; positions that are none become 0, and values of partly attended tiles that are not finite too, with a mark.
+  __device__ __forceinline__ void decode_step(Raw& x, int step, int tag) const {
+    const int t = my_tile(step), slot = wave / kPartsOfTile;
+    if (!(x.there[0] && x.there[1] && (t + 1) * kTile <= w.known)) clean(x, t, tag);
+    bool exact = false;
+    if constexpr (FMT == FMT_NVFP4) {
+      bool any = false;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+          for (int i = 0; i < S::KS; ++i) any |= beyond_exponent(scale_value<FMT>(x.ks[h][u][i]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) any |= beyond_exponent(scale_value<FMT>(x.vs[j]));
+      exact = __ballot(any) != 0;
+    }
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+      static_for<kUnits>([&](auto U) {
+        constexpr int u = decltype(U)::value;
+        float sc[S::KS];
+#pragma unroll
+        for (int i = 0; i < S::KS; ++i) sc[i] = scale_operand<FMT>(x.ks[h][u][i]);
+        static_for<S::kHalves>([&](auto H) {
+          constexpr int hf = decltype(H)::value, is = hf / 2 < S::KS ? hf / 2 : 0;
+          uint32_t y[4];
+          static_for<4>([&](auto I) {
+            y[decltype(I)::value] = decode<hf * 4 + decltype(I)::value>(x.k[h][u], sc[is], exact);
+          });
+          sm.key[slot][kHalves == 2 ? h : my_half()][(my_unit() + u) * S::kHalves + hf][lane] = u32x4_t{y[0], y[1], y[2], y[3]};
+        });
+      });
+    float sc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = scale_operand<FMT>(x.vs[j]);
+    static_for<VC / 2>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      uint32_t y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = decode<i>(x.v[j], sc[j], exact);
+      uint32_t z[2][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[0][j] = __builtin_amdgcn_perm(y[2 * j + 1], y[2 * j], 0x05040100u);
+        z[1][j] = __builtin_amdgcn_perm(y[2 * j + 1], y[2 * j], 0x07060302u);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        sm.value[slot][my_channels() * 8 + 2 * i + half][lane] = u32x4_t{z[half][0], z[half][1], z[half][2], z[half][3]};
+    });
+  }
+  __device__ __forceinline__ void clean(Raw& x, int t, int tag) const {
+    constexpr uint32_t kOnes = S::kFp8 ? 0x01010101u : 0x11111111u, kTop = S::kFp8 ? 0x80808080u : 0x88888888u;
+    constexpr int kBits = S::kFp8 ? 8 : 4, kHalf = 1 << (kBits - 1);
+    uint32_t bad[8][VW], any = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
+      const bool none = !x.there[j / 4] || pos >= w.end;
+      const int least = least_odd<FMT>(x.vs[j]);
+      x.vs[j] = none || least == 0 ? (FMT == FMT_NVFP4 ? 0x38u : 127u) : x.vs[j];
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        const uint32_t word = none ? 0u : x.v[j][i];
+        bad[j][i] = none ? 0u : ((word & ~kTop) + (kHalf - least) * kOnes) & kTop;
+        x.v[j][i] = word & ~((bad[j][i] >> (kBits - 1)) * (2 * kHalf - 1));
+        any |= bad[j][i];
+      }
+    }
+    if (__ballot(any != 0) == 0) return;
+    if (lane == 0) sm.marked = tag;
+    const int channel = my_channels() * 128 + col * VC;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int c = 0; c < VC; ++c) bits |= (bad[j][c * kBits / 32] >> (c * kBits % 32 + kBits - 1) & 1u) << c;
+      const int pos = wave / kPartsOfTile * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
+      if (bits) atomicOr(&sm.odd[pos][channel / 32], bits << (channel % 32));
+    }
+  }
+
+  // Steps [first, last) of the problem; `whole`: they are all, else the sums go to `slot`.
+  __device__ __forceinline__ void piece(int first, int last, bool whole, float* slot) {
+    place();
+    for (int i = wave * 64 + lane; i < kRows * kWords; i += kAttnThreads) sm.nan[i / kWords][i % kWords] = 0;
+    for (int i = wave * 64 + lane; i < kStep * kWords; i += kAttnThreads) sm.odd[i / kWords][i % kWords] = 0;
+    if (wave == 0 && lane == 0) sm.marked = -1;
+    bf16x8_t q[MT][S::kSteps][QP];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st) {
+        const int ch = st / S::kHalves * 4 * S::KC + quarter * S::KC + st % S::kHalves * 8, r = row_of(mt);
+        float x[8] = {};
+        if (r < a.d.tokens * a.d.group) to_f32<DT>(load8<DT>(a.q, row_at(r) * D + ch, 8), x);
+        if (a.d.negative)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = -x[i];
+#pragma unroll
+        for (int p = 0; p < QP; ++p) q[mt][st][p] = take_part(x, p == QP - 1, minus);
+      }
+    f32x4_t o[MT][kTilesV];
+    float m[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int t = 0; t < kTilesV; ++t) o[mt][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      m[mt] = -__builtin_inff();
+      l[mt] = 0.0f;
+    }
+    // waves whose rows are all padding only decode
+    const bool works = tile * kRows + wave * MT * 16 < w.count * a.d.group;
+    if (first < last) {
+      Raw x;
+      load(x, first);
+      bool odd = false;
+      for (int step = first; step < last; ++step) {
+        __syncthreads();                   // the fragments of the step before have been read
+        if (odd) {
+          for (int i = wave * 64 + lane; i < kStep * kWords; i += kAttnThreads) sm.odd[i / kWords][i % kWords] = 0;
+          __syncthreads();
+        }
+        decode_step(x, step, step);
+        __syncthreads();
+        odd = __builtin_amdgcn_readfirstlane(sm.marked) == step;
+        if (step + 1 < last) load(x, step + 1);
+        if (works) products(step, q, odd, m, l, o);
+      }
+    }
+    finish(o, m, l, whole, slot);
+  }
+  __device__ __forceinline__ void products(int step, const bf16x8_t (&q)[MT][S::kSteps][QP], bool odd, float (&m)[MT],
+                                           float (&l)[MT], f32x4_t (&o)[MT][kTilesV]) const {
+#pragma unroll 1
+    for (int ti = 0; ti < kTiles; ++ti) {
+      const int t = step * kTiles + ti;
+      if (t * kTile >= w.end) break;
+      f32x4_t s[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int st = 0; st < S::kSteps; ++st) {
+        bf16x8_t key[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) key[h] = __builtin_bit_cast(bf16x8_t, sm.key[ti][h][st][lane]);
+#pragma unroll
+        for (int p = 0; p < QP; ++p)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s[mt][h] = mfma(key[h], q[mt][st][p], s[mt][h]);
+      }
+      bool there[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = (t * kTile + h * 16) >> a.d.page_shift;
+        const int page = uniform_load(a.table, (int64_t)b * a.d.width + min(at, a.d.width - 1));
+        there[h] = at < a.d.width && (uint32_t)page < (uint32_t)a.d.pages;
+      }
+      if (!(there[0] && there[1] && (t + 1) * kTile <= w.known)) {
+        uint32_t may[MT];
+        mask_scores<MT>(a, w, b, t, there[0], there[1], row_of(0), quarter, s, may);
+        if (odd) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              if (!(may[mt] >> j & 1)) continue;
+              const uint32_t* from = sm.odd[ti * kTile + (j / 4) * 16 + quarter * 4 + j % 4];
+              for (int i = 0; i < kWords; ++i)
+                if (from[i]) atomicOr(&sm.nan[(wave * MT + mt) * 16 + col][i], from[i]);
+            }
+        }
+      }
+      bf16x8_t p[MT][PP];
+      softmax_step<MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
+#pragma unroll
+      for (int t = 0; t < kTilesV; t += 2) {
+        bf16x8_t val[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) val[h] = __builtin_bit_cast(bf16x8_t, sm.value[ti][t + h][lane]);
+#pragma unroll
+        for (int part = 0; part < PP; ++part)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) o[mt][t + h] = mfma(val[h], p[mt][part], o[mt][t + h]);
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
+    place();
+    __syncthreads();                       // the marks are all there
+    const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float sum = row_sum(l[mt]);
+      const int r = (wave * MT + mt) * 16 + col, at = tile * kRows + r;
+#pragma unroll
+      for (int u = 0; u < kTilesV / VC; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ch = u * 16 * VC + (quarter * 4 + i) * VC;
+          const uint32_t bits = sm.nan[r][ch / 32] >> (ch % 32);
+          float x[VC];
+#pragma unroll
+          for (int e = 0; e < VC; ++e) x[e] = bits >> e & 1 ? __builtin_nanf("") : o[mt][u * VC + e][i];
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < VC; e += 4)
+              *reinterpret_cast<f32x4_t*>(slot + r * D + ch + e) = f32x4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
+          } else if (at < rows) {
+            write_row<DT, VC>(a, row_at(at), D, ch, x, m[mt], at < live ? sum : 0.0f);
+          }
+        }
+      if (!whole && quarter == 0) {
+        slot[kRows * D + r] = m[mt];
+        slot[kRows * D + kRows + r] = sum;
+      }
+    }
   }
 };
 
@@ -745,30 +1105,28 @@ __device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
 }
 
 // One workgroup for each problem.
-template <int DT, int FMT, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attention(AttnArgs a) {
-  using A = Attention<DT, FMT, D, MT>;
+template <class A>
+__global__ void __launch_bounds__(kAttnThreads, A::kWaves) k_cache_attention(AttnArgs a) {
   __shared__ typename A::Shared sm;
   A x(a, sm);
   const int each = a.d.kv_heads * a.d.row_tiles;
   x.b = blockIdx.x / each;
   x.kv = (blockIdx.x - x.b * each) / a.d.row_tiles;
   x.tile = blockIdx.x % a.d.row_tiles;
-  x.w = work_of_all(a, x.b, A::kRows);
+  x.w = work_of_all<A>(a, x.b);
   x.piece(0, x.tile < x.w.tiles ? x.w.steps : 0, true, nullptr);
 }
 
 // The steps of all problems shared out evenly: workgroup w takes those of share_of, a piece of a problem at a time.  A
 // problem that lies within one share is written here, the others' parts are joined by k_cache_attention_join.
-template <int DT, int FMT, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attention_split(AttnArgs a) {
-  using A = Attention<DT, FMT, D, MT>;
+template <class A>
+__global__ void __launch_bounds__(kAttnThreads, A::kWaves) k_cache_attention_split(AttnArgs a) {
   __shared__ typename A::Shared sm;
   A x(a, sm);
   int total = 0;
   for (int b0 = 0; b0 < a.d.sequences; b0 += kAttnThreads) {
     int sum;
-    attn_scan(units_of(a, b0 + (int)threadIdx.x, A::kRows), sm.sums, sum);
+    attn_scan(units_of<A>(a, b0 + (int)threadIdx.x), sm.sums, sum);
     total += sum;
   }
   total = __builtin_amdgcn_readfirstlane(total);
@@ -779,7 +1137,7 @@ __global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attenti
   int base = 0;                     // steps of the sequences before b0
   for (int b0 = 0; u < end; b0 += kAttnThreads) {
     int sum;
-    const int below = attn_scan(units_of(a, b0 + (int)threadIdx.x, A::kRows), sm.sums, sum);
+    const int below = attn_scan(units_of<A>(a, b0 + (int)threadIdx.x), sm.sums, sum);
     sum = __builtin_amdgcn_readfirstlane(sum);
     sm.first[threadIdx.x] = base + below;
     __syncthreads();
@@ -788,14 +1146,14 @@ __global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attenti
       for (int s = kAttnThreads / 2; s > 0; s /= 2)
         if (__builtin_amdgcn_readfirstlane(sm.first[lo + s]) <= u) lo += s;
       x.b = b0 + lo;
-      x.w = work_of_all(a, x.b, A::kRows);
+      x.w = work_of_all<A>(a, x.b);
       const int local = u - __builtin_amdgcn_readfirstlane(sm.first[lo]), problem = local / x.w.steps;
       const int step = local - problem * x.w.steps;
       x.kv = problem / x.w.tiles;
       x.tile = problem - x.kv * x.w.tiles;
       const int n = min(x.w.steps - step, end - u);
       const bool whole = n == x.w.steps;
-      x.piece(step, step + n, whole, a.parts + (int64_t)(2 * me + (step == 0)) * kSlotFloats<MT, D>);
+      x.piece(step, step + n, whole, a.parts + (int64_t)(2 * me + (step == 0)) * kSlotFloats<A>);
       u += n;
       __syncthreads();
     }
@@ -807,9 +1165,9 @@ __global__ void __launch_bounds__(kAttnThreads, (kWaves<D, MT>)) k_cache_attenti
 // The parts of problems that several workgroups worked on; and zeros for those that none did.  A workgroup takes 64 groups
 // of 8 channels, a lane each, and its waves take turns at the parts, so that a wave has a few parts' loads under way at a
 // time (a lane that took them one after another made 12 us of 16 parts).
-template <int DT, int FMT, int D, int MT>
+template <class A>
 __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs a) {
-  using A = Attention<DT, FMT, D, MT>;
+  constexpr int D = A::kDim;
   __shared__ int counts[4][2];
   __shared__ float sums[4][64][10];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -817,7 +1175,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
   const int b = blockIdx.x / each, kv = (blockIdx.x - b * each) / a.d.row_tiles, tile = blockIdx.x % a.d.row_tiles;
   int before = 0, all = 0;
   for (int s = threadIdx.x; s < a.d.sequences; s += kAttnThreads) {
-    const int units = units_of(a, s, A::kRows);
+    const int units = units_of<A>(a, s);
     all += units;
     before += s < b ? units : 0;
   }
@@ -833,7 +1191,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
   __syncthreads();
   const int total = __builtin_amdgcn_readfirstlane(counts[0][0] + counts[1][0] + counts[2][0] + counts[3][0]);
   int first = __builtin_amdgcn_readfirstlane(counts[0][1] + counts[1][1] + counts[2][1] + counts[3][1]);
-  const Work w = work_of_all(a, b, A::kRows);
+  const Work w = work_of_all<A>(a, b);
   const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
   const bool none = w.steps == 0 || tile >= w.tiles;
   int w0 = 0, w1 = -1;
@@ -848,7 +1206,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
   const bool wanted = at < rows;
   float x[8] = {}, top = -__builtin_inff(), sum = 0.0f;
   if (wanted && at < live) {
-    auto slot_of = [&](int s) { return a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<MT, D>; };
+    auto slot_of = [&](int s) { return a.parts + (int64_t)(2 * s + (s == w0)) * kSlotFloats<A>; };
 #pragma unroll 4
     for (int s = w0 + wave; s <= w1; s += 4) top = fmaxf(top, slot_of(s)[A::kRows * D + r]);
 #pragma unroll 2
@@ -887,55 +1245,71 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
     for (int e = 0; e < 8; ++e) x[e] += sums[s][lane][e] * keep;
   }
   const int t = at / a.d.group;
-  A::write_row(a, ((int64_t)b * a.d.tokens + t) * a.d.heads + kv * a.d.group + (at - t * a.d.group), ch, x, best, whole);
+  write_row<A::kType, 8>(a, ((int64_t)b * a.d.tokens + t) * a.d.heads + kv * a.d.group + (at - t * a.d.group), D, ch, x, best,
+                         whole);
 }
 
-// Rows of a wave's tile, in 16s: as many as the problem has, while the sums fit the registers.
-inline int attention_row_tiles(int dt, int dim, int64_t rows) {
-  const int most = dim <= 128 ? (dt == DT_BF16 ? 4 : 2) : dim == 256 ? 2 : 1;
-#ifndef MTMAX
-#define MTMAX 2
-#endif
-  const int want = rows <= 16 ? 1 : rows <= 32 || MTMAX == 2 ? 2 : 4;
-  return want < most ? want : most;
+// Rows of a problem's tile.  Up to 16 or 32: the four waves take different positions of the same rows, so that a few rows
+// keep a whole workgroup's loads under way.  More: each wave has rows of its own, 16 or 32, and all take the same positions,
+// decoded once.
+inline int attention_rows(int dim, int64_t rows) {
+  if (rows <= 16) return 16;
+  if (rows <= 32 && dim <= 128) return 32;
+  return rows <= 64 || dim > 128 ? 64 : 128;
 }
+template <int DT, int FMT, int D, int ROWS>
+struct KernelOf {
+  using Type = std::conditional_t<(ROWS <= 32), Attention<DT, FMT, D, (ROWS <= 32 ? ROWS / 16 : 1)>,
+                                  SharedAttention<DT, FMT, D, (ROWS <= 32 ? 1 : ROWS / 64)>>;
+};
+// What the launches have to know of a kernel.
+struct AttnShape {
+  int step, waves;
+};
 
-template <int DT, int FMT, int D, int MT>
+template <class A>
 hipError_t launch_attention_of(const AttnArgs& a, int64_t problems, hipStream_t st) {
   if (a.d.workgroups == 0) {
-    k_cache_attention<DT, FMT, D, MT><<<(unsigned)problems, kAttnThreads, 0, st>>>(a);
+    k_cache_attention<A><<<(unsigned)problems, kAttnThreads, 0, st>>>(a);
   } else {
-    k_cache_attention_split<DT, FMT, D, MT><<<(unsigned)a.d.workgroups, kAttnThreads, 0, st>>>(a);
-    k_cache_attention_join<DT, FMT, D, MT><<<dim3((unsigned)problems, 16 * MT * D / 512), kAttnThreads, 0, st>>>(a);
+    k_cache_attention_split<A><<<(unsigned)a.d.workgroups, kAttnThreads, 0, st>>>(a);
+    k_cache_attention_join<A><<<dim3((unsigned)problems, A::kRows * A::kDim / 512), kAttnThreads, 0, st>>>(a);
   }
   return hipGetLastError();
 }
 
+// The kernel for a head size and rows: its shape (a NULL), or a launch.
 template <int DT, int FMT>
-hipError_t launch_attention_dim(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st) {
-#define CASE(D, MT) \
-  if (dim == D && tiles == MT) return launch_attention_of<DT, FMT, D, MT>(a, problems, st)
-  CASE(64, 1);
-  CASE(64, 2);
-  CASE(128, 1);
-  CASE(128, 2);
-  if constexpr (DT == DT_BF16) {
-    CASE(64, 4);
-    CASE(128, 4);
+hipError_t attention_dim(const AttnArgs* a, int dim, int rows, int64_t problems, AttnShape* shape, hipStream_t st) {
+#define CASE(D, ROWS)                                         \
+  if (dim == D && rows == ROWS) {                             \
+    using A = typename KernelOf<DT, FMT, D, ROWS>::Type;      \
+    if (a) return launch_attention_of<A>(*a, problems, st);   \
+    *shape = {A::kStep, A::kWaves};                           \
+    return hipSuccess;                                        \
   }
-  CASE(256, 1);
-  CASE(256, 2);
-  CASE(512, 1);
+  CASE(64, 16)
+  CASE(64, 32)
+  CASE(64, 64)
+  CASE(64, 128)
+  CASE(128, 16)
+  CASE(128, 32)
+  CASE(128, 64)
+  CASE(128, 128)
+  CASE(256, 16)
+  CASE(256, 64)
+  CASE(512, 16)
+  CASE(512, 64)
 #undef CASE
   return hipErrorInvalidValue;
 }
 
 // The kernels of one type and format (csrc/cache_attention_<format>_<type>.hip).
 template <int DT, int FMT>
-hipError_t launch_attention_kernels(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st);
-#define DECLARE(DT, FMT) \
-  template <>            \
-  hipError_t launch_attention_kernels<DT, FMT>(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st)
+hipError_t attention_kernels(const AttnArgs* a, int dim, int rows, int64_t problems, AttnShape* shape, hipStream_t st);
+#define DECLARE(DT, FMT)                                                                                               \
+  template <>                                                                                                          \
+  hipError_t attention_kernels<DT, FMT>(const AttnArgs* a, int dim, int rows, int64_t problems, AttnShape* shape, hipStream_t st)
 #define DECLARE_FORMATS(DT) \
   DECLARE(DT, FMT_FP8);     \
   DECLARE(DT, FMT_MXFP4);   \

@@ -4,8 +4,9 @@
 namespace mxq {
 
 template <>
-hipError_t launch_attention_kernels<DT_BF16, FMT_FP8>(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st) {
-  return launch_attention_dim<DT_BF16, FMT_FP8>(a, dim, tiles, problems, st);
+hipError_t attention_kernels<DT_BF16, FMT_FP8>(const AttnArgs* a, int dim, int rows, int64_t problems, AttnShape* shape,
+                                     hipStream_t st) {
+  return attention_dim<DT_BF16, FMT_FP8>(a, dim, rows, problems, shape, st);
 }
 
 }  // namespace mxq

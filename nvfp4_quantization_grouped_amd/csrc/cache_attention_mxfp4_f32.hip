@@ -4,8 +4,9 @@
 namespace mxq {
 
 template <>
-hipError_t launch_attention_kernels<DT_F32, FMT_MXFP4>(const AttnArgs& a, int dim, int tiles, int64_t problems, hipStream_t st) {
-  return launch_attention_dim<DT_F32, FMT_MXFP4>(a, dim, tiles, problems, st);
+hipError_t attention_kernels<DT_F32, FMT_MXFP4>(const AttnArgs* a, int dim, int rows, int64_t problems, AttnShape* shape,
+                                     hipStream_t st) {
+  return attention_dim<DT_F32, FMT_MXFP4>(a, dim, rows, problems, shape, st);
 }
 
 }  // namespace mxq
