@@ -254,27 +254,34 @@ __device__ __forceinline__ void mask_scores(const AttnArgs& a, const Work& w, in
 template <int MT, int PP, int NT>
 __device__ __forceinline__ void softmax_step(const f32x4_t (&s)[MT][2], float scale, const MinusOne& minus, float (&m)[MT],
                                              float (&l)[MT], f32x4_t (&o)[MT][NT], bf16x8_t (&p)[MT][PP]) {
+  float top[MT];
+  bool past = false;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    float e[8];
+    top[mt] = s[mt][0][0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = s[mt][i / 4][i % 4];
-    float top = e[0];
+    for (int i = 1; i < 8; ++i) top[mt] = fmaxf(top[mt], s[mt][i / 4][i % 4]);
+    top[mt] *= scale;
+    past |= top[mt] > m[mt] + kLazy;
+  }
+  if (__ballot(past) != 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, e[i]);
-    top *= scale;
-    if (__ballot(top > m[mt] + kLazy) != 0) {
-      const float to = fmaxf(m[mt], row_max(top));
+    for (int mt = 0; mt < MT; ++mt) {
+      const float to = fmaxf(m[mt], row_max(top[mt]));
       const float keep = m[mt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[mt] - to);
       m[mt] = to;
       l[mt] *= keep;
 #pragma unroll
       for (int c = 0; c < NT; ++c) o[mt][c] *= keep;
     }
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
     const float sub = m[mt] == -__builtin_inff() ? 0.0f : m[mt];
+    float e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[i], scale, -sub));
+      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][i / 4][i % 4], scale, -sub));
       l[mt] += e[i];
     }
 #pragma unroll
@@ -767,6 +774,7 @@ struct SharedAttention {
     uint32_t odd[kStep][kWords];          // channels of a position whose value is not finite
     uint32_t nan[kRows][kWords];          // outputs that one reached
     int marked;                           // the step that `odd` is of
+    int there[kTiles];                    // which halves of a tile have a page
     int first[kAttnThreads + 1];
     int sums[4];
   };
@@ -803,19 +811,27 @@ struct SharedAttention {
   struct Raw {
     uint32_t k[kHalves][kUnits][S::KW], ks[kHalves][kUnits][S::KS];
     uint32_t v[8][VW], vs[8];
-    bool there[2];
+    int page[2], next[2];       // of the halves' positions, -1 for none; and of those of the step after
   };
+  __device__ __forceinline__ void look_up(int (&page)[2], int step) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int slot = (my_tile(step) * kTile + h * 16) >> a.d.page_shift;
+      const int entry = uniform_load(a.table, (int64_t)b * a.d.width + min(slot, a.d.width - 1));
+      page[h] = slot < a.d.width && (uint32_t)entry < (uint32_t)a.d.pages ? entry : -1;
+    }
+  }
+  // The step's rows, whose pages were looked up a step ago.
   __device__ __forceinline__ void load(Raw& x, int step) const {
     const int t = my_tile(step), blocks = D >> a.block_shift;
     int64_t row[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int pos = t * kTile + h * 16, slot = pos >> a.d.page_shift;
-      const int page = uniform_load(a.table, (int64_t)b * a.d.width + min(slot, a.d.width - 1));
-      x.there[h] = slot < a.d.width && (uint32_t)page < (uint32_t)a.d.pages;
-      row[h] = (((int64_t)(x.there[h] ? page : 0) * a.d.kv_heads + kv) << a.d.page_shift) +
-               (pos & ((1 << a.d.page_shift) - 1));
+      x.page[h] = x.next[h];
+      row[h] = (((int64_t)max(x.page[h], 0) * a.d.kv_heads + kv) << a.d.page_shift) +
+               ((t * kTile + h * 16) & ((1 << a.d.page_shift) - 1));
     }
+    look_up(x.next, step + 1);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int64_t r = kHalves == 2 ? row[h] : my_half() ? row[1] : row[0];
@@ -852,17 +868,17 @@ struct SharedAttention {
     }
   }
   // Two channels in bf16; a scale that is more than its exponent is multiplied in fp32 (exact, as the product is in bf16).
-  template <int I>
-  __device__ __forceinline__ static uint32_t decode(const uint32_t* words, float s, bool exact) {
-    if (FMT != FMT_NVFP4 || !exact) return decode_pair<FMT, I>(words, s);
+  template <bool EXACT, int I>
+  __device__ __forceinline__ static uint32_t decode(const uint32_t* words, float s) {
+    if constexpr (!EXACT) return decode_pair<FMT, I>(words, s);
     const uint32_t v = decode_pair<FMT, I>(words, 1.0f);
     return pack_bf16(bf16_lo(v) * s, bf16_hi(v) * s);
   }
   // Raw to LDS; positions that are none become 0, and values of partly attended tiles that are not finite too, with a mark.
   __device__ __forceinline__ void decode_step(Raw& x, int step, int tag) const {
-    const int t = my_tile(step), slot = wave / kPartsOfTile;
-    if (!(x.there[0] && x.there[1] && (t + 1) * kTile <= w.known)) clean(x, t, tag);
-    bool exact = false;
+    const int t = my_tile(step);
+    if (lane == 0) sm.there[wave / kPartsOfTile] = (int)(x.page[0] >= 0) + 2 * (int)(x.page[1] >= 0);   // each part says the same
+    if (!(x.page[0] >= 0 && x.page[1] >= 0 && (t + 1) * kTile <= w.known)) clean(x, t, tag);
     if constexpr (FMT == FMT_NVFP4) {
       bool any = false;
 #pragma unroll
@@ -873,8 +889,13 @@ struct SharedAttention {
           for (int i = 0; i < S::KS; ++i) any |= beyond_exponent(scale_value<FMT>(x.ks[h][u][i]));
 #pragma unroll
       for (int j = 0; j < 8; ++j) any |= beyond_exponent(scale_value<FMT>(x.vs[j]));
-      exact = __ballot(any) != 0;
+      if (__ballot(any) != 0) return emit<true>(x);
     }
+    emit<false>(x);
+  }
+  template <bool EXACT>
+  __device__ __forceinline__ void emit(const Raw& x) const {
+    const int slot = wave / kPartsOfTile;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
       static_for<kUnits>([&](auto U) {
@@ -886,7 +907,7 @@ struct SharedAttention {
           constexpr int hf = decltype(H)::value, is = hf / 2 < S::KS ? hf / 2 : 0;
           uint32_t y[4];
           static_for<4>([&](auto I) {
-            y[decltype(I)::value] = decode<hf * 4 + decltype(I)::value>(x.k[h][u], sc[is], exact);
+            y[decltype(I)::value] = decode<EXACT, hf * 4 + decltype(I)::value>(x.k[h][u], sc[is]);
           });
           sm.key[slot][kHalves == 2 ? h : my_half()][(my_unit() + u) * S::kHalves + hf][lane] = u32x4_t{y[0], y[1], y[2], y[3]};
         });
@@ -898,7 +919,7 @@ struct SharedAttention {
       constexpr int i = decltype(I)::value;
       uint32_t y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = decode<i>(x.v[j], sc[j], exact);
+      for (int j = 0; j < 8; ++j) y[j] = decode<EXACT, i>(x.v[j], sc[j]);
       uint32_t z[2][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -917,7 +938,7 @@ struct SharedAttention {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
-      const bool none = !x.there[j / 4] || pos >= w.end;
+      const bool none = x.page[j / 4] < 0 || pos >= w.end;
       const int least = least_odd<FMT>(x.vs[j]);
       x.vs[j] = none || least == 0 ? (FMT == FMT_NVFP4 ? 0x38u : 127u) : x.vs[j];
 #pragma unroll
@@ -974,6 +995,7 @@ struct SharedAttention {
     const bool works = tile * kRows + wave * MT * 16 < w.count * a.d.group;
     if (first < last) {
       Raw x;
+      look_up(x.next, first);
       load(x, first);
       bool odd = false;
       for (int step = first; step < last; ++step) {
@@ -1012,16 +1034,10 @@ struct SharedAttention {
 #pragma unroll
             for (int h = 0; h < 2; ++h) s[mt][h] = mfma(key[h], q[mt][st][p], s[mt][h]);
       }
-      bool there[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int at = (t * kTile + h * 16) >> a.d.page_shift;
-        const int page = uniform_load(a.table, (int64_t)b * a.d.width + min(at, a.d.width - 1));
-        there[h] = at < a.d.width && (uint32_t)page < (uint32_t)a.d.pages;
-      }
-      if (!(there[0] && there[1] && (t + 1) * kTile <= w.known)) {
+      const int there = __builtin_amdgcn_readfirstlane(sm.there[ti]);
+      if (there != 3 || (t + 1) * kTile > w.known) {
         uint32_t may[MT];
-        mask_scores<MT>(a, w, b, t, there[0], there[1], row_of(0), quarter, s, may);
+        mask_scores<MT>(a, w, b, t, there & 1, there >> 1, row_of(0), quarter, s, may);
         if (odd) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
