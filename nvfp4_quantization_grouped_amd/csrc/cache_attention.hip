@@ -39,7 +39,7 @@ Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64
   (void)kernels(nullptr, dt, c.fmt, c.head_dim, p.rows, 0, &shape, nullptr);
   const int64_t steps = (width * c.page_size + shape.step - 1) / shape.step;
   const bool split = p.problems < kManyProblems && steps > kFewSteps && p.problems * steps < (int64_t(1) << 31);
-  p.workgroups = split ? kComputeUnits * shape.waves : 0;
+  p.workgroups = split ? kComputeUnits * shape.resident : 0;
   return p;
 }
 

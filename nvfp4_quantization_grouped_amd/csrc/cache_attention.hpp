@@ -297,6 +297,7 @@ struct Attention {
   static constexpr int kTilesV = D / 16, kType = DT;
   // waves of a SIMD that the registers are kept to, which is workgroups of a CU
   static constexpr int kWaves = D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
+  static constexpr int kThreads = kAttnThreads, kResident = kWaves;
   // q's fragments stay in registers up to 32 of them, else in LDS
   static constexpr bool kQInRegs = D * QP * MT <= 256;
   static constexpr int kPad = D + 4;
@@ -311,7 +312,7 @@ struct Attention {
     __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
     __attribute__((aligned(16))) uint8_t nan[kRows * D];   // outputs that a value that is not finite reached
     float m[4][kRows], l[4][kRows];
-    int first[kAttnThreads + 1];                           // prefix sums of the schedule
+    int first[kThreads];                                   // prefix sums of the schedule
     int sums[4];
   };
 
@@ -752,16 +753,17 @@ struct Attention {
 // quarter to each wave, into LDS as the fragments that the products take, and each wave takes all of them for 16 * MT rows
 // of its own.  Decoding costs four times less a row than where each wave decodes what it reads, and needs no registers
 // beside the sums.  LDS holds one step (64 KB); two workgroups of a CU take turns at decoding and products.
-template <int DT, int FMT, int D, int MT>
+template <int DT, int FMT, int D, int MT, int WAVES>
 struct SharedAttention {
   using S = Shape<FMT, D>;
   static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kDim = D, kType = DT;
-  static constexpr int kTilesV = D / 16, kRows = 64 * MT;
-  static constexpr int kStep = D <= 128 ? 128 : 16384 / D, kTiles = kStep / kTile;
-  // two workgroups of a CU where q and the sums leave the registers for it
+  static constexpr int kTilesV = D / 16, kThreads = 64 * WAVES, kRows = 16 * MT * WAVES;
+  static constexpr int kStep = D <= 128 ? kTile * WAVES : 4096 * WAVES / D, kTiles = kStep / kTile;
+  // waves of a SIMD that the registers are kept to: two where q and the sums leave room for it
   static constexpr int kWaves = MT * (D / 8 * QP + D / 4) <= 192 ? 2 : 1;
-  // a wave's quarter of a step: tile `part`, and of that
-  static constexpr int kPartsOfTile = 4 / kTiles;
+  static constexpr int kResident = kWaves * 4 / WAVES;                 // workgroups of a CU
+  // a wave's share of a step: a tile, or of that a part:
+  static constexpr int kPartsOfTile = WAVES / kTiles;
   static constexpr int kHalves = kPartsOfTile > 1 ? 1 : 2;             // halves of its positions for the keys
   static constexpr int kUnits = kPartsOfTile > 2 ? S::KU / 2 : S::KU;  // units of them
   static constexpr int VC = D / 16 < 8 ? D / 16 : 8;                   // channels of a lane for the values, of all positions
@@ -775,7 +777,7 @@ struct SharedAttention {
     uint32_t nan[kRows][kWords];          // outputs that one reached
     int marked;                           // the step that `odd` is of
     int there[kTiles];                    // which halves of a tile have a page
-    int first[kAttnThreads + 1];
+    int first[kThreads];
     int sums[4];
   };
 
@@ -965,8 +967,8 @@ struct SharedAttention {
   // Steps [first, last) of the problem; `whole`: they are all, else the sums go to `slot`.
   __device__ __forceinline__ void piece(int first, int last, bool whole, float* slot) {
     place();
-    for (int i = wave * 64 + lane; i < kRows * kWords; i += kAttnThreads) sm.nan[i / kWords][i % kWords] = 0;
-    for (int i = wave * 64 + lane; i < kStep * kWords; i += kAttnThreads) sm.odd[i / kWords][i % kWords] = 0;
+    for (int i = wave * 64 + lane; i < kRows * kWords; i += kThreads) sm.nan[i / kWords][i % kWords] = 0;
+    for (int i = wave * 64 + lane; i < kStep * kWords; i += kThreads) sm.odd[i / kWords][i % kWords] = 0;
     if (wave == 0 && lane == 0) sm.marked = -1;
     bf16x8_t q[MT][S::kSteps][QP];
 #pragma unroll
@@ -1001,7 +1003,7 @@ struct SharedAttention {
       for (int step = first; step < last; ++step) {
         __syncthreads();                   // the fragments of the step before have been read
         if (odd) {
-          for (int i = wave * 64 + lane; i < kStep * kWords; i += kAttnThreads) sm.odd[i / kWords][i % kWords] = 0;
+          for (int i = wave * 64 + lane; i < kStep * kWords; i += kThreads) sm.odd[i / kWords][i % kWords] = 0;
           __syncthreads();
         }
         decode_step(x, step, step);
@@ -1099,7 +1101,8 @@ struct SharedAttention {
   }
 };
 
-// Sum of v over the threads below this one, of kAttnThreads; all of them in `total`.
+// Sum of v over the threads below this one, of 64 * WAVES; all of them in `total`.
+template <int WAVES>
 __device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
   int x = v;
 #pragma unroll
@@ -1113,7 +1116,7 @@ __device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
   int below = x - v;
   total = 0;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < WAVES; ++s) {
     if (s < (int)(threadIdx.x >> 6)) below += sums[s];
     total += sums[s];
   }
@@ -1122,7 +1125,7 @@ __device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
 
 // One workgroup for each problem.
 template <class A>
-__global__ void __launch_bounds__(kAttnThreads, A::kWaves) k_cache_attention(AttnArgs a) {
+__global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention(AttnArgs a) {
   __shared__ typename A::Shared sm;
   A x(a, sm);
   const int each = a.d.kv_heads * a.d.row_tiles;
@@ -1136,13 +1139,13 @@ __global__ void __launch_bounds__(kAttnThreads, A::kWaves) k_cache_attention(Att
 // The steps of all problems shared out evenly: workgroup w takes those of share_of, a piece of a problem at a time.  A
 // problem that lies within one share is written here, the others' parts are joined by k_cache_attention_join.
 template <class A>
-__global__ void __launch_bounds__(kAttnThreads, A::kWaves) k_cache_attention_split(AttnArgs a) {
+__global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention_split(AttnArgs a) {
   __shared__ typename A::Shared sm;
   A x(a, sm);
   int total = 0;
-  for (int b0 = 0; b0 < a.d.sequences; b0 += kAttnThreads) {
+  for (int b0 = 0; b0 < a.d.sequences; b0 += A::kThreads) {
     int sum;
-    attn_scan(units_of<A>(a, b0 + (int)threadIdx.x), sm.sums, sum);
+    attn_scan<A::kThreads / 64>(units_of<A>(a, b0 + (int)threadIdx.x), sm.sums, sum);
     total += sum;
   }
   total = __builtin_amdgcn_readfirstlane(total);
@@ -1151,15 +1154,15 @@ __global__ void __launch_bounds__(kAttnThreads, A::kWaves) k_cache_attention_spl
   int u = share_of(me, total, g);
   const int end = share_of(me + 1, total, g);
   int base = 0;                     // steps of the sequences before b0
-  for (int b0 = 0; u < end; b0 += kAttnThreads) {
+  for (int b0 = 0; u < end; b0 += A::kThreads) {
     int sum;
-    const int below = attn_scan(units_of<A>(a, b0 + (int)threadIdx.x), sm.sums, sum);
+    const int below = attn_scan<A::kThreads / 64>(units_of<A>(a, b0 + (int)threadIdx.x), sm.sums, sum);
     sum = __builtin_amdgcn_readfirstlane(sum);
     sm.first[threadIdx.x] = base + below;
     __syncthreads();
     while (u < min(end, base + sum)) {
       int lo = 0;                   // the last sequence of the chunk that starts at or before u, and is not empty
-      for (int s = kAttnThreads / 2; s > 0; s /= 2)
+      for (int s = A::kThreads / 2; s > 0; s /= 2)
         if (__builtin_amdgcn_readfirstlane(sm.first[lo + s]) <= u) lo += s;
       x.b = b0 + lo;
       x.w = work_of_all<A>(a, x.b);
@@ -1266,8 +1269,8 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
 }
 
 // Rows of a problem's tile.  Up to 16 or 32: the four waves take different positions of the same rows, so that a few rows
-// keep a whole workgroup's loads under way.  More: each wave has rows of its own, 16 or 32, and all take the same positions,
-// decoded once.
+// keep a whole workgroup's loads under way.  More: each wave has rows of its own, 32 (16 of the wide heads), and all take
+// the same positions, decoded once; two waves are enough for 64.
 inline int attention_rows(int dim, int64_t rows) {
   if (rows <= 16) return 16;
   if (rows <= 32 && dim <= 128) return 32;
@@ -1276,19 +1279,19 @@ inline int attention_rows(int dim, int64_t rows) {
 template <int DT, int FMT, int D, int ROWS>
 struct KernelOf {
   using Type = std::conditional_t<(ROWS <= 32), Attention<DT, FMT, D, (ROWS <= 32 ? ROWS / 16 : 1)>,
-                                  SharedAttention<DT, FMT, D, (ROWS <= 32 ? 1 : ROWS / 64)>>;
+                                  SharedAttention<DT, FMT, D, (D <= 128 ? 2 : 1), (ROWS == 64 && D <= 128 ? 2 : 4)>>;
 };
 // What the launches have to know of a kernel.
 struct AttnShape {
-  int step, waves;
+  int step, resident;     // positions of a step; workgroups of a CU
 };
 
 template <class A>
 hipError_t launch_attention_of(const AttnArgs& a, int64_t problems, hipStream_t st) {
   if (a.d.workgroups == 0) {
-    k_cache_attention<A><<<(unsigned)problems, kAttnThreads, 0, st>>>(a);
+    k_cache_attention<A><<<(unsigned)problems, A::kThreads, 0, st>>>(a);
   } else {
-    k_cache_attention_split<A><<<(unsigned)a.d.workgroups, kAttnThreads, 0, st>>>(a);
+    k_cache_attention_split<A><<<(unsigned)a.d.workgroups, A::kThreads, 0, st>>>(a);
     k_cache_attention_join<A><<<dim3((unsigned)problems, A::kRows * A::kDim / 512), kAttnThreads, 0, st>>>(a);
   }
   return hipGetLastError();
@@ -1301,7 +1304,7 @@ hipError_t attention_dim(const AttnArgs* a, int dim, int rows, int64_t problems,
   if (dim == D && rows == ROWS) {                             \
     using A = typename KernelOf<DT, FMT, D, ROWS>::Type;      \
     if (a) return launch_attention_of<A>(*a, problems, st);   \
-    *shape = {A::kStep, A::kWaves};                           \
+    *shape = {A::kStep, A::kResident};                           \
     return hipSuccess;                                        \
   }
   CASE(64, 16)
