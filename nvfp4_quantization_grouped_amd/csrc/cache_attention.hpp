@@ -21,9 +21,13 @@
 //
 // Roundings.  Codes times scales have at most 6 significant bits and are exact
 // in bf16.  q of fp16 / fp32 enters as 2 / 3 bf16 parts (exact but for what
-// lies 2^-24 below), probabilities as 2 parts (3 for fp32 outputs): one part
-// alone, 2^-8 of each probability, would double the error that rounding the
-// output to bf16 makes.
+// lies 2^-24 below).  Probabilities are a choice: one bf16 part, up to 2^-8 of
+// each, would make the error of bf16 outputs 1.4 times what rounding them costs;
+// two parts (three for fp32 outputs) leave nothing to see, at as many products.
+// For bf16 outputs one fp16 part does (2^-11; the error is 1.01 times the
+// rounding's) where the values fit fp16 exactly, which the scales tell: always
+// for nvfp4, else for values between 2^-15 or so and 2^15.  A workgroup that
+// meets other scales starts its piece again with two bf16 parts.
 #pragma once
 
 #include <type_traits>
@@ -38,7 +42,12 @@ typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 
 constexpr int kAttnThreads = 256;
 constexpr int kTile = 32;                    // positions of a wave's tile
-constexpr float kLazy = 8.0f;                // log2 units that a score may exceed the running maximum by
+// Log2 units by which probabilities may exceed 1, and (fp16) what the largest is when the maximum moves: fp16's range is
+// then 2^-30 to 2^14 times the row's largest, so that n small ones lose at most n 2^-31 of the sum.
+template <bool HALF>
+constexpr float kOver = HALF ? 14.0f : 8.0f;
+template <bool HALF>
+constexpr float kAtMove = HALF ? 6.0f : 0.0f;
 
 struct AttnDims {
   int sequences, tokens, heads, group, kv_heads, width, page_shift;
@@ -65,6 +74,12 @@ template <int DT>
 constexpr int kQParts = DT == DT_BF16 ? 1 : DT == DT_F16 ? 2 : 3;
 template <int DT>
 constexpr int kPParts = DT == DT_F32 ? 3 : 2;
+
+// Whether fp16 probabilities serve whatever the scales are.  The other formats take them first where there are many rows
+// (products bound those calls: 64-token trees 308 us, with them FIGURE); where a wave's loads do, the second way's registers
+// cost more than the products save.
+template <int DT, int FMT>
+constexpr bool kHalfOnly = DT == DT_BF16 && FMT == FMT_NVFP4;
 
 template <int FMT, int D>
 struct Shape {
@@ -100,6 +115,18 @@ __device__ __forceinline__ uint32_t decode_pair(const uint32_t* w, float s) {
   if constexpr (FMT == FMT_FP8) return dec_fp8_bf16x2<(I & 1) != 0>(w[I / 2], s);
   else return dec_fp4_bf16x2<I & 3>(w[I / 4], s);
 }
+// The same as a pair of fp16.
+template <int FMT, int I>
+__device__ __forceinline__ uint32_t decode_pair_half(const uint32_t* w, float s) {
+  if constexpr (FMT == FMT_FP8)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[I / 2], s, (I & 1) != 0));
+  else return dec_fp4_f16x2<I & 3>(w[I / 4], s);
+}
+template <bool HALF, int FMT, int I>
+__device__ __forceinline__ uint32_t decode_value(const uint32_t* w, float s) {
+  if constexpr (HALF) return decode_pair_half<FMT, I>(w, s);
+  else return decode_pair<FMT, I>(w, s);
+}
 // Scale byte -> scale for the conversions, which take its exponent: for E8M0 that is the byte (0 means 2^-127 and 0xFF NaN
 // there too, bit for bit over every code).
 template <int FMT>
@@ -129,6 +156,23 @@ __device__ __forceinline__ int least_odd(int e) {
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8_t, u32x4_t{a, b, c, d});
 }
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+// Values times probabilities, bf16 or fp16.
+template <bool HALF>
+__device__ __forceinline__ f32x4_t mfma_value(u32x4_t a, u32x4_t b, f32x4_t c) {
+  if constexpr (HALF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+// Whether eight scale bytes keep every code of theirs exact in fp16: 448 or 6 times the scale within 65504, 2^-9 or 0.5
+// times it no less than 2^-24.
+template <int FMT>
+__device__ __forceinline__ bool fits_half(uint32_t least, uint32_t most) {
+  if constexpr (FMT == FMT_FP8) return least >= 112 && most <= 134;
+  else if constexpr (FMT == FMT_MXFP4) return least >= 104 && most <= 140;
+  else return true;
+}
 __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -155,6 +199,23 @@ __device__ __forceinline__ bf16x8_t take_part(float (&x)[8], bool last, const Mi
     }
   }
   return as_bf16x8(w[0], w[1], w[2], w[3]);
+}
+// A loaded value, not looked at before this point: what is computed from it (a scale from its byte) would otherwise be
+// moved up to the load, and the wait for the load with it, before the products that are to hide it.
+template <int N>
+__device__ __forceinline__ void from_here(uint32_t (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
+}
+template <int N, int M>
+__device__ __forceinline__ void from_here(uint32_t (&x)[N][M]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) from_here(x[i]);
+}
+template <int N, int M, int L>
+__device__ __forceinline__ void from_here(uint32_t (&x)[N][M][L]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) from_here(x[i]);
 }
 // Over the four lanes that hold a row (16 apart).
 __device__ __forceinline__ float row_max(float v) {
@@ -251,9 +312,10 @@ __device__ __forceinline__ void mask_scores(const AttnArgs& a, const Work& w, in
 }
 
 // Probabilities of a tile's scores in bf16 parts, and the rows' running maximum m, sum l and sums o.
-template <int MT, int PP, int NT>
+// (m is what the exponents are taken relative to; for fp16 a row's largest probability is 2^6 when it moves.)
+template <bool HALF, int MT, int PP, int NT>
 __device__ __forceinline__ void softmax_step(const f32x4_t (&s)[MT][2], float scale, const MinusOne& minus, float (&m)[MT],
-                                             float (&l)[MT], f32x4_t (&o)[MT][NT], bf16x8_t (&p)[MT][PP]) {
+                                             float (&l)[MT], f32x4_t (&o)[MT][NT], u32x4_t (&p)[MT][PP]) {
   float top[MT];
   bool past = false;
 #pragma unroll
@@ -262,12 +324,12 @@ __device__ __forceinline__ void softmax_step(const f32x4_t (&s)[MT][2], float sc
 #pragma unroll
     for (int i = 1; i < 8; ++i) top[mt] = fmaxf(top[mt], s[mt][i / 4][i % 4]);
     top[mt] *= scale;
-    past |= top[mt] > m[mt] + kLazy;
+    past |= top[mt] > m[mt] + kOver<HALF>;
   }
   if (__ballot(past) != 0) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float to = fmaxf(m[mt], row_max(top[mt]));
+      const float to = fmaxf(m[mt], row_max(top[mt]) - kAtMove<HALF>);
       const float keep = m[mt] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[mt] - to);
       m[mt] = to;
       l[mt] *= keep;
@@ -285,15 +347,25 @@ __device__ __forceinline__ void softmax_step(const f32x4_t (&s)[MT][2], float sc
       l[mt] += e[i];
     }
 #pragma unroll
-    for (int part = 0; part < PP; ++part) p[mt][part] = take_part(e, part == PP - 1, minus);
+    for (int part = 0; part < PP; ++part) {
+      if constexpr (HALF) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[mt][part][i] =
+              __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{e[2 * i], e[2 * i + 1]}, f16x2_t));
+      } else {
+        p[mt][part] = __builtin_bit_cast(u32x4_t, take_part(e, part == PP - 1, minus));
+      }
+    }
   }
 }
 
 // ------------------------------------------------------------------ one piece
-template <int DT, int FMT, int D, int MT>
+template <int DT, int FMT, int D, int MT, bool HALF>
 struct Attention {
   using S = Shape<FMT, D>;
-  static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
+  using Other = std::conditional_t<HALF && !kHalfOnly<DT, FMT>, Attention<DT, FMT, D, MT, false>, void>;
+  static constexpr int QP = kQParts<DT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
   static constexpr int kTilesV = D / 16, kType = DT;
   // waves of a SIMD that the registers are kept to, which is workgroups of a CU
   static constexpr int kWaves = D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
@@ -312,6 +384,7 @@ struct Attention {
     __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
     __attribute__((aligned(16))) uint8_t nan[kRows * D];   // outputs that a value that is not finite reached
     float m[4][kRows], l[4][kRows];
+    int again;                                             // a scale was met that fp16 does not hold
     int first[kThreads];                                   // prefix sums of the schedule
     int sums[4];
   };
@@ -522,7 +595,7 @@ struct Attention {
     });
   }
   // O^T += V^T P^T.
-  __device__ __forceinline__ void values(const V& v, const bf16x8_t (&p)[MT][PP], int pass, int passes, f32x4_t (&o)[MT][kTilesV]) const {
+  __device__ __forceinline__ void values(const V& v, const u32x4_t (&p)[MT][PP], int pass, int passes, f32x4_t (&o)[MT][kTilesV]) const {
     static_for<S::VU>([&](auto U) {
       constexpr int u = decltype(U)::value;
       float sc[8][S::VS];
@@ -534,7 +607,7 @@ struct Attention {
         constexpr int i = decltype(I)::value, is = i / 8 < S::VS ? i / 8 : 0;
         uint32_t x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = decode_pair<FMT, i>(v.w[j][u], sc[j][is]);
+        for (int j = 0; j < 8; ++j) x[j] = decode_value<HALF, FMT, i>(v.w[j][u], sc[j][is]);
         uint32_t y[2][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -548,7 +621,8 @@ struct Attention {
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
-              o[mt][t + half] = mfma(as_bf16x8(y[half][0], y[half][1], y[half][2], y[half][3]), p[mt][part], o[mt][t + half]);
+              o[mt][t + half] =
+                  mfma_value<HALF>(u32x4_t{y[half][0], y[half][1], y[half][2], y[half][3]}, p[mt][part], o[mt][t + half]);
       });
     });
   }
@@ -613,8 +687,10 @@ struct Attention {
   }
 
   // Steps [first, last) of the problem, this wave's tile of each; `whole`: they are all, else the sums go to `slot`.
-  __device__ __forceinline__ void piece(int first, int last, bool whole, float* slot) {
+  // False, with nothing written, where fp16 does not hold the values.
+  __device__ __forceinline__ bool piece(int first, int last, bool whole, float* slot) {
     place();
+    if (wave == 0 && lane == 0) sm.again = 0;
     for (int i = wave * 64 + lane; i < kRows * D / 16; i += kAttnThreads)
       *reinterpret_cast<u32x4_t*>(sm.nan + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
     Q q;
@@ -639,12 +715,17 @@ struct Attention {
       V v;
       load_k(k, now, t);
       load_v(v, now, t);
+      // the first bytes, as words: were all of them bytes that are widened, the widening would wait at the loads
+      from_here(k.s);
+      from_here(v.s);
       // One tile, while the next one's rows are on their way: its keys from the scores on, its values from the values on.
       // (After the last tile that is the same tile again, from the caches.)
       while (true) {
         f32x4_t s[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        from_here(k.w);
+        from_here(k.s);
         int passes = passes_of(k.w, k.s);
         for (int pass = 0;;) {
           scores(k, q, pass, passes, s);
@@ -654,8 +735,26 @@ struct Attention {
         const int beyond = ahead + 4 < end ? ahead + 4 : ahead;
         const Pages after = pages_of(beyond);
         if (!(now.there[0] && now.there[1] && (t + 1) * kTile <= w.known)) mask(now, t, s, v);
-        bf16x8_t p[MT][PP];
-        softmax_step<MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
+        if constexpr (HALF && !kHalfOnly<DT, FMT>) {
+          uint32_t least = 255, most = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+              for (int i = 0; i < S::VS; ++i) {
+                least = min(least, v.s[j][u][i]);
+                most = max(most, v.s[j][u][i]);
+              }
+          if (__ballot(!fits_half<FMT>(least, most)) != 0) {
+            if (lane == 0) sm.again = 1;
+            break;
+          }
+        }
+        u32x4_t p[MT][PP];
+        softmax_step<HALF, MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
+        from_here(v.w);
+        from_here(v.s);
         passes = passes_of(v.w, v.s);
         for (int pass = 0;;) {
           values(v, p, pass, passes, o);
@@ -669,13 +768,14 @@ struct Attention {
         ahead = beyond;
       }
     }
-    join(o, m, l, whole, slot);
+    return join(o, m, l, whole, slot);
   }
 
   // The four waves' sums joined: written as outputs, or as a part of them.
-  __device__ __forceinline__ void join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
+  __device__ __forceinline__ bool join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
     place();
     __syncthreads();      // q's fragments, and the last piece's sums, have been read
+    if (HALF && __builtin_amdgcn_readfirstlane(sm.again)) return false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       l[mt] = row_sum(l[mt]);
@@ -745,6 +845,7 @@ struct Attention {
         write_row<DT, 8>(a, row_at(at), D, ch, x, top, at < live ? sum : 0.0f);
       }
     }
+    return true;
   }
 };
 
@@ -753,10 +854,11 @@ struct Attention {
 // quarter to each wave, into LDS as the fragments that the products take, and each wave takes all of them for 16 * MT rows
 // of its own.  Decoding costs four times less a row than where each wave decodes what it reads, and needs no registers
 // beside the sums.  LDS holds one step (64 KB); two workgroups of a CU take turns at decoding and products.
-template <int DT, int FMT, int D, int MT, int WAVES>
+template <int DT, int FMT, int D, int MT, int WAVES, bool HALF>
 struct SharedAttention {
   using S = Shape<FMT, D>;
-  static constexpr int QP = kQParts<DT>, PP = kPParts<DT>, kDim = D, kType = DT;
+  using Other = std::conditional_t<HALF && !kHalfOnly<DT, FMT>, SharedAttention<DT, FMT, D, MT, WAVES, false>, void>;
+  static constexpr int QP = kQParts<DT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kType = DT;
   static constexpr int kTilesV = D / 16, kThreads = 64 * WAVES, kRows = 16 * MT * WAVES;
   static constexpr int kStep = D <= 128 ? kTile * WAVES : 4096 * WAVES / D, kTiles = kStep / kTile;
   // waves of a SIMD that the registers are kept to: two where q and the sums leave room for it
@@ -777,6 +879,7 @@ struct SharedAttention {
     uint32_t nan[kRows][kWords];          // outputs that one reached
     int marked;                           // the step that `odd` is of
     int there[kTiles];                    // which halves of a tile have a page
+    int again;                            // a scale was met that fp16 does not hold
     int first[kThreads];
     int sums[4];
   };
@@ -870,17 +973,32 @@ struct SharedAttention {
     }
   }
   // Two channels in bf16; a scale that is more than its exponent is multiplied in fp32 (exact, as the product is in bf16).
-  template <bool EXACT, int I>
+  template <bool EXACT, bool TO_HALF, int I>
   __device__ __forceinline__ static uint32_t decode(const uint32_t* words, float s) {
-    if constexpr (!EXACT) return decode_pair<FMT, I>(words, s);
+    if constexpr (!EXACT) return decode_value<TO_HALF, FMT, I>(words, s);
     const uint32_t v = decode_pair<FMT, I>(words, 1.0f);
-    return pack_bf16(bf16_lo(v) * s, bf16_hi(v) * s);
+    const float lo = bf16_lo(v) * s, hi = bf16_hi(v) * s;
+    if constexpr (TO_HALF) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, f16x2_t));
+    return pack_bf16(lo, hi);
   }
   // Raw to LDS; positions that are none become 0, and values of partly attended tiles that are not finite too, with a mark.
   __device__ __forceinline__ void decode_step(Raw& x, int step, int tag) const {
     const int t = my_tile(step);
+    from_here(x.k);
+    from_here(x.ks);
+    from_here(x.v);
+    from_here(x.vs);
     if (lane == 0) sm.there[wave / kPartsOfTile] = (int)(x.page[0] >= 0) + 2 * (int)(x.page[1] >= 0);   // each part says the same
     if (!(x.page[0] >= 0 && x.page[1] >= 0 && (t + 1) * kTile <= w.known)) clean(x, t, tag);
+    if constexpr (HALF && !kHalfOnly<DT, FMT>) {
+      uint32_t least = 255, most = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        least = min(least, x.vs[j]);
+        most = max(most, x.vs[j]);
+      }
+      if (__ballot(!fits_half<FMT>(least, most)) != 0 && lane == 0) sm.again = 1;
+    }
     if constexpr (FMT == FMT_NVFP4) {
       bool any = false;
 #pragma unroll
@@ -909,7 +1027,7 @@ struct SharedAttention {
           constexpr int hf = decltype(H)::value, is = hf / 2 < S::KS ? hf / 2 : 0;
           uint32_t y[4];
           static_for<4>([&](auto I) {
-            y[decltype(I)::value] = decode<EXACT, hf * 4 + decltype(I)::value>(x.k[h][u], sc[is]);
+            y[decltype(I)::value] = decode<EXACT, false, hf * 4 + decltype(I)::value>(x.k[h][u], sc[is]);
           });
           sm.key[slot][kHalves == 2 ? h : my_half()][(my_unit() + u) * S::kHalves + hf][lane] = u32x4_t{y[0], y[1], y[2], y[3]};
         });
@@ -921,7 +1039,7 @@ struct SharedAttention {
       constexpr int i = decltype(I)::value;
       uint32_t y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = decode<EXACT, i>(x.v[j], sc[j]);
+      for (int j = 0; j < 8; ++j) y[j] = decode<EXACT, HALF, i>(x.v[j], sc[j]);
       uint32_t z[2][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -964,12 +1082,16 @@ struct SharedAttention {
     }
   }
 
-  // Steps [first, last) of the problem; `whole`: they are all, else the sums go to `slot`.
-  __device__ __forceinline__ void piece(int first, int last, bool whole, float* slot) {
+  // Steps [first, last) of the problem; `whole`: they are all, else the sums go to `slot`.  False, with nothing written,
+  // where fp16 does not hold the values.
+  __device__ __forceinline__ bool piece(int first, int last, bool whole, float* slot) {
     place();
     for (int i = wave * 64 + lane; i < kRows * kWords; i += kThreads) sm.nan[i / kWords][i % kWords] = 0;
     for (int i = wave * 64 + lane; i < kStep * kWords; i += kThreads) sm.odd[i / kWords][i % kWords] = 0;
-    if (wave == 0 && lane == 0) sm.marked = -1;
+    if (wave == 0 && lane == 0) {
+      sm.marked = -1;
+      sm.again = 0;
+    }
     bf16x8_t q[MT][S::kSteps][QP];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -999,6 +1121,8 @@ struct SharedAttention {
       Raw x;
       look_up(x.next, first);
       load(x, first);
+      from_here(x.ks);                     // as words, as the loads of the other variant's first tile
+      from_here(x.vs);
       bool odd = false;
       for (int step = first; step < last; ++step) {
         __syncthreads();                   // the fragments of the step before have been read
@@ -1008,12 +1132,14 @@ struct SharedAttention {
         }
         decode_step(x, step, step);
         __syncthreads();
+        if (HALF && !kHalfOnly<DT, FMT> && __builtin_amdgcn_readfirstlane(sm.again)) return false;
         odd = __builtin_amdgcn_readfirstlane(sm.marked) == step;
         if (step + 1 < last) load(x, step + 1);
         if (works) products(step, q, odd, m, l, o);
       }
     }
     finish(o, m, l, whole, slot);
+    return true;
   }
   __device__ __forceinline__ void products(int step, const bf16x8_t (&q)[MT][S::kSteps][QP], bool odd, float (&m)[MT],
                                            float (&l)[MT], f32x4_t (&o)[MT][kTilesV]) const {
@@ -1052,19 +1178,19 @@ struct SharedAttention {
             }
         }
       }
-      bf16x8_t p[MT][PP];
-      softmax_step<MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
+      u32x4_t p[MT][PP];
+      softmax_step<HALF, MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
 #pragma unroll
       for (int t = 0; t < kTilesV; t += 2) {
-        bf16x8_t val[2];
+        u32x4_t val[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) val[h] = __builtin_bit_cast(bf16x8_t, sm.value[ti][t + h][lane]);
+        for (int h = 0; h < 2; ++h) val[h] = sm.value[ti][t + h][lane];
 #pragma unroll
         for (int part = 0; part < PP; ++part)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) o[mt][t + h] = mfma(val[h], p[mt][part], o[mt][t + h]);
+            for (int mt = 0; mt < MT; ++mt) o[mt][t + h] = mfma_value<HALF>(val[h], p[mt][part], o[mt][t + h]);
       }
     }
   }
@@ -1123,17 +1249,35 @@ __device__ __forceinline__ int attn_scan(int v, int* sums, int& total) {
   return below;
 }
 
+// A piece, with fp16 probabilities where they are enough.
+template <class A>
+__device__ __forceinline__ void work_on(const AttnArgs& a, typename A::Shared& sm, int b, int kv, int tile, const Work& w,
+                                        int first, int last, bool whole, float* slot) {
+  A x(a, sm);
+  x.b = b;
+  x.kv = kv;
+  x.tile = tile;
+  x.w = w;
+  if (x.piece(first, last, whole, slot)) return;
+  if constexpr (!std::is_same_v<typename A::Other, void>) {
+    __syncthreads();
+    typename A::Other y(a, reinterpret_cast<typename A::Other::Shared&>(sm));
+    y.b = b;
+    y.kv = kv;
+    y.tile = tile;
+    y.w = w;
+    y.piece(first, last, whole, slot);
+  }
+}
+
 // One workgroup for each problem.
 template <class A>
 __global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention(AttnArgs a) {
   __shared__ typename A::Shared sm;
-  A x(a, sm);
   const int each = a.d.kv_heads * a.d.row_tiles;
-  x.b = blockIdx.x / each;
-  x.kv = (blockIdx.x - x.b * each) / a.d.row_tiles;
-  x.tile = blockIdx.x % a.d.row_tiles;
-  x.w = work_of_all<A>(a, x.b);
-  x.piece(0, x.tile < x.w.tiles ? x.w.steps : 0, true, nullptr);
+  const int b = blockIdx.x / each, kv = (blockIdx.x - b * each) / a.d.row_tiles, tile = blockIdx.x % a.d.row_tiles;
+  const Work w = work_of_all<A>(a, b);
+  work_on<A>(a, sm, b, kv, tile, w, 0, tile < w.tiles ? w.steps : 0, true, nullptr);
 }
 
 // The steps of all problems shared out evenly: workgroup w takes those of share_of, a piece of a problem at a time.  A
@@ -1141,7 +1285,6 @@ __global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention(Attn
 template <class A>
 __global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention_split(AttnArgs a) {
   __shared__ typename A::Shared sm;
-  A x(a, sm);
   int total = 0;
   for (int b0 = 0; b0 < a.d.sequences; b0 += A::kThreads) {
     int sum;
@@ -1164,15 +1307,13 @@ __global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention_spli
       int lo = 0;                   // the last sequence of the chunk that starts at or before u, and is not empty
       for (int s = A::kThreads / 2; s > 0; s /= 2)
         if (__builtin_amdgcn_readfirstlane(sm.first[lo + s]) <= u) lo += s;
-      x.b = b0 + lo;
-      x.w = work_of_all<A>(a, x.b);
-      const int local = u - __builtin_amdgcn_readfirstlane(sm.first[lo]), problem = local / x.w.steps;
-      const int step = local - problem * x.w.steps;
-      x.kv = problem / x.w.tiles;
-      x.tile = problem - x.kv * x.w.tiles;
-      const int n = min(x.w.steps - step, end - u);
-      const bool whole = n == x.w.steps;
-      x.piece(step, step + n, whole, a.parts + (int64_t)(2 * me + (step == 0)) * kSlotFloats<A>);
+      const int seq = b0 + lo;
+      const Work w = work_of_all<A>(a, seq);
+      const int local = u - __builtin_amdgcn_readfirstlane(sm.first[lo]), problem = local / w.steps;
+      const int step = local - problem * w.steps, kv = problem / w.tiles;
+      const int n = min(w.steps - step, end - u);
+      work_on<A>(a, sm, seq, kv, problem - kv * w.tiles, w, step, step + n, n == w.steps,
+                 a.parts + (2 * me + (step == 0)) * kSlotFloats<A>);
       u += n;
       __syncthreads();
     }
@@ -1278,8 +1419,10 @@ inline int attention_rows(int dim, int64_t rows) {
 }
 template <int DT, int FMT, int D, int ROWS>
 struct KernelOf {
-  using Type = std::conditional_t<(ROWS <= 32), Attention<DT, FMT, D, (ROWS <= 32 ? ROWS / 16 : 1)>,
-                                  SharedAttention<DT, FMT, D, (D <= 128 ? 2 : 1), (ROWS == 64 && D <= 128 ? 2 : 4)>>;
+  using Type = std::conditional_t<
+      (ROWS <= 32), Attention<DT, FMT, D, (ROWS <= 32 ? ROWS / 16 : 1), kHalfOnly<DT, FMT>>,
+      SharedAttention<DT, FMT, D, (D <= 128 ? 2 : 1), (ROWS == 64 && D <= 128 ? 2 : 4),
+                      (kHalfOnly<DT, FMT> || (DT == DT_BF16 && D <= 256))>>;
 };
 // What the launches have to know of a kernel.
 struct AttnShape {

@@ -11,8 +11,11 @@ from oracle import paged
 from tests.gpu_util import DTYPES, dev
 from tests.moe_util import U, assert_rounded, f64
 
-# What the probabilities are off by before the products: two bf16 parts (two half steps of 2^-8), three for fp32.
-PARTS = {"bf16": 2.0 ** -16, "f16": 2.0 ** -16, "f32": 2.0 ** -24}
+# What the probabilities are off by before the products: for bf16 outputs one fp16 part (a half step of 2^-11) or two bf16
+# parts, two bf16 parts (two half steps of 2^-8) for fp16, three for fp32.
+PARTS = {"bf16": 2.0 ** -11, "f16": 2.0 ** -16, "f32": 2.0 ** -24}
+# And of a row's largest: fp16's spacing of 2^-24 below 2^-14, half of it, where the largest is 2^6.
+FLOOR = {"bf16": 2.0 ** -31, "f16": 0.0, "f32": 0.0}
 
 
 def pools(g, pages, heads, size, dim, fmt, block, shared=False, std=1.0):
@@ -77,7 +80,7 @@ def check_attention(q, cache, table, what, gpu=None, mask=None, counts=None, sca
     relative error of each probability; exp2 adds 2 roundings, the parts of p their remainder, the two sums over n
     positions n + 64 roundings each (64: the joining of parts), the division 1.  Relative to the largest one, a
     probability below 2^-126, and what a part below that holds, is 0 in fp32 and bf16: with up to three parts and the
-    probability itself 4 * 2^-126 of a value's size for each position."""
+    probability itself 4 * 2^-126 of a value's size for each position (2^-31 where parts are fp16)."""
     c, t = gpu if gpu is not None else (on_gpu(cache), table_on_gpu(table))
     put = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to(dev())  # noqa: E731
     out, lse = mxq.cache_attention(q.to(dev()), c, t, mask=put(mask), counts=put(counts), scale=scale, return_lse=True)
@@ -85,7 +88,7 @@ def check_attention(q, cache, table, what, gpu=None, mask=None, counts=None, sca
     D = q.shape[-1]
     off = 2 * reach * (D + 6) * U + 2 * U
     rel = 2 * off + PARTS[dtype] + (2 * met + 140) * U
-    gone = 4 * 2.0 ** -126 * met[..., None] * peak
+    gone = (4 * 2.0 ** -126 + FLOOR[dtype]) * met[..., None] * peak
     assert_rounded(out, want, dtype, rel[..., None] * mass + gone, f"{what} out")
     got_lse = f64(lse)
     empty = met == 0
