@@ -6,9 +6,6 @@ namespace {
 
 // Steps are shared out among as many workgroups as run at a time.
 constexpr int kComputeUnits = 256;
-#ifndef OVER
-#define OVER 1
-#endif
 // From so many problems on each has a workgroup of its own: there are enough of them to keep the card busy.
 constexpr int64_t kManyProblems = 2048;
 // Problems of so many steps at most are not worth sharing.
@@ -42,7 +39,7 @@ Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64
   (void)kernels(nullptr, dt, c.fmt, c.head_dim, p.rows, 0, &shape, nullptr);
   const int64_t steps = (width * c.page_size + shape.step - 1) / shape.step;
   const bool split = p.problems < kManyProblems && steps > kFewSteps && p.problems * steps < (int64_t(1) << 31);
-  p.workgroups = split ? kComputeUnits * shape.resident * OVER : 0;
+  p.workgroups = split ? kComputeUnits * shape.resident : 0;
   return p;
 }
 

@@ -76,7 +76,7 @@ template <int DT>
 constexpr int kPParts = DT == DT_F32 ? 3 : 2;
 
 // Whether fp16 probabilities serve whatever the scales are.  The other formats take them first where there are many rows
-// (products bound those calls: 64-token trees 308 us, with them FIGURE); where a wave's loads do, the second way's registers
+// (products bound those calls: 64-token trees 311 us, with them 273); where a wave's loads do, the second way's registers
 // cost more than the products save.
 template <int DT, int FMT>
 constexpr bool kHalfOnly = DT == DT_BF16 && FMT == FMT_NVFP4;
