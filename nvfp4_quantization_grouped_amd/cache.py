@@ -98,41 +98,41 @@ def page_table(sequences, width, cache):
 
 def _cache_args(cache, name):
     """The cache as the C ABI takes it, and its device."""
-    if cache.format not in _FMT:
+    kc, ks, vc, vs, form = cache
+    fmt = _FMT.get(form)
+    if fmt is None:
         raise ValueError(f"{name}: format must be 'fp8', 'mxfp4' or 'nvfp4'")
-    kc, ks, vc, vs = cache[:4]
     if (vc is None) != (vs is None):
         raise ValueError(f"{name}: v_codes and v_scales belong together")
     device = kc.device
-    for pool in cache[:4]:
-        if pool is None:
-            continue
+    for pool in (kc, ks) if vc is None else (kc, ks, vc, vs):
         if not pool.is_cuda:
             raise ValueError("libmxq ops take GPU tensors only (there is no CPU implementation)")
         if pool.device != device:
             raise ValueError("all tensors must be on the same device")
-        if pool.dtype != torch.uint8 or pool.dim() != 4:
+        if pool.dtype is not torch.uint8 or pool.dim() != 4:
             raise TypeError(f"{name}: pools must be uint8 [pages, kv_heads, page_size, width]")
         if not pool.is_contiguous():
             raise ValueError(f"{name}: pools must be contiguous")
-    pages, heads, size, width = kc.shape
-    dim, groups = width * (1 if cache.format == "fp8" else 2), ks.shape[3]
-    if ks.shape[:3] != kc.shape[:3] or groups == 0 or dim % groups or (
-            vc is not None and (vc.shape != kc.shape or vs.shape != ks.shape)):
+    codes, scales = kc.shape, ks.shape
+    pages, heads, size, width = codes
+    groups = scales[3]
+    dim = width if form == "fp8" else 2 * width
+    if scales[0] != pages or scales[1] != heads or scales[2] != size or groups == 0 or dim % groups or (
+            vc is not None and (vc.shape != codes or vs.shape != scales)):
         raise ValueError(f"{name}: pools of different shapes")
-    return _lib.Cache(pages, size, heads, dim, _FMT[cache.format], dim // groups, kc.data_ptr(), ks.data_ptr(),
-                      _ptr(vc), _ptr(vs)), device
+    return _lib.Cache(pages, size, heads, dim, fmt, dim // groups, kc.data_ptr(), ks.data_ptr(),
+                      0 if vc is None else vc.data_ptr(), 0 if vs is None else vs.data_ptr()), device
 
 
 def _table_args(table, pages, device, name):
     """The table's tensors, contiguous."""
     rows, lengths, refs = table
-    for t, dims in ((rows, 2), (lengths, 1), (refs, 1)):
-        if t.dtype != torch.int32 or t.dim() != dims:
-            raise TypeError(f"{name}: the table must be int32 pages [sequences, width], lengths [sequences] and refs "
-                            "[pages]")
-        if t.device != device:
-            raise ValueError("all tensors must be on the same device")
+    if (rows.dtype is not torch.int32 or lengths.dtype is not torch.int32 or refs.dtype is not torch.int32
+            or rows.dim() != 2 or lengths.dim() != 1 or refs.dim() != 1):
+        raise TypeError(f"{name}: the table must be int32 pages [sequences, width], lengths [sequences] and refs [pages]")
+    if rows.device != device or lengths.device != device or refs.device != device:
+        raise ValueError("all tensors must be on the same device")
     if lengths.shape[0] != rows.shape[0] or (pages is not None and refs.shape[0] != pages):
         raise ValueError(f"{name}: the table's lengths must be [sequences] and refs [pages of the cache]")
     return rows.contiguous(), lengths.contiguous(), refs.contiguous()
@@ -244,7 +244,7 @@ def cache_attention(q, cache, table, *, mask=None, counts=None, scale=None, retu
     q = q.contiguous()
     if q.data_ptr() & 15:
         q = q.clone()
-    out = torch.empty(B, T, H, D, dtype=q.dtype, device=device)
+    out = torch.empty_like(q)
     lse = torch.empty(B, T, H, dtype=torch.float32, device=device) if return_lse else None
     ref = ctypes.byref(args)
     work, need = _workspace("cache_attention", device, ref, B, rows.shape[1], dt, T, H)
@@ -257,8 +257,10 @@ def cache_attention(q, cache, table, *, mask=None, counts=None, scale=None, retu
 # -------------------------------------------------------------------- pages
 def _fork(name, table, page_size, parents, children, keep, release):
     rows, lengths, refs = table
-    out = PageTable(rows.new_empty((children, rows.shape[1])), rows.new_empty(children), torch.empty_like(refs))
-    _call("cache_fork", rows.device, _ptr(rows), rows.shape[0], rows.shape[1], _ptr(lengths), _ptr(refs), refs.shape[0],
+    device = rows.device
+    out = PageTable(torch.empty((children, rows.shape[1]), dtype=torch.int32, device=device),
+                    torch.empty(children, dtype=torch.int32, device=device), torch.empty_like(refs))
+    _call("cache_fork", device, _ptr(rows), rows.shape[0], rows.shape[1], _ptr(lengths), _ptr(refs), refs.shape[0],
           page_size, _ptr(parents), children, _ptr(keep), int(release), *(_ptr(t) for t in out))
     return out
 
