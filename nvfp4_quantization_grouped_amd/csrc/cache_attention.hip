@@ -35,10 +35,11 @@ Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64
   p.rows = attention_rows(c.head_dim, rows);
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   p.problems = sequences * c.kv_heads * p.row_tiles;
-  AttnShape shape = {128, 1};
+  AttnShape shape = {128, 0, 1};
   (void)kernels(nullptr, dt, c.fmt, c.head_dim, p.rows, 0, &shape, nullptr);
   const int64_t steps = (width * c.page_size + shape.step - 1) / shape.step;
-  const bool split = p.problems < kManyProblems && steps > kFewSteps && p.problems * steps < (int64_t(1) << 31);
+  const bool split = p.problems < kManyProblems && steps > kFewSteps &&
+                     p.problems * (steps + shape.start) < (int64_t(1) << 31);
   p.workgroups = split ? kComputeUnits * shape.resident : 0;
   return p;
 }

@@ -21,7 +21,7 @@
 //
 // Roundings.  Codes times scales have at most 6 significant bits and are exact
 // in bf16.  q of fp16 / fp32 enters as 2 / 3 bf16 parts (exact but for what
-// lies 2^-24 below).  Probabilities are a choice: one bf16 part, up to 2^-8 of
+// lies 2^-24 below), or fp16 as it is where the keys are exact in fp16 too.  Probabilities are a choice: one bf16 part, up to 2^-8 of
 // each, would make the error of bf16 outputs 1.4 times what rounding them costs;
 // two parts (three for fp32 outputs) leave nothing to see, at as many products.
 // For bf16 outputs one fp16 part does (2^-11; the error is 1.01 times the
@@ -70,8 +70,11 @@ struct AttnArgs {
 };
 
 // ------------------------------------------------------------------- shapes
-template <int DT>
-constexpr int kQParts = DT == DT_BF16 ? 1 : DT == DT_F16 ? 2 : 3;
+// Whether keys and q multiply as fp16: q is, and the keys fit whatever their scales are.
+template <int DT, int FMT>
+constexpr bool kHalfKeys = DT == DT_F16 && FMT == FMT_NVFP4;
+template <int DT, int FMT>
+constexpr int kQParts = DT == DT_BF16 || kHalfKeys<DT, FMT> ? 1 : DT == DT_F16 ? 2 : 3;
 template <int DT>
 constexpr int kPParts = DT == DT_F32 ? 3 : 2;
 
@@ -173,8 +176,9 @@ __device__ __forceinline__ bool fits_half(uint32_t least, uint32_t most) {
   else if constexpr (FMT == FMT_MXFP4) return least >= 104 && most <= 140;
   else return true;
 }
-__device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+template <bool HALF>
+__device__ __forceinline__ f32x4_t mfma_key(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return mfma_value<HALF>(__builtin_bit_cast(u32x4_t, a), __builtin_bit_cast(u32x4_t, b), c);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));     // one conversion of two
@@ -199,6 +203,20 @@ __device__ __forceinline__ bf16x8_t take_part(float (&x)[8], bool last, const Mi
     }
   }
   return as_bf16x8(w[0], w[1], w[2], w[3]);
+}
+// q's parts: eight values of them.
+template <int DT, int FMT>
+__device__ __forceinline__ void parts_of(float (&x)[8], const MinusOne& minus, bf16x8_t (&part)[kQParts<DT, FMT>]) {
+  if constexpr (kHalfKeys<DT, FMT>) {
+    u32x4_t w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{x[2 * i], x[2 * i + 1]}, f16x2_t));
+    part[0] = __builtin_bit_cast(bf16x8_t, w);
+  } else {
+#pragma unroll
+    for (int p = 0; p < kQParts<DT, FMT>; ++p) part[p] = take_part(x, p == kQParts<DT, FMT> - 1, minus);
+  }
 }
 // A loaded value, not looked at before this point: what is computed from it (a scale from its byte) would otherwise be
 // moved up to the load, and the wait for the load with it, before the products that are to hide it.
@@ -255,16 +273,19 @@ template <class A>
 __device__ __forceinline__ Work work_of_all(const AttnArgs& a, int b) {
   return work_of<A>(a, uniform_load(a.lengths, b), a.counts ? uniform_load(a.counts, b) : a.d.tokens);
 }
-// Steps of a thread's sequence, all its problems together.
+// Units of a thread's sequence, all its problems together: steps, and for each problem kStart before them, as many as
+// beginning and ending a piece takes the time of (12 to 18 us), so that a workgroup whose share ends one problem and begins
+// another does fewer steps (16-token trees 105 -> 97 us, 100 and 98 with 2 and 6 of them; [4, 8192, 512] 47 -> 42, 64
+// contexts of 16384 142 -> 138).
 template <class A>
 __device__ __forceinline__ int units_of(const AttnArgs& a, int b) {
   if (b >= a.d.sequences) return 0;
   const Work w = work_of<A>(a, a.lengths[b], a.counts ? a.counts[b] : a.d.tokens);
-  return w.steps * w.tiles * a.d.kv_heads;
+  return w.steps > 0 ? (w.steps + A::kStart) * w.tiles * a.d.kv_heads : 0;
 }
-// Steps [first, last) of all problems' that workgroup w of g takes.
+// Units [first, last) of all problems' that workgroup w of g takes.
 __device__ __forceinline__ int share_of(int w, int total, int g) { return (int)((int64_t)w * total / g); }
-// The workgroup that takes step u.
+// The workgroup that takes unit u.
 __device__ __forceinline__ int owner_of(int u, int total, int g) { return (int)((((int64_t)u + 1) * g - 1) / total); }
 
 // A part of a problem that several workgroups share: sums [rows][D], then m and l [rows].
@@ -365,11 +386,11 @@ template <int DT, int FMT, int D, int MT, bool HALF>
 struct Attention {
   using S = Shape<FMT, D>;
   using Other = std::conditional_t<HALF && !kHalfOnly<DT, FMT>, Attention<DT, FMT, D, MT, false>, void>;
-  static constexpr int QP = kQParts<DT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
+  static constexpr int QP = kQParts<DT, FMT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
   static constexpr int kTilesV = D / 16, kType = DT;
   // waves of a SIMD that the registers are kept to, which is workgroups of a CU
   static constexpr int kWaves = D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
-  static constexpr int kThreads = kAttnThreads, kResident = kWaves;
+  static constexpr int kThreads = kAttnThreads, kResident = kWaves, kStart = 4;
   // q's fragments stay in registers up to 32 of them, else in LDS
   static constexpr bool kQInRegs = D * QP * MT <= 256;
   static constexpr int kPad = D + 4;
@@ -426,8 +447,7 @@ struct Attention {
     if (a.d.negative)
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = -x[i];
-#pragma unroll
-    for (int p = 0; p < QP; ++p) part[p] = take_part(x, p == QP - 1, minus);
+    parts_of<DT, FMT>(x, minus, part);
   }
   struct Q {
     bf16x8_t f[kQInRegs ? MT : 1][kQInRegs ? S::kSteps : 1][QP];
@@ -579,7 +599,7 @@ struct Attention {
         for (int h = 0; h < 2; ++h) {
           uint32_t x[4];
           static_for<4>([&](auto I) {
-            x[decltype(I)::value] = decode_pair<FMT, hf * 4 + decltype(I)::value>(k.w[h][u], sc[h][is]);
+            x[decltype(I)::value] = decode_value<kHalfKeys<DT, FMT>, FMT, hf * 4 + decltype(I)::value>(k.w[h][u], sc[h][is]);
           });
           key[h] = as_bf16x8(x[0], x[1], x[2], x[3]);
         }
@@ -589,7 +609,7 @@ struct Attention {
           for (int mt = 0; mt < MT; ++mt) {
             const bf16x8_t f = q_part(q, mt, u * S::kHalves + hf, p);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) s[mt][h] = mfma(key[h], f, s[mt][h]);
+            for (int h = 0; h < 2; ++h) s[mt][h] = mfma_key<kHalfKeys<DT, FMT>>(key[h], f, s[mt][h]);
           }
       });
     });
@@ -858,12 +878,13 @@ template <int DT, int FMT, int D, int MT, int WAVES, bool HALF>
 struct SharedAttention {
   using S = Shape<FMT, D>;
   using Other = std::conditional_t<HALF && !kHalfOnly<DT, FMT>, SharedAttention<DT, FMT, D, MT, WAVES, false>, void>;
-  static constexpr int QP = kQParts<DT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kType = DT;
+  static constexpr int QP = kQParts<DT, FMT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kType = DT;
   static constexpr int kTilesV = D / 16, kThreads = 64 * WAVES, kRows = 16 * MT * WAVES;
   static constexpr int kStep = D <= 128 ? kTile * WAVES : 4096 * WAVES / D, kTiles = kStep / kTile;
   // waves of a SIMD that the registers are kept to: two where q and the sums leave room for it
-  static constexpr int kWaves = MT * (D / 8 * QP + D / 4) <= 192 ? 2 : 1;
+  static constexpr int kWaves = MT * (D / 8 * QP + D / 4) <= 160 ? 2 : 1;
   static constexpr int kResident = kWaves * 4 / WAVES;                 // workgroups of a CU
+  static constexpr int kStart = D == 512 ? 6 : 4;
   // a wave's share of a step: a tile, or of that a part:
   static constexpr int kPartsOfTile = WAVES / kTiles;
   static constexpr int kHalves = kPartsOfTile > 1 ? 1 : 2;             // halves of its positions for the keys
@@ -1027,7 +1048,7 @@ struct SharedAttention {
           constexpr int hf = decltype(H)::value, is = hf / 2 < S::KS ? hf / 2 : 0;
           uint32_t y[4];
           static_for<4>([&](auto I) {
-            y[decltype(I)::value] = decode<EXACT, false, hf * 4 + decltype(I)::value>(x.k[h][u], sc[is]);
+            y[decltype(I)::value] = decode<EXACT, kHalfKeys<DT, FMT>, hf * 4 + decltype(I)::value>(x.k[h][u], sc[is]);
           });
           sm.key[slot][kHalves == 2 ? h : my_half()][(my_unit() + u) * S::kHalves + hf][lane] = u32x4_t{y[0], y[1], y[2], y[3]};
         });
@@ -1103,8 +1124,7 @@ struct SharedAttention {
         if (a.d.negative)
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = -x[i];
-#pragma unroll
-        for (int p = 0; p < QP; ++p) q[mt][st][p] = take_part(x, p == QP - 1, minus);
+        parts_of<DT, FMT>(x, minus, q[mt][st]);
       }
     f32x4_t o[MT][kTilesV];
     float m[MT], l[MT];
@@ -1160,7 +1180,7 @@ struct SharedAttention {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) s[mt][h] = mfma(key[h], q[mt][st][p], s[mt][h]);
+            for (int h = 0; h < 2; ++h) s[mt][h] = mfma_key<kHalfKeys<DT, FMT>>(key[h], q[mt][st][p], s[mt][h]);
       }
       const int there = __builtin_amdgcn_readfirstlane(sm.there[ti]);
       if (there != 3 || (t + 1) * kTile > w.known) {
@@ -1309,13 +1329,16 @@ __global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention_spli
         if (__builtin_amdgcn_readfirstlane(sm.first[lo + s]) <= u) lo += s;
       const int seq = b0 + lo;
       const Work w = work_of_all<A>(a, seq);
-      const int local = u - __builtin_amdgcn_readfirstlane(sm.first[lo]), problem = local / w.steps;
-      const int step = local - problem * w.steps, kv = problem / w.tiles;
-      const int n = min(w.steps - step, end - u);
-      work_on<A>(a, sm, seq, kv, problem - kv * w.tiles, w, step, step + n, n == w.steps,
-                 a.parts + (2 * me + (step == 0)) * kSlotFloats<A>);
+      const int each = w.steps + A::kStart;
+      const int local = u - __builtin_amdgcn_readfirstlane(sm.first[lo]), problem = local / each;
+      const int from = local - problem * each, n = min(each - from, end - u), kv = problem / w.tiles;
+      const int step = max(from - A::kStart, 0), last = from + n - A::kStart;
+      if (last > step) {
+        work_on<A>(a, sm, seq, kv, problem - kv * w.tiles, w, step, last, last - step == w.steps,
+                   a.parts + (2 * me + (step == 0)) * kSlotFloats<A>);
+        __syncthreads();
+      }
       u += n;
-      __syncthreads();
     }
     base += sum;
     __syncthreads();
@@ -1357,7 +1380,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
   int w0 = 0, w1 = -1;
   const int g = min(a.d.workgroups, total);
   if (!none) {
-    first += (kv * w.tiles + tile) * w.steps;
+    first += (kv * w.tiles + tile) * (w.steps + A::kStart) + A::kStart;
     w0 = owner_of(first, total, g);
     w1 = owner_of(first + w.steps - 1, total, g);
     if (w0 == w1) return;
@@ -1426,7 +1449,7 @@ struct KernelOf {
 };
 // What the launches have to know of a kernel.
 struct AttnShape {
-  int step, resident;     // positions of a step; workgroups of a CU
+  int step, start, resident;     // positions of a step; units before a problem's steps; workgroups of a CU
 };
 
 template <class A>
@@ -1447,7 +1470,7 @@ hipError_t attention_dim(const AttnArgs* a, int dim, int rows, int64_t problems,
   if (dim == D && rows == ROWS) {                             \
     using A = typename KernelOf<DT, FMT, D, ROWS>::Type;      \
     if (a) return launch_attention_of<A>(*a, problems, st);   \
-    *shape = {A::kStep, A::kResident};                           \
+    *shape = {A::kStep, A::kStart, A::kResident};             \
     return hipSuccess;                                        \
   }
   CASE(64, 16)
