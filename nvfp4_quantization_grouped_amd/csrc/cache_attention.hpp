@@ -1113,18 +1113,20 @@ struct SharedAttention {
       sm.marked = -1;
       sm.again = 0;
     }
+    Raw x;
+    look_up(x.next, first);
     bf16x8_t q[MT][S::kSteps][QP];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int st = 0; st < S::kSteps; ++st) {
         const int ch = st / S::kHalves * 4 * S::KC + quarter * S::KC + st % S::kHalves * 8, r = row_of(mt);
-        float x[8] = {};
-        if (r < a.d.tokens * a.d.group) to_f32<DT>(load8<DT>(a.q, row_at(r) * D + ch, 8), x);
+        float e[8] = {};
+        if (r < a.d.tokens * a.d.group) to_f32<DT>(load8<DT>(a.q, row_at(r) * D + ch, 8), e);
         if (a.d.negative)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = -x[i];
-        parts_of<DT, FMT>(x, minus, q[mt][st]);
+          for (int i = 0; i < 8; ++i) e[i] = -e[i];
+        parts_of<DT, FMT>(e, minus, q[mt][st]);
       }
     f32x4_t o[MT][kTilesV];
     float m[MT], l[MT];
@@ -1138,8 +1140,6 @@ struct SharedAttention {
     // waves whose rows are all padding only decode
     const bool works = tile * kRows + wave * MT * 16 < w.count * a.d.group;
     if (first < last) {
-      Raw x;
-      look_up(x.next, first);
       load(x, first);
       from_here(x.ks);                     // as words, as the loads of the other variant's first tile
       from_here(x.vs);
