@@ -85,6 +85,16 @@ def test_prompts_of_many_tokens():
     check(g, cache, table, 1083, "bf16", "prompts", np.array([700, 1083], np.int32))
 
 
+@pytest.mark.parametrize("dim,heads,T", [(64, 9, 1), (64, 200, 1), (128, 5, 2), (512, 33, 1), (512, 3, 15), (256, 2, 70),
+                                         (64, 3, 129)])
+def test_tiles_that_tokens_and_heads_do_not_fill(dim, heads, T):
+    g = np.random.default_rng(dim + heads)
+    lengths = [5, 0, 31]
+    cache = pools(g, 20, heads, 32, dim, "mxfp4", 16)
+    table = counted(table_of(g, [n + T for n in lengths], 32, 6, 20), lengths, 20)
+    check(g, cache, table, T, "bf16", f"{heads} heads, {T} tokens", np.array([T, T, T - 1], np.int32))
+
+
 def test_nothing_to_append():
     g = np.random.default_rng(3)
     cache = pools(g, 4, 2, 16, 64, "fp8", 32)

@@ -249,6 +249,140 @@ def test_the_same_answer_every_time():
         assert torch.equal(mxq.cache_attention(x, c, t), first)
 
 
+def shifted(cache, name, pages, by):
+    """The scale exponents of these pages raised (no byte is 255, which is NaN)."""
+    x = cache[name][pages].astype(np.int64) + by
+    cache[name][pages] = np.clip(x, 0, 254).astype(np.uint8)
+
+
+@pytest.mark.parametrize("fmt,block", [("fp8", 32), ("fp8", 128), ("mxfp4", 32)])
+@pytest.mark.parametrize("dim,T,heads", [(64, 12, 4), (64, 33, 4), (128, 24, 2), (128, 10, 8), (256, 9, 4)])
+def test_values_that_fp16_does_not_hold(fmt, block, dim, T, heads):
+    """More rows than one tile of 32, whose probabilities are fp16 where the values' scales allow it: values near 2^30,
+    near 2^-60 and 0 (scale bytes of 0 as well), in all pages, in one page of a long context, in the drafted rows alone."""
+    if block > dim:
+        pytest.skip("a block is no more than a row")
+    g = np.random.default_rng(dim + T)
+    cache, table, q = case(g, [700, 33, 0], T, 16, heads, 1, dim, fmt, block, "bf16")
+    mask = tree(g, T)
+    used = table[0][table[0] >= 0]
+    for what, pages, by in (("all large", used, 30), ("all small", used, -60), ("one page large", table[0][0, 20:21], 18),
+                            ("one page small", table[0][0, 3:4], -40), ("drafted", table[0][0, 43:44], 20),
+                            ("zero scales", table[0][0, 7:9], -255)):
+        other = copied(cache)
+        shifted(other, "v_scales", pages, by)
+        check_attention(q, other, table, f"{fmt} {what}", mask=mask)
+    zero = copied(cache)
+    zero["v_codes"][table[0][0, 5]] = 0
+    zero["v_scales"][table[0][0, 5]] = 0
+    check_attention(q, zero, table, f"{fmt} rows of zeros", mask=mask)
+
+
+@pytest.mark.parametrize("fmt,block", [("fp8", 32), ("mxfp4", 32), ("nvfp4", 16)])
+@pytest.mark.parametrize("dim,T,heads", [(64, 20, 2), (64, 40, 4), (128, 12, 4), (128, 40, 4), (256, 10, 4), (512, 24, 4)])
+def test_nan_values_of_many_rows(fmt, block, dim, T, heads):
+    """As above where the rows are more than a wave's: a drafted value that is not finite in some channels reaches those
+    channels of the rows that see it alone; the first sequence's context is long enough to be shared out."""
+    g = np.random.default_rng(dim + T + 1)
+    cache, table, q = case(g, [900, 0, 30], T, 16, heads, 1, dim, fmt, block, "bf16")
+    mask = np.eye(T, dtype=bool)
+    mask[T - 1, [2, 5]] = True
+    mask[7, 2] = True
+    put = lambda a: torch.from_numpy(a).to(dev())  # noqa: E731
+    clean = mxq.cache_attention(q.to(dev()), on_gpu(cache), table_on_gpu(table), mask=put(mask))
+    want = torch.zeros_like(clean, dtype=torch.bool)
+    for b, n in enumerate(table[1]):
+        for token, channel in ((2, dim - 3), (5, 17)):
+            page, row = table[0][b, (n + token) // 16], (n + token) % 16
+            sees = np.flatnonzero(mask[:, token])
+            if fmt == "fp8":
+                cache["v_codes"][page, 0, row, channel] = 0xFF
+                want[b, sees, :, channel] = True
+            else:
+                first = channel // block * block
+                cache["v_scales"][page, 0, row, channel // block] = 0x7F if fmt == "nvfp4" else 0xFF
+                want[b, sees, :, first: first + block] = True
+    out = mxq.cache_attention(q.to(dev()), on_gpu(cache), table_on_gpu(table), mask=put(mask))
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], clean[~want])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,T", [(64, 30), (128, 12), (512, 17)])
+def test_nvfp4_scales_with_mantissas_of_many_rows(dtype, dim, T):
+    g = np.random.default_rng(16)
+    cache, table, q = case(g, [300, 31], T, 16, 4, 1, dim, "nvfp4", 16, dtype)
+    for name in ("k_scales", "v_scales"):
+        x = g.integers(0, 0x40, cache[name].shape)                                # up to 2, of both signs
+        cache[name] = (x | g.integers(0, 2, x.shape) << 7).astype(np.uint8)
+    check_attention(q, cache, table, "mantissas", mask=tree(g, T), dtype=dtype)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 40.0])
+@pytest.mark.parametrize("T", [1, 20])
+def test_probabilities_all_alike_and_of_one_position(scale, T):
+    """Scores so close that every position counts, and so far apart that one does, its score first or last."""
+    g = np.random.default_rng(17)
+    cache, table, q = case(g, [1500, 200], T, 32, 4, 1, 128, "nvfp4", 16, "bf16")
+    check_attention(q, cache, table, "scores", scale=scale)
+
+
+def test_largest_scores_rise_all_the_way():
+    """Each tile's largest score is past the last one's by more than the running maximum lets pass."""
+    g = np.random.default_rng(18)
+    for T in (1, 20):
+        cache, table, q = case(g, [640, 640], T, 32, 4, 1, 64, "fp8", 64, "bf16")
+        q = q.abs()
+        codes, scales = cache["k_codes"], cache["k_scales"]
+        codes &= 0x7F                                                   # positive scores
+        for b in range(2):
+            order = table[0][b] if b == 0 else table[0][b][::-1]
+            for i, page in enumerate(p for p in order if p >= 0):
+                scales[page] = 118 + min(i, 12)
+        check_attention(q, cache, table, f"rising, {T}", scale=1.0)
+
+
+@pytest.mark.parametrize("B,T,heads,dim", [(65, 1, 4, 64), (300, 1, 4, 64), (300, 10, 4, 64), (130, 17, 2, 128), (520, 2, 2, 64)])
+def test_many_sequences_share_the_workgroups(B, T, heads, dim):
+    """More sequences than a workgroup has threads, lengths from none to many steps, some of them padding alone."""
+    g = np.random.default_rng(B + T)
+    lengths = (g.integers(0, 40, B) * g.integers(0, 40, B)).tolist()
+    cache, table, q = case(g, lengths, T, 64, heads, 1, dim, "mxfp4", 32, "bf16")
+    counts = g.integers(-1, T + 1, B).astype(np.int32)
+    counts[g.random(B) < 0.5] = T
+    check_attention(q, cache, table, "sequences", counts=counts)
+
+
+def test_two_calls_at_once():
+    """Two streams, a call of its own on each, over and over: neither sees the other's workspace."""
+    g = np.random.default_rng(19)
+    made = []
+    for fmt, block, T in (("fp8", 32, 1), ("nvfp4", 16, 20)):
+        cache, table, q = case(g, [3000, 500, 90], T, 64, 8, 2, 128, fmt, block, "bf16")
+        made.append((on_gpu(cache), table_on_gpu(table), q.to(dev()), torch.cuda.Stream()))
+    want = [mxq.cache_attention(q, c, t) for c, t, q, _ in made]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, (c, t, q, stream) in enumerate(made):
+            with torch.cuda.stream(stream):
+                got[i].append(mxq.cache_attention(q, c, t))
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
+def test_nothing_to_attend_with():
+    g = np.random.default_rng(20)
+    cache, table, q = case(g, [20], 2, 16, 4, 2, 64, "fp8", 32, "bf16")
+    c = on_gpu(cache)
+    out, lse = mxq.cache_attention(torch.empty(0, 3, 4, 64, device=dev()), c, mxq.page_table(0, 2, c), return_lse=True)
+    assert out.shape == (0, 3, 4, 64) and lse.shape == (0, 3, 4)
+    out, lse = mxq.cache_attention(q.to(dev()), c, table_on_gpu(table), counts=torch.zeros(1, dtype=torch.int32, device=dev()),
+                                   return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
 def test_many_short_sequences():
     g = np.random.default_rng(10)
     lengths = list(g.integers(0, 40, 700))
