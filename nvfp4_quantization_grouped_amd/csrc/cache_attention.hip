@@ -6,10 +6,14 @@ namespace {
 
 // Steps are shared out among as many workgroups as run at a time.
 constexpr int kComputeUnits = 256;
-// From so many problems on each has a workgroup of its own: there are enough of them to keep the card busy.
+// From so many problems on each has a workgroup of its own: there are enough of them to keep the card busy (8 heads of 512
+// sequences of 2048 154 us, 183 shared out; of 256 of 4096 150 and 158; of 128 of 4096 90 and 88).
 constexpr int64_t kManyProblems = 2048;
-// Problems of so many steps at most are not worth sharing.
-constexpr int64_t kFewSteps = 4;
+// Below, problems are shared out if they have more steps than a kernel's `few` (14 of 1 us, or 4 of 3 us: what joining
+// costs) and this many more for each workgroup's worth of problems.  Of 4 sequences' 8 heads 1024 positions take 16 us, 19
+// shared out, 2048 22 and 19; of 32 sequences' 17 and 24, 25 and 29, 3000 35 and 34; of 96 3000 79 and 88; of [4, n, 512] 128
+// positions 29 and 26; 16-token trees over 500 positions of 4 sequences 34 and 24, of 32 35 and 41, over 1000 49 and 43.
+constexpr int64_t kStepsPerShare = 20;
 
 hipError_t kernels(const AttnArgs* a, int dt, int fmt, int dim, int rows, int64_t problems, AttnShape* shape,
                    hipStream_t st) {
@@ -35,12 +39,13 @@ Plan plan_of(const CacheArgs& c, int64_t sequences, int64_t width, int dt, int64
   p.rows = attention_rows(c.head_dim, rows);
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   p.problems = sequences * c.kv_heads * p.row_tiles;
-  AttnShape shape = {128, 0, 1};
+  AttnShape shape = {128, 0, 0, 1};
   (void)kernels(nullptr, dt, c.fmt, c.head_dim, p.rows, 0, &shape, nullptr);
   const int64_t steps = (width * c.page_size + shape.step - 1) / shape.step;
-  const bool split = p.problems < kManyProblems && steps > kFewSteps &&
+  const int workgroups = kComputeUnits * shape.resident;
+  const bool split = p.problems < kManyProblems && steps > shape.few + kStepsPerShare * p.problems / workgroups &&
                      p.problems * (steps + shape.start) < (int64_t(1) << 31);
-  p.workgroups = split ? kComputeUnits * shape.resident : 0;
+  p.workgroups = split ? workgroups : 0;
   return p;
 }
 

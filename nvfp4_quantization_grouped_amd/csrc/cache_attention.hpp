@@ -390,7 +390,7 @@ struct Attention {
   static constexpr int kTilesV = D / 16, kType = DT;
   // waves of a SIMD that the registers are kept to, which is workgroups of a CU
   static constexpr int kWaves = D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
-  static constexpr int kThreads = kAttnThreads, kResident = kWaves, kStart = 4;
+  static constexpr int kThreads = kAttnThreads, kResident = kWaves, kStart = 4, kFew = 14;
   // q's fragments stay in registers up to 32 of them, else in LDS
   static constexpr bool kQInRegs = D * QP * MT <= 256;
   static constexpr int kPad = D + 4;
@@ -884,7 +884,7 @@ struct SharedAttention {
   // waves of a SIMD that the registers are kept to: two where q and the sums leave room for it
   static constexpr int kWaves = MT * (D / 8 * QP + D / 4) <= 160 ? 2 : 1;
   static constexpr int kResident = kWaves * 4 / WAVES;                 // workgroups of a CU
-  static constexpr int kStart = D == 512 ? 6 : 4;
+  static constexpr int kStart = D == 512 ? 6 : 4, kFew = 4;
   // a wave's share of a step: a tile, or of that a part:
   static constexpr int kPartsOfTile = WAVES / kTiles;
   static constexpr int kHalves = kPartsOfTile > 1 ? 1 : 2;             // halves of its positions for the keys
@@ -1433,8 +1433,9 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
 }
 
 // Rows of a problem's tile.  Up to 16 or 32: the four waves take different positions of the same rows, so that a few rows
-// keep a whole workgroup's loads under way.  More: each wave has rows of its own, 32 (16 of the wide heads), and all take
-// the same positions, decoded once; two waves are enough for 64.
+// keep a whole workgroup's loads under way (32 sequences of 8192 with 32 rows 76 us, 89 the other way).  More: each wave has
+// rows of its own, 32 (16 of the wide heads), and all take the same positions, decoded once (64 rows 164 us with the first
+// way, 143 so); two waves are enough for 64 (four, half of them idle, 121 us against 118).
 inline int attention_rows(int dim, int64_t rows) {
   if (rows <= 16) return 16;
   if (rows <= 32 && dim <= 128) return 32;
@@ -1449,7 +1450,7 @@ struct KernelOf {
 };
 // What the launches have to know of a kernel.
 struct AttnShape {
-  int step, start, resident;     // positions of a step; units before a problem's steps; workgroups of a CU
+  int step, start, few, resident;   // positions of a step; units before a problem's steps; kFew; workgroups of a CU
 };
 
 template <class A>
@@ -1470,7 +1471,7 @@ hipError_t attention_dim(const AttnArgs* a, int dim, int rows, int64_t problems,
   if (dim == D && rows == ROWS) {                             \
     using A = typename KernelOf<DT, FMT, D, ROWS>::Type;      \
     if (a) return launch_attention_of<A>(*a, problems, st);   \
-    *shape = {A::kStep, A::kStart, A::kResident};             \
+    *shape = {A::kStep, A::kStart, A::kFew, A::kResident};    \
     return hipSuccess;                                        \
   }
   CASE(64, 16)

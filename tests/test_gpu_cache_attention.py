@@ -353,6 +353,17 @@ def test_many_sequences_share_the_workgroups(B, T, heads, dim):
     check_attention(q, cache, table, "sequences", counts=counts)
 
 
+def test_many_long_sequences_of_one_token():
+    """The same for a kernel whose waves share the rows, and contexts long enough for it."""
+    g = np.random.default_rng(21)
+    lengths = (g.integers(0, 61, 300) * g.integers(0, 101, 300)).tolist()
+    lengths[0], lengths[299] = 6000, 0
+    cache, table, q = case(g, lengths, 1, 64, 4, 1, 64, "mxfp4", 32, "bf16")
+    counts = g.integers(0, 2, 300).astype(np.int32)
+    counts[:100] = 1
+    check_attention(q, cache, table, "sequences", counts=counts)
+
+
 def test_two_calls_at_once():
     """Two streams, a call of its own on each, over and over: neither sees the other's workspace."""
     g = np.random.default_rng(19)
