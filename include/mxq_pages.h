@@ -87,14 +87,15 @@ int cache_append(const mxq_cache* cache, const int32_t* table, int64_t sequences
  * tokens, heads] (NULL: not wanted).  A token with nothing to attend to, and
  * tokens from counts on (int32 [sequences], NULL = tokens), get out = 0 and
  * lse = -inf.  Positions a token does not attend to may hold anything, NaN
- * too.  Keys, values and q enter the products as they are (q and the
- * probabilities in as many bf16 parts as their type has bits), sums are fp32.
+ * too.  Keys, values and q enter the products as they are (q in as many bf16
+ * parts as its type takes, or fp16), probabilities in enough bf16 or fp16 parts
+ * that what is lost stays below the output's rounding; sums are fp32.
  * workspace: cache_attention_workspace(the same sizes) bytes, 16-byte aligned;
  * its contents before and after the call mean nothing, and calls that may run
  * at the same time need one each.
  * Errors: as cache_append, and MXQ_ERR_SHAPE (heads not a multiple of
  * kv_heads or more than 2^14, tokens > 1024, more than 2^31 - 1 rows of q, a
- * workspace that is too small).  cache_attention_workspace returns
+ * scale of 2^127 or more by size or NaN, a workspace that is too small).  cache_attention_workspace returns
  * MXQ_ERR_SHAPE, MXQ_ERR_DTYPE, MXQ_ERR_FORMAT or MXQ_ERR_BLOCK for sizes that
  * cache_attention refuses; it reads no pool, whose pointers may be NULL.
  */

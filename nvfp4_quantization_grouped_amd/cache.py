@@ -8,9 +8,9 @@ device, outputs and workspaces are allocated with PyTorch's caching allocator.
 There is no CPU path, and no gradient: a tensor that wants one is refused.
 
 Nothing is read back to the host, so everything can be captured into a graph.
-The pools are written in place; tables, lengths and counts come back as new
-tensors, which a loop around a captured graph copies into the ones it started
-from.
+The pools are written in place; what a call changes of a table comes back as
+new tensors (the rest are the ones that were given), which a loop around a
+captured graph copies into the ones it started from.
 
 A step of a serving loop with drafted tokens::
 
@@ -218,7 +218,7 @@ def cache_attention(q, cache, table, *, mask=None, counts=None, scale=None, retu
     ``mask[i, j]`` (bool [tokens, tokens], or [sequences, tokens, tokens]: a tree
     of drafted tokens, each row true at the token itself and its ancestors), or
     with j <= i without a mask.  ``counts`` (int32 [sequences]): tokens from
-    there on are padding.  ``scale``: default 1 / sqrt(head_dim).
+    there on are padding.  ``scale``: default 1 / sqrt(head_dim); finite.
 
     Tokens with nothing to attend to get zeros.  With ``return_lse`` also the log
     of the softmax's sum, float32 [sequences, tokens, heads] (-inf there)."""

@@ -114,7 +114,7 @@ int cache_attention(const mxq_cache* cache, const int32_t* table, int64_t sequen
                     int64_t workspace_bytes, void* stream) {
   const int64_t need = cache_attention_workspace(cache, sequences, width, t, tokens, heads);
   if (need < 0) return (int)need;
-  if (workspace_bytes < need) return MXQ_ERR_SHAPE;
+  if (workspace_bytes < need || !(scale < 0x1p127 && scale > -0x1p127)) return MXQ_ERR_SHAPE;
   const int64_t rows = sequences * tokens * heads;
   if (rows == 0) return MXQ_OK;
   const int st = pools_ok(cache);

@@ -92,6 +92,7 @@ def test_attention(L):
     assert call(tokens=-1) == call(tokens=1025) == call(heads=30) == call(heads=0) == call(heads=1 << 15) == SHAPE
     assert call(heads=1 << 14, tokens=1024, sequences=1 << 10) == SHAPE
     assert call(t=-1) == DTYPE
+    assert call(scale=float("nan")) == call(scale=float("inf")) == call(scale=-2.0 ** 127) == SHAPE
     assert call(table=None) == call(lengths=None) == call(q=None) == call(out=None) == NULL
     assert call(q=A[2] + 8) == call(out=A[5] + 8) == call(lse=A[6] + 2) == call(counts=A[4] + 2) == ALIGN
     assert call(out=A[2] + 64) == call(lse=A[5] + 64) == call(out=A[3]) == call(lse=A[8]) == call(out=A[11]) == ALIAS
