@@ -21,13 +21,15 @@
 //
 // Roundings.  Codes times scales have at most 6 significant bits and are exact
 // in bf16.  q of fp16 / fp32 enters as 2 / 3 bf16 parts (exact but for what
-// lies 2^-24 below), or fp16 as it is where the keys are exact in fp16 too.  Probabilities are a choice: one bf16 part, up to 2^-8 of
-// each, would make the error of bf16 outputs 1.4 times what rounding them costs;
-// two parts (three for fp32 outputs) leave nothing to see, at as many products.
+// lies 2^-24 below), fp16 as it is where the keys are exact in fp16 too (64
+// contexts of 16384, [1, 64 / 1, 512], 237 us against 270).  Probabilities are a
+// choice: one bf16 part, up to 2^-8 of each, would make the error of bf16 outputs
+// 1.4 times what rounding them costs; two parts (three for fp32 outputs) leave
+// nothing to see, at as many products.
 // For bf16 outputs one fp16 part does (2^-11; the error is 1.01 times the
 // rounding's) where the values fit fp16 exactly, which the scales tell: always
-// for nvfp4, else for values between 2^-15 or so and 2^15.  A workgroup that
-// meets other scales starts its piece again with two bf16 parts.
+// for nvfp4, else (and where there are many rows) for scales of 2^-23 to 2^13 or
+// so.  A workgroup that meets others starts its piece again with two bf16 parts.
 //
 // What bounds it.  One token a sequence: memory (64 contexts of up to 16384, 8
 // heads of 8 queries, mxfp4: 638 MB in 138 us, 4.6 TB/s).  Trees: the products
@@ -176,13 +178,12 @@ __device__ __forceinline__ f32x4_t mfma_value(u32x4_t a, u32x4_t b, f32x4_t c) {
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
-// Whether eight scale bytes keep every code of theirs exact in fp16: 448 or 6 times the scale within 65504, 2^-9 or 0.5
+// Whether E8M0 scale bytes keep every code of theirs exact in fp16: 448 or 6 times the scale within 65504, 2^-9 or 0.5
 // times it no less than 2^-24.
 template <int FMT>
 __device__ __forceinline__ bool fits_half(uint32_t least, uint32_t most) {
   if constexpr (FMT == FMT_FP8) return least >= 112 && most <= 134;
-  else if constexpr (FMT == FMT_MXFP4) return least >= 104 && most <= 140;
-  else return true;
+  else return least >= 104 && most <= 140;
 }
 template <bool HALF>
 __device__ __forceinline__ f32x4_t mfma_key(bf16x8_t a, bf16x8_t b, f32x4_t c) {
@@ -393,7 +394,8 @@ __device__ __forceinline__ void softmax_step(const f32x4_t (&s)[MT][2], float sc
 template <int DT, int FMT, int D, int MT, bool HALF>
 struct Attention {
   using S = Shape<FMT, D>;
-  using Other = std::conditional_t<HALF && !kHalfOnly<DT, FMT>, Attention<DT, FMT, D, MT, false>, void>;
+  static_assert(!HALF || kHalfOnly<DT, FMT>, "a piece is not started again here");
+  using Other = void;
   static constexpr int QP = kQParts<DT, FMT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
   static constexpr int kTilesV = D / 16, kType = DT;
   // waves of a SIMD that the registers are kept to, which is workgroups of a CU
@@ -413,7 +415,6 @@ struct Attention {
     __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
     __attribute__((aligned(16))) uint8_t nan[kRows * D];   // outputs that a value that is not finite reached
     float m[4][kRows], l[4][kRows];
-    int again;                                             // a scale was met that fp16 does not hold
     int first[kThreads];                                   // prefix sums of the schedule
     int sums[4];
   };
@@ -715,10 +716,8 @@ struct Attention {
   }
 
   // Steps [first, last) of the problem, this wave's tile of each; `whole`: they are all, else the sums go to `slot`.
-  // False, with nothing written, where fp16 does not hold the values.
   __device__ __forceinline__ bool piece(int first, int last, bool whole, float* slot) {
     place();
-    if (wave == 0 && lane == 0) sm.again = 0;
     for (int i = wave * 64 + lane; i < kRows * D / 16; i += kAttnThreads)
       *reinterpret_cast<u32x4_t*>(sm.nan + i * 16) = u32x4_t{0u, 0u, 0u, 0u};
     Q q;
@@ -763,22 +762,6 @@ struct Attention {
         const int beyond = ahead + 4 < end ? ahead + 4 : ahead;
         const Pages after = pages_of(beyond);
         if (!(now.there[0] && now.there[1] && (t + 1) * kTile <= w.known)) mask(now, t, s, v);
-        if constexpr (HALF && !kHalfOnly<DT, FMT>) {
-          uint32_t least = 255, most = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int u = 0; u < S::VU; ++u)
-#pragma unroll
-              for (int i = 0; i < S::VS; ++i) {
-                least = min(least, v.s[j][u][i]);
-                most = max(most, v.s[j][u][i]);
-              }
-          if (__ballot(!fits_half<FMT>(least, most)) != 0) {
-            if (lane == 0) sm.again = 1;
-            break;
-          }
-        }
         u32x4_t p[MT][PP];
         softmax_step<HALF, MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
         from_here(v.w);
@@ -796,14 +779,14 @@ struct Attention {
         ahead = beyond;
       }
     }
-    return join(o, m, l, whole, slot);
+    join(o, m, l, whole, slot);
+    return true;
   }
 
   // The four waves' sums joined: written as outputs, or as a part of them.
-  __device__ __forceinline__ bool join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
+  __device__ __forceinline__ void join(f32x4_t (&o)[MT][kTilesV], float (&m)[MT], float (&l)[MT], bool whole, float* slot) {
     place();
     __syncthreads();      // q's fragments, and the last piece's sums, have been read
-    if (HALF && __builtin_amdgcn_readfirstlane(sm.again)) return false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       l[mt] = row_sum(l[mt]);
@@ -873,7 +856,6 @@ struct Attention {
         write_row<DT, 8>(a, row_at(at), D, ch, x, top, at < live ? sum : 0.0f);
       }
     }
-    return true;
   }
 };
 

@@ -64,6 +64,20 @@ def test_free(B, W, pages, size):
     assert int(got.pages.max()) == -1 and not got.lengths.any() and not got.refs.any()
 
 
+@pytest.mark.parametrize("B,W,pages", [(600, 9, 2000), (455, 9, 3000), (456, 9, 3000), (40, 100, 70000)])
+def test_free_and_fork_of_many_entries(B, W, pages):
+    """Around the number of entries from which two launches take the place of one."""
+    g = np.random.default_rng(B)
+    gpu = mxq.paged_cache(pages, 32, 1, 64, "fp8", 64, shared=True)
+    table = random_table(g, B, W, 32, pages)
+    keep = g.integers(-3, W * 32 + 9, B)
+    got = mxq.cache_free(gpu, table_on_gpu(table), i32(keep))
+    assert_same_table(got, paged.fork(table, range(B), 32, True, keep), "free")
+    parents = g.integers(0, B, B)
+    got = mxq.cache_fork(table_on_gpu(table), i32(parents), release=True)
+    assert_same_table(got, paged.fork(table, parents, 16, True), "fork")
+
+
 def test_fork_of_entries_that_name_no_page():
     rows = np.array([[2, 5, -9], [1 << 30, 0, 2]], np.int32)
     table = rows, np.array([-4, 2 ** 31 - 1], np.int32), np.array([1, 0, 2, 0, 0], np.int32)
