@@ -104,11 +104,10 @@ def _cache_args(cache, name):
         raise ValueError(f"{name}: format must be 'fp8', 'mxfp4' or 'nvfp4'")
     if (vc is None) != (vs is None):
         raise ValueError(f"{name}: v_codes and v_scales belong together")
-    device = kc.device
+    device, index = kc.device, kc.get_device()
     for pool in (kc, ks) if vc is None else (kc, ks, vc, vs):
-        if not pool.is_cuda:
-            raise ValueError("libmxq ops take GPU tensors only (there is no CPU implementation)")
-        if pool.device != device:
+        if index < 0 or pool.get_device() != index:
+            _need_cuda(kc, pool)
             raise ValueError("all tensors must be on the same device")
         if pool.dtype is not torch.uint8 or pool.dim() != 4:
             raise TypeError(f"{name}: pools must be uint8 [pages, kv_heads, page_size, width]")
@@ -131,7 +130,8 @@ def _table_args(table, pages, device, name):
     if (rows.dtype is not torch.int32 or lengths.dtype is not torch.int32 or refs.dtype is not torch.int32
             or rows.dim() != 2 or lengths.dim() != 1 or refs.dim() != 1):
         raise TypeError(f"{name}: the table must be int32 pages [sequences, width], lengths [sequences] and refs [pages]")
-    if rows.device != device or lengths.device != device or refs.device != device:
+    index = device.index
+    if rows.get_device() != index or lengths.get_device() != index or refs.get_device() != index:
         raise ValueError("all tensors must be on the same device")
     if lengths.shape[0] != rows.shape[0] or (pages is not None and refs.shape[0] != pages):
         raise ValueError(f"{name}: the table's lengths must be [sequences] and refs [pages of the cache]")
