@@ -297,7 +297,7 @@ __device__ __forceinline__ int share_of(int w, int total, int g) { return (int)(
 // The workgroup that takes unit u.
 __device__ __forceinline__ int owner_of(int u, int total, int g) { return (int)((((int64_t)u + 1) * g - 1) / total); }
 
-// A part of a problem that several workgroups share: sums [rows][D], then m and l [rows].
+// A part of a problem that several workgroups share: sums (rows * D, in A's order), then m and l [rows].
 template <class A>
 constexpr int64_t kSlotFloats = (int64_t)A::kRows * (A::kDim + 2);
 
@@ -398,6 +398,7 @@ struct Attention {
   using Other = void;
   static constexpr int QP = kQParts<DT, FMT>, PP = HALF ? 1 : kPParts<DT>, kDim = D, kRows = 16 * MT, kStep = 4 * kTile;
   static constexpr int kTilesV = D / 16, kType = DT;
+  static constexpr bool kFragments = false;                // parts are rows
   // waves of a SIMD that the registers are kept to, which is workgroups of a CU
   static constexpr int kWaves = D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
   static constexpr int kThreads = kAttnThreads, kResident = kWaves, kStart = 4, kFew = 14;
@@ -882,6 +883,9 @@ struct SharedAttention {
   static constexpr int VC = D / 16 < 8 ? D / 16 : 8;                   // channels of a lane for the values, of all positions
   static constexpr int VB = S::kFp8 ? VC : VC / 2, VW = VB < 4 ? 1 : VB / 4;
   static constexpr int kWords = D / 32;                                // of a row's marks
+  // Parts are kept as the registers hold them, a store of 1 KB at a time (as rows it is 64 pieces of 16 bytes: [4, 8192, 512]
+  // 42 us against 40, 16-token trees 100 against 96).  Four channels of a lane are too few for the joining lanes' eight.
+  static constexpr bool kFragments = VC == 8;
 
   struct Shared {
     __attribute__((aligned(16))) u32x4_t key[kTiles][2][S::kSteps][64];
@@ -1213,22 +1217,35 @@ struct SharedAttention {
       const float sum = row_sum(l[mt]);
       const int r = (wave * MT + mt) * 16 + col, at = tile * kRows + r;
 #pragma unroll
-      for (int u = 0; u < kTilesV / VC; ++u)
+      for (int u = 0; u < kTilesV / VC; ++u) {
+        const int ch = u * 16 * VC + quarter * 4 * VC;                   // four times VC channels
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int ch = u * 16 * VC + (quarter * 4 + i) * VC;
-          const uint32_t bits = sm.nan[r][ch / 32] >> (ch % 32);
+          const uint32_t bits = sm.nan[r][(ch + i * VC) / 32] >> ((ch + i * VC) % 32);
+#pragma unroll
+          for (int e = 0; e < VC; ++e) o[mt][u * VC + e][i] = bits >> e & 1 ? __builtin_nanf("") : o[mt][u * VC + e][i];
+        }
+        if (!whole && kFragments) {
+#pragma unroll
+          for (int e = 0; e < VC; ++e)
+            *reinterpret_cast<f32x4_t*>(slot + (((wave * MT + mt) * kTilesV + u * VC + e) * 64 + lane) * 4) =
+                o[mt][u * VC + e];
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           float x[VC];
 #pragma unroll
-          for (int e = 0; e < VC; ++e) x[e] = bits >> e & 1 ? __builtin_nanf("") : o[mt][u * VC + e][i];
+          for (int e = 0; e < VC; ++e) x[e] = o[mt][u * VC + e][i];
           if (!whole) {
 #pragma unroll
             for (int e = 0; e < VC; e += 4)
-              *reinterpret_cast<f32x4_t*>(slot + r * D + ch + e) = f32x4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
+              *reinterpret_cast<f32x4_t*>(slot + r * D + ch + i * VC + e) = f32x4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
           } else if (at < rows) {
-            write_row<DT, VC>(a, row_at(at), D, ch, x, m[mt], at < live ? sum : 0.0f);
+            write_row<DT, VC>(a, row_at(at), D, ch + i * VC, x, m[mt], at < live ? sum : 0.0f);
           }
         }
+      }
       if (!whole && quarter == 0) {
         slot[kRows * D + r] = m[mt];
         slot[kRows * D + kRows + r] = sum;
@@ -1375,7 +1392,15 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
     w1 = owner_of(first + w.steps - 1, total, g);
     if (w0 == w1) return;
   }
-  const int r = blockIdx.y * (512 / D) + lane / (D / 8), ch = lane % (D / 8) * 8, at = tile * A::kRows + r;
+  int r = blockIdx.y * (512 / D) + lane / (D / 8), ch = lane % (D / 8) * 8, from = r * D + ch;
+  if constexpr (A::kFragments) {
+    // the same 64 groups of 16 rows and 32 channels (a quarter's), where SharedAttention::finish puts them
+    const int piece = blockIdx.y / (D / 32), u = blockIdx.y % (D / 32) / 4, quarter = blockIdx.y % 4;
+    r = piece * 16 + lane / 4;
+    ch = u * 128 + (quarter * 4 + lane % 4) * 8;
+    from = ((piece * (D / 16) + u * 8) * 64 + quarter * 16) * 4 + lane;
+  }
+  const int at = tile * A::kRows + r;
   const bool wanted = at < rows;
   float x[8] = {}, top = -__builtin_inff(), sum = 0.0f;
   if (wanted && at < live) {
@@ -1386,8 +1411,17 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
     for (int s = w0 + wave; s <= w1; s += 4) {
       const float* slot = slot_of(s);
       const float m = slot[A::kRows * D + r], l = slot[A::kRows * D + A::kRows + r];
-      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(slot + r * D + ch);
-      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(slot + r * D + ch + 4);
+      f32x4_t lo, hi;
+      if constexpr (A::kFragments) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[e] = slot[from + e * 256];
+          hi[e] = slot[from + e * 256 + 1024];
+        }
+      } else {
+        lo = *reinterpret_cast<const f32x4_t*>(slot + from);
+        hi = *reinterpret_cast<const f32x4_t*>(slot + from + 4);
+      }
       // nothing met, or NaN alone: l is 0 or NaN
       const float keep = m == -__builtin_inff() ? l : __builtin_amdgcn_exp2f(m - top);
       sum += m == -__builtin_inff() ? l : l * keep;
