@@ -34,10 +34,10 @@
 // What bounds it.  One token a sequence: memory (64 contexts of up to 16384, 8
 // heads of 8 queries, mxfp4: 638 MB in 138 us, 4.6 TB/s).  Trees: the products
 // and what feeds them (64 tokens, 8 contexts of up to 16384, fp8: 167 GFLOP in
-// 258 us, 650 TFLOP/s; without its products 137 us, without its loads 275 of
-// 325 then).  Short calls: beginning and ending a piece, 12 to 18 us of waits
-// that follow one another (lengths and shares 2.4, queries 4.5, first rows 2.3,
-// first products 2.5, sums written 2 to 9 us).
+// 252 us, 660 TFLOP/s; when it took 325, 137 without its products and 275
+// without its loads).  Short calls: beginning and ending a piece, 12 to 15 us of
+// waits that follow one another (lengths and shares 2.4, queries 4.5, first rows
+// 2.3, first products 2.5, sums written 2 to 4 us).
 #pragma once
 
 #include <type_traits>
