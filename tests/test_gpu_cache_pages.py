@@ -230,6 +230,41 @@ def test_compact_of_many_pages_and_odd_entries():
     assert np.array_equal(gpu.k_codes.cpu().numpy(), stub["k_codes"])
 
 
+def test_offsets_past_32_bits():
+    """Rows copied, appended and moved in the last pages of a pool of 4.8 GB, all others of which are held."""
+    pages, size, dim = 9300, 256, 512
+    gpu = mxq.paged_cache(pages, size, 4, dim, "fp8", 128, shared=True)
+    assert gpu.k_codes.numel() > 1 << 32
+    g = np.random.default_rng(8)
+    cache = pools(g, 6, 4, size, dim, "fp8", 128, True)
+    far = np.array([8200, 8300, 8400, 9297, 9298, 9299])
+    at = torch.from_numpy(far).to(dev())
+    gpu.k_codes[at] = torch.from_numpy(cache["k_codes"]).to(dev())
+    gpu.k_scales[at] = torch.from_numpy(cache["k_scales"]).to(dev())
+
+    def placed(table):
+        refs = np.ones(pages, np.int32)
+        refs[far] = table[2]
+        return np.where(table[0] >= 0, far[np.maximum(table[0], 0)], -1).astype(np.int32), table[1], refs
+
+    def same(what):
+        assert_same_table(on_card, placed(table), what)
+        for name in ("k_codes", "k_scales"):
+            assert np.array_equal(getattr(gpu, name)[at].cpu().numpy(), cache[name]), (what, name)
+    table = counted(np.array([[5, -1], [5, -1], [4, -1]], np.int32), [200, 200, 250], 6)
+    on_card, lack = mxq.cache_reserve(gpu, table_on_gpu(placed(table)), 9)
+    table, want_lack = paged.reserve(cache, table, [9] * 3)
+    assert lack.tolist() == want_lack.tolist() == [0, 0, 0]
+    same("reserve")
+    k = torch.from_numpy(g.standard_normal((3, 9, 4, dim)).astype(np.float32))
+    mxq.cache_append(gpu, on_card, k.to(dev()))
+    paged.append(cache, table, k.double().numpy())
+    same("append")
+    accepted = np.array([[1, 3, 8], [0, 1, -1], [2, 6, 7]], np.int32)
+    on_card, table = mxq.cache_accept(gpu, on_card, i32(accepted)), paged.accept(cache, table, accepted)
+    same("accept")
+
+
 def test_refusals():
     gpu = mxq.paged_cache(6, 16, 2, 64, "fp8", 32)
     table = mxq.page_table(3, 2, gpu)
