@@ -129,17 +129,17 @@ int cache_fork(const int32_t* table, int64_t sequences, int64_t width, const int
 /*
  * cache_reserve -- pages for the next tokens of every sequence (tokens, or
  * tokens_each int32 [sequences] where that is not NULL; below 0 counts as 0),
- * so that cache_append can write positions lengths .. lengths + tokens - 1:
- *   an entry of these positions without a page gets a free one;
- *   the page of position lengths, if rows of it are filled (lengths %
- *   page_size > 0) and other entries name it too, is copied (its filled rows)
- *   into a free page, which takes its place in this sequence's row.  Of the
- *   sequences that ask for the same page in one call the last keeps it, if no
- *   other entry is left that names it.
- * Free pages are taken in rising order, sequence by sequence: first the copy,
- * then the missing entries in rising order.  short_out int32 [sequences] says
- * how many pages a sequence lacks in the end: the pool ran out, its row of the
- * table is too short, or a page could not be made its own.
+ * so that cache_append can write positions lengths .. lengths + tokens - 1.
+ * Each entry of these positions that has no page, or a page that other entries
+ * name too (refs > 1), gets a free one.  Of a page that others name, the rows
+ * below lengths (the first entry's, where lengths % page_size > 0) are copied;
+ * rows behind them are not.  If all entries that name a page ask for it in one
+ * call, the last of them keeps it.
+ * Free pages are taken in rising order, sequence by sequence, entry by entry.
+ * short_out int32 [sequences] says how many pages a sequence lacks in the end:
+ * the pool ran out, its row of the table is too short, or a page could not be
+ * made its own.  Where it is 0, every entry of the positions names a page with
+ * refs_out 1.
  * Outputs: table_out, refs_out like table and refs; copied rows in the pools.
  * workspace: cache_reserve_workspace(sequences, width, pages) bytes, 4-byte
  * aligned, as for cache_attention.

@@ -270,8 +270,8 @@ def cache_fork(table, parents, *, release=False):
     the result shares all pages of sequence ``parents[c]`` (int32 [children];
     one may have several children, or none).  The counts include both tables'
     entries, or with ``release`` only the new one's.  No row is copied:
-    ``cache_reserve`` gives a sequence its own copy of a shared page that it is
-    about to write to."""
+    ``cache_reserve`` gives a sequence pages of its own in place of shared ones
+    that it is about to write to, those reserved ahead among them."""
     _need_cuda(table.pages, parents)
     device = table.pages.device
     args = _table_args(table, None, device, "cache_fork")
@@ -294,13 +294,14 @@ def cache_free(cache, table, keep=None):
 
 
 def cache_reserve(cache, table, tokens):
-    """Pages for the next ``tokens`` positions of every sequence (a number, or
-    int32 [sequences]): free ones for entries that have none, in rising order,
-    and a copy of the partly filled last page where other sequences share it.
+    """Pages of its own for the next ``tokens`` positions of every sequence (a
+    number, or int32 [sequences]): free ones, in rising order, for entries that
+    have none or one that other entries name too (its last holder keeps it).
+    The cached rows of a partly filled last page come along.
 
     Returns (table, short): short int32 [sequences] is the number of pages a
-    sequence still lacks (0: all there); ``cache_append`` leaves out the rows
-    that they would hold."""
+    sequence still lacks (0: all there, and ``cache_append`` writes every row);
+    ``cache_append`` leaves out the rows that they would hold."""
     args, device = _cache_args(cache, "cache_reserve")
     rows, lengths, refs = _table_args(table, args.pages, device, "cache_reserve")
     each = _each(tokens, rows.shape[0], device, "cache_reserve", "tokens") if isinstance(tokens, torch.Tensor) else None

@@ -7,9 +7,10 @@
 // loads, not bytes: each is one or two launches.  Whatever depends on an order
 // (which sequence gets which free page) is decided by one workgroup with prefix
 // sums; counts are integer atomics, whose sum does not depend on their order.
-// Measured: fork 3 us, reserve 7 to 11 (five loads in a row, then the scans over
-// the sequences and the pages) and 3 to 6 for the copies, accept 3.6, the plan
-// of a compaction 6; its copies 13 us for 55 MB, 4.2 TB/s.
+// Measured: fork 3 us, the plan of a reserve 9 to 12 (four loads in a row, three
+// more round trips where pages are shared, then the scans over the sequences and
+// the pages) and its copies 4 to 9, accept 3.6, the plan of a compaction 6; its
+// copies 13 us for 55 MB, 4.2 TB/s.
 #include "cache_device.hpp"
 
 namespace mxq {
@@ -162,43 +163,51 @@ struct ReserveDims {
   int64_t pages;
   int sequences, width, page_shift, tokens;
 };
-// int32 arrays of the workspace: [0] pages granted, then per sequence its first rank among the wanted pages, whether it
-// wants a copy, and what it lacks that no free page mends; then the free pages in rising order.
+// int32 arrays of the workspace: [0] pages granted, then per sequence its first rank among the wanted pages; per page (of
+// those that shared entries ask for) how many ask, and the last that does; then the free pages in rising order.
 struct ReserveSpace {
-  int32_t *granted, *rank, *copy, *lack, *free;
+  int32_t *granted, *rank, *asks, *last, *free;
 };
-__host__ __device__ inline ReserveSpace reserve_space(int32_t* w, int sequences) {
-  return {w, w + 1, w + 1 + sequences, w + 1 + 2 * (int64_t)sequences, w + 1 + 3 * (int64_t)sequences};
+__host__ __device__ inline ReserveSpace reserve_space(int32_t* w, int sequences, int64_t pages) {
+  return {w, w + 1, w + 1 + sequences, w + 1 + sequences + pages, w + 1 + sequences + 2 * pages};
 }
 
 // What a sequence asks for.
 struct Need {
-  int length, slot, last, end;   // slots slot .. end - 1 must have pages; `last`: the partly filled page, or -1
+  int length, slot, end;         // slots slot .. end - 1 must have pages of the sequence's own
   int beyond;                    // pages for which the table has no room
 };
-__device__ __forceinline__ Need need_of(const int32_t* __restrict__ row, int length, int tokens, const ReserveDims& d) {
+__device__ __forceinline__ Need need_of(int length, int tokens, const ReserveDims& d) {
   Need n;
   n.length = cached_positions(length, d.width, 1 << d.page_shift);
   n.slot = n.length >> d.page_shift;
   const int64_t end = ((int64_t)n.length + max(tokens, 0) + (1 << d.page_shift) - 1) >> d.page_shift;
   n.beyond = (int)max(end - d.width, (int64_t)0);
   n.end = tokens > 0 ? (int)min(end, (int64_t)d.width) : 0;
-  n.last = -1;
-  if (n.slot < n.end && (n.length & ((1 << d.page_shift) - 1))) {
-    const int page = row[n.slot];
-    if (valid_page(page, d.pages)) n.last = page;
-  }
   return n;
 }
 
+// Memory that the planning workgroup's waves share among themselves, in order across its barriers.  (Fences for the whole
+// device write back the L2 as well: a fork and a reserve of 64 beams, alone, 62 us with them and 51 without.)
+__device__ __forceinline__ int shared_load(const int32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+__device__ __forceinline__ void shared_store(int32_t* p, int v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
 // Workgroup 0 plans; the others copy the table and the counts, which the second launch changes.
+//
+// An entry that asks for a page which others name too (refs > 1) gets another one, unless it is the last to ask and all
+// that name the page ask.  So each page needs two numbers, how many entries ask and which is the last: a count and a
+// maximum, whose order does not matter, where comparing the entries would take the square of their number.
 __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve_plan(const int32_t* __restrict__ table,
                                                                      const int32_t* __restrict__ lengths,
                                                                      const int32_t* __restrict__ refs,
                                                                      const int32_t* __restrict__ tokens_each,
                                                                      int32_t* __restrict__ table_out,
-                                                                     int32_t* __restrict__ refs_out,
-                                                                     int32_t* __restrict__ work, ReserveDims d) {
+                                                                     int32_t* __restrict__ refs_out, int32_t* work,
+                                                                     ReserveDims d) {
   const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
     const int64_t entries = (int64_t)d.sequences * d.width, step = (int64_t)(gridDim.x - 1) * kPlanThreads;
@@ -210,55 +219,78 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve_plan(const int32
     }
     return;
   }
-  const ReserveSpace w = reserve_space(work, d.sequences);
-  __shared__ __attribute__((aligned(16))) int asked[kMaxReserveSequences];   // the partly filled page a sequence will write to, or -1
-  __shared__ int wants[kMaxReserveSequences];     // free pages it wants
+  const ReserveSpace w = reserve_space(work, d.sequences, d.pages);
+  __shared__ int wants[kMaxReserveSequences];     // free pages a sequence wants, then its first rank among all
   __shared__ int sums[kPlanWaves];
   // as many lanes to a sequence, side by side, as let all sequences go at once
   const int shift = min(max(31 - __builtin_clz(kPlanThreads / max(d.sequences, 1) | 1), 0), 6), lanes = 1 << shift;
   const int lane = tid & (lanes - 1);
   const uint64_t group = (lanes == 64 ? ~0ull : (1ull << lanes) - 1) << (tid & 63 & ~(lanes - 1));
-  for (int b = tid >> shift; b < d.sequences; b += kPlanThreads >> shift) {
-    const int32_t* row = table + (int64_t)b * d.width;
-    const Need n = need_of(row, lengths[b], tokens_each ? tokens_each[b] : d.tokens, d);
-    int missing = 0;
-    for (int s0 = n.slot; s0 < n.end; s0 += lanes) {
-      const int s = s0 + lane;
-      missing += __popcll(__ballot(s < n.end && !valid_page(row[min(s, d.width - 1)], d.pages)) & group);
-    }
-    if (lane == 0) {
-      asked[b] = n.last;
-      w.lack[b] = n.beyond;
-      wants[b] = missing;
-    }
-  }
-  __syncthreads();
-  // copies: of the sequences that ask for a page, all but the one that is left with it
-  for (int b = tid; b < d.sequences; b += kPlanThreads) {
-    const int page = asked[b];
-    int copy = 0;
-    if (page >= 0) {
-      const int held = refs[page];
-      if (held > 1) {
-        int before = 0, o = 0;
-        for (; o + 4 <= b; o += 4) {
-          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(asked + o);
-          before += ((int)x.x == page) + ((int)x.y == page) + ((int)x.z == page) + ((int)x.w == page);
-        }
-        for (; o < b; ++o) before += asked[o] == page;
-        copy = before < held - 1;
+  const uint64_t below_me = (1ull << (tid & 63)) - 1;
+  // f(sequence, entry of the table, whether it is asked for, its page or -1, refs of the page or 0), the lanes of a
+  // sequence at its entries in turn; begin(sequence) and end(sequence) around them
+  auto walk = [&](auto begin, auto f, auto end) {
+    for (int b = tid >> shift; b < d.sequences; b += kPlanThreads >> shift) {
+      const Need n = need_of(lengths[b], tokens_each ? tokens_each[b] : d.tokens, d);
+      begin(b);
+      for (int s0 = n.slot; s0 < n.end; s0 += lanes) {
+        const int s = s0 + lane;
+        const bool in = s < n.end;
+        int page = table[(int64_t)b * d.width + min(s, d.width - 1)];
+        page = in && valid_page(page, d.pages) ? page : -1;
+        f(b * d.width + s, in, page, page >= 0 ? refs[page] : 0);
       }
+      end(b);
     }
-    w.copy[b] = copy;
-    wants[b] += copy;
+  };
+  bool found_shared = false;
+  int missing = 0;
+  walk([&](int) { missing = 0; },
+       [&](int, bool in, int page, int held) {
+         missing += __popcll(__ballot(in && page < 0) & group);
+         if (held > 1) {
+           found_shared = true;
+           shared_store(w.asks + page, 0);
+           shared_store(w.last + page, -1);
+         }
+       },
+       [&](int b) {
+         if (lane == 0) wants[b] = missing;
+       });
+  const bool any_shared = __syncthreads_or(found_shared) != 0;
+  if (any_shared) {
+    walk([](int) {},
+         [&](int entry, bool, int page, int held) {
+           if (held > 1) {
+             __hip_atomic_fetch_add(w.asks + page, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+             __hip_atomic_fetch_max(w.last + page, entry, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+           }
+         },
+         [](int) {});
+    __syncthreads();
+    int replaced = 0;
+    walk([&](int) { replaced = 0; },
+         [&](int entry, bool, int page, int held) {
+           bool keeps = false;
+           if (held > 1 && shared_load(w.last + page) == entry) {
+             keeps = shared_load(w.asks + page) == held;
+             // from here on: whether one of the others that ask got none; and no last one where none keeps the page
+             shared_store(w.asks + page, 0);
+             if (!keeps) shared_store(w.last + page, -1);
+           }
+           replaced += __popcll(__ballot(held > 1 && !keeps) & group);
+         },
+         [&](int b) {
+           if (lane == 0) wants[b] += replaced;
+         });
+    __syncthreads();
   }
-  __syncthreads();
   int total = 0;
   for (int b0 = 0; b0 < d.sequences; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int sum;
     const int below = block_scan(b < d.sequences ? wants[b] : 0, sums, sum);
-    if (b < d.sequences) w.rank[b] = total + below;
+    if (b < d.sequences) w.rank[b] = wants[b] = total + below;
     total += sum;
   }
   // the first `total` free pages
@@ -272,7 +304,20 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve_plan(const int32
     for (; open != 0 && rank < total; open &= open - 1, ++rank) w.free[rank] = (int)first + __builtin_ctz(open);
     found += sum;
   }
-  if (tid == 0) *w.granted = min(found, total);
+  const int granted = min(found, total);
+  if (tid == 0) *w.granted = granted;
+  if (!any_shared || granted == total) return;
+  // the pool ran out: who keeps a page that another one asked for in vain has it not to itself
+  __syncthreads();
+  int next = 0;
+  walk([&](int b) { next = wants[b]; },
+       [&](int entry, bool in, int page, int held) {
+         const bool replaced = held > 1 && shared_load(w.last + page) != entry;
+         const uint64_t all = __ballot((in && page < 0) || replaced) & group;
+         if (replaced && next + __popcll(all & below_me) >= granted) shared_store(w.asks + page, 1);
+         next += __popcll(all);
+       },
+       [](int) {});
 }
 
 // Rows 0 .. n - 1 of every head of page src into page dst, by the workgroups of blockIdx.y.
@@ -299,54 +344,45 @@ __global__ void __launch_bounds__(kThreads) k_cache_reserve(CacheArgs c, const i
                                                             int32_t* __restrict__ table_out,
                                                             int32_t* __restrict__ refs_out, int32_t* __restrict__ short_out,
                                                             int32_t* __restrict__ work, ReserveDims d) {
-  const ReserveSpace w = reserve_space(work, d.sequences);
+  const ReserveSpace w = reserve_space(work, d.sequences, d.pages);
   const int b = blockIdx.x, granted = *w.granted;
   const int32_t* row = table + (int64_t)b * d.width;
-  const Need n = need_of(row, lengths[b], tokens_each ? tokens_each[b] : d.tokens, d);
-  const int rank = w.rank[b], copy = w.copy[b];
-  const int filled = n.length & ((1 << d.page_shift) - 1);
-  const bool copied = copy && rank < granted;
-  if (copied) {
-    const int src = n.last, dst = w.free[rank], codes = c.fmt == FMT_FP8 ? c.head_dim : c.head_dim / 2;
-    copy_rows(c.k_codes, src, dst, c.kv_heads, d.page_shift, codes, filled);
-    copy_rows(c.k_scales, src, dst, c.kv_heads, d.page_shift, c.head_dim / c.block, filled);
-    if (!c.shared) {
-      copy_rows(c.v_codes, src, dst, c.kv_heads, d.page_shift, codes, filled);
-      copy_rows(c.v_scales, src, dst, c.kv_heads, d.page_shift, c.head_dim / c.block, filled);
+  const Need n = need_of(lengths[b], tokens_each ? tokens_each[b] : d.tokens, d);
+  const int rank = w.rank[b], filled = n.length & ((1 << d.page_shift) - 1);
+  // the rows of a partly filled page that others name too, into the first page that the sequence gets
+  if (n.slot < n.end && filled && rank < granted) {
+    const int src = row[n.slot];
+    if (valid_page(src, d.pages) && refs[src] > 1 && w.last[src] != b * d.width + n.slot) {
+      const int dst = w.free[rank], codes = c.fmt == FMT_FP8 ? c.head_dim : c.head_dim / 2;
+      copy_rows(c.k_codes, src, dst, c.kv_heads, d.page_shift, codes, filled);
+      copy_rows(c.k_scales, src, dst, c.kv_heads, d.page_shift, c.head_dim / c.block, filled);
+      if (!c.shared) {
+        copy_rows(c.v_codes, src, dst, c.kv_heads, d.page_shift, codes, filled);
+        copy_rows(c.v_scales, src, dst, c.kv_heads, d.page_shift, c.head_dim / c.block, filled);
+      }
     }
   }
   if (blockIdx.y > 0 || threadIdx.x >= 64) return;
   // entries and counts: the first wave
   const int lane = threadIdx.x;
-  int next = rank + copy, lack = w.lack[b] + (copy && !copied);
-  if (lane == 0 && copied) {
-    const int dst = w.free[rank];
-    table_out[(int64_t)b * d.width + n.slot] = dst;
-    refs_out[dst] = 1;
-    atomicSub(refs_out + n.last, 1);
-  }
-  if (n.last >= 0 && !copy && refs[n.last] > 1) {
-    // this sequence keeps the page: if the copy of the one that asked last before it failed, others hold it still
-    int failed = 0;
-    for (int o = lane; o < b; o += 64)
-      if (w.copy[o] && w.rank[o] >= granted) {
-        const Need m = need_of(table + (int64_t)o * d.width, lengths[o], tokens_each ? tokens_each[o] : d.tokens, d);
-        failed |= m.last == n.last;
-      }
-    lack += __ballot(failed) != 0;
-  }
+  int next = rank, lack = n.beyond;
   for (int s0 = n.slot; s0 < n.end; s0 += 64) {
-    const int s = s0 + lane;
-    const bool missing = s < n.end && !valid_page(row[min(s, d.width - 1)], d.pages);
-    const uint64_t all = __ballot(missing);
+    const int s = s0 + lane, entry = b * d.width + s;
+    const bool in = s < n.end;
+    int page = row[min(s, d.width - 1)];
+    page = in && valid_page(page, d.pages) ? page : -1;
+    const bool common = page >= 0 && refs[page] > 1, keeps = common && w.last[page] == entry;
+    const bool want = in && (page < 0 || (common && !keeps));
+    const uint64_t all = __ballot(want);
     const int mine = next + __popcll(all & ((1ull << lane) - 1));
-    if (missing && mine < granted) {
-      const int page = w.free[mine];
-      table_out[(int64_t)b * d.width + s] = page;
-      refs_out[page] = 1;
+    if (want && mine < granted) {
+      const int fresh = w.free[mine];
+      table_out[entry] = fresh;
+      refs_out[fresh] = 1;
+      if (page >= 0) atomicSub(refs_out + page, 1);
     }
     next += __popcll(all);
-    lack += __popcll(__ballot(missing && mine >= granted));
+    lack += __popcll(__ballot((want && mine >= granted) || (keeps && w.asks[page])));
   }
   if (lane == 0) short_out[b] = lack;
 }
@@ -517,7 +553,7 @@ hipError_t launch_cache_fork(const TableArgs& t, int64_t pages, int page_size, c
 }
 
 int64_t reserve_workspace_bytes(int64_t sequences, int64_t width, int64_t pages) {
-  return 4 * (1 + 3 * sequences + min(pages, sequences * (width + 1)));
+  return 4 * (1 + sequences + 2 * pages + min(pages, sequences * width));
 }
 
 hipError_t launch_cache_reserve(const CacheArgs& c, const TableArgs& t, int tokens, const int32_t* tokens_each,

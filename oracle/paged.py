@@ -131,23 +131,21 @@ def reserve(cache, table, tokens):
         if t == 0:
             continue
         slot, filled = divmod(n, size)
-        if filled and slot < W and new[b, slot] >= 0 and held[new[b, slot]] > 1:
-            if free:
-                to, src = free.pop(0), new[b, slot]
+        for i in range(slot, min(end, W)):
+            old = new[b, i]
+            if old >= 0 and held[old] <= 1:
+                continue
+            if not free:
+                lack[b] += 1
+                continue
+            new[b, i] = free.pop(0)
+            held[new[b, i]] = 1
+            if old >= 0:                    # others name it too: what is cached of it comes along
+                held[old] -= 1
+                rows = filled if i == slot else 0
                 for name in POOLS:
                     if cache[name] is not None:
-                        cache[name][to, :, :filled] = cache[name][src, :, :filled]
-                held[src] -= 1
-                held[to], new[b, slot] = 1, to
-            else:
-                lack[b] += 1
-        for i in range(slot, min(end, W)):
-            if new[b, i] < 0:
-                if free:
-                    new[b, i] = free.pop(0)
-                    held[new[b, i]] = 1
-                else:
-                    lack[b] += 1
+                        cache[name][new[b, i], :, :rows] = cache[name][old, :, :rows]
     return (new, lengths.copy(), held), lack
 
 
