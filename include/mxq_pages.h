@@ -87,9 +87,14 @@ int cache_append(const mxq_cache* cache, const int32_t* table, int64_t sequences
  * tokens, heads] (NULL: not wanted).  A token with nothing to attend to, and
  * tokens from counts on (int32 [sequences], NULL = tokens), get out = 0 and
  * lse = -inf.  Positions a token does not attend to may hold anything, NaN
- * too.  Keys, values and q enter the products as they are (q in as many bf16
+ * too.  A value of 2^128 or more by size (code times scale) counts as an
+ * infinity: a token that attends to it, however small the probability, gets
+ * that infinity in its channel, or NaN where it attends to both signs or to a
+ * NaN.  Keys that are attended to must be finite.  Keys, values and q enter the products as they are (q in as many bf16
  * parts as its type takes, or fp16), probabilities in enough bf16 or fp16 parts
- * that what is lost stays below the output's rounding; sums are fp32.
+ * that what is lost stays below the output's rounding; sums are fp32, of
+ * probabilities that may be 2^8 times the largest (so that n values of 2^120 / n
+ * or more by size may come out infinite).
  * workspace: cache_attention_workspace(the same sizes) bytes, 16-byte aligned;
  * its contents before and after the call mean nothing, and calls that may run
  * at the same time need one each.

@@ -220,7 +220,9 @@ def cache_attention(q, cache, table, *, mask=None, counts=None, scale=None, retu
     with j <= i without a mask.  ``counts`` (int32 [sequences]): tokens from
     there on are padding.  ``scale``: default 1 / sqrt(head_dim); finite.
 
-    Tokens with nothing to attend to get zeros.  With ``return_lse`` also the log
+    Tokens with nothing to attend to get zeros.  Keys must be finite; a value past
+    bf16's range is an infinity to the tokens that attend to it, a NaN is NaN, and
+    neither reaches any other token.  With ``return_lse`` also the log
     of the softmax's sum, float32 [sequences, tokens, heads] (-inf there)."""
     args, device = _cache_args(cache, "cache_attention")
     _need_cuda(q)

@@ -166,6 +166,39 @@ __device__ __forceinline__ int least_odd(int e) {
   else return e == 255 ? 0 : min(8, max(256 - e, 0) << 1);
 }
 
+// The same of a word's codes: the top bit of each that is +inf or NaN, and of each that is -inf or NaN.  `least` is least_odd
+// of their scale byte, `more` kHalf - least in each code.
+template <int FMT>
+struct Odd {
+  static constexpr uint32_t kOnes = FMT == FMT_FP8 ? 0x01010101u : 0x11111111u, kTop = FMT == FMT_FP8 ? 0x80808080u : 0x88888888u;
+  static constexpr int kBits = FMT == FMT_FP8 ? 8 : 4, kHalf = 1 << (kBits - 1);
+  uint32_t sign[2];
+  __device__ __forceinline__ Odd(uint32_t word, uint32_t more, bool nan_scale) {
+    const uint32_t f = ((word & ~kTop) + more) & kTop;
+    const uint32_t nan = nan_scale ? kTop : FMT == FMT_FP8 ? ((word & ~kTop) + kOnes) & kTop : 0u;   // (0x7F is NaN)
+    sign[0] = f & (~word | nan);
+    sign[1] = f & (word | nan);
+  }
+  __device__ __forceinline__ uint32_t any() const { return sign[0] | sign[1]; }
+  // All bits of those codes.
+  __device__ __forceinline__ uint32_t codes() const { return (any() >> (kBits - 1)) * (2 * kHalf - 1); }
+};
+// Scale bytes from here on make some finite code infinite in bf16 (nvfp4's never do).
+template <int FMT>
+constexpr uint32_t kPastBf16 = FMT == FMT_FP8 ? 247 : 253;
+
+// What infinite values make of an output: marks 1 for +inf, 2 for -inf, 3 for both (or NaN).
+__device__ __forceinline__ float marked_value(float x, uint32_t marks) {
+  const float inf = __builtin_inff();
+  return marks == 0 ? x : marks == 1 ? inf : marks == 2 ? -inf : __builtin_nanf("");
+}
+// What a part's sums are multiplied by whose maximum is m, where the whole's is `top`.  Never 0, so that an infinity stays
+// one however small the part's share is (2^-126 of any other is nothing).  A part that met nothing, or NaN alone, has an m
+// of -inf and an l of 0 or NaN.
+__device__ __forceinline__ float share_of_part(float m, float l, float top) {
+  return m == -__builtin_inff() ? l : fmaxf(__builtin_amdgcn_exp2f(m - top), 0x1p-126f);
+}
+
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __builtin_bit_cast(bf16x8_t, u32x4_t{a, b, c, d});
 }
@@ -243,6 +276,35 @@ template <int N, int M, int L>
 __device__ __forceinline__ void from_here(uint32_t (&x)[N][M][L]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) from_here(x[i]);
+}
+// The first of eight moved behind the others: what a loop does to the first of them it does to each, once in its code.
+__device__ __forceinline__ void to_the_end(uint32_t (&x)[8]) {
+  const uint32_t first = x[0];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) x[i] = x[i + 1];
+  x[7] = first;
+}
+template <int N>
+__device__ __forceinline__ void to_the_end(uint32_t (&x)[8][N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint32_t first = x[0][n];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) x[i][n] = x[i + 1][n];
+    x[7][n] = first;
+  }
+}
+template <int N, int M>
+__device__ __forceinline__ void to_the_end(uint32_t (&x)[8][N][M]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const uint32_t first = x[0][n][m];
+#pragma unroll
+      for (int i = 0; i < 7; ++i) x[i][n][m] = x[i + 1][n][m];
+      x[7][n][m] = first;
+    }
 }
 // Over the four lanes that hold a row (16 apart).
 __device__ __forceinline__ float row_max(float v) {
@@ -414,7 +476,7 @@ struct Attention {
 
   struct Shared {
     __attribute__((aligned(16))) uint8_t big[kLdsBytes];   // q's fragments, then the waves' sums
-    __attribute__((aligned(16))) uint8_t nan[kRows * D];   // outputs that a value that is not finite reached
+    __attribute__((aligned(16))) uint8_t nan[kRows * D];   // marks of outputs that a value that is not finite reached
     float m[4][kRows], l[4][kRows];
     int first[kThreads];                                   // prefix sums of the schedule
     int sums[4];
@@ -657,62 +719,93 @@ struct Attention {
     });
   }
 
-  // A tile of which not every row attends to every position: scores of the others become -inf, values of rows that are
-  // no position 0.  A value that is not finite counts for the rows that attend to it alone: it becomes 0 here (0 times
-  // NaN is NaN) and is marked for those rows, whose sums are NaN in the end.
-  __device__ __forceinline__ void mask(const Pages& now, int t, f32x4_t (&s)[MT][2], V& v) const {
-    uint32_t may[MT];
-    mask_scores<MT>(a, w, b, t, now.there[0], now.there[1], row_of(0), quarter, s, may);
-    // codes whose value is not finite: from `least` on (by size), which the scale says
-    constexpr uint32_t kOnes = S::kFp8 ? 0x01010101u : 0x11111111u, kTop = S::kFp8 ? 0x80808080u : 0x88888888u;
-    constexpr int kBits = S::kFp8 ? 8 : 4, kHalf = 1 << (kBits - 1);
-    uint32_t bad[8][S::VU][S::VW], any = 0;
+  // Whether a value of the tile may be infinite in bf16.
+  __device__ __forceinline__ static bool past_bf16(const V& v) {
+    if constexpr (FMT == FMT_NVFP4) return false;
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+        for (int i = 0; i < S::VS; ++i) most = max(most, v.s[j][u][i]);
+    return __ballot(most >= kPastBf16<FMT>) != 0;
+  }
+  // The values of a tile that not every row attends to, or that holds infinities.  Those of rows that are no position become
+  // 0.  A value that is not finite counts for the rows that attend to it alone, whatever its probability's parts are: it
+  // becomes 0 here (0 times it is NaN) and is marked for those rows, whose sums are set in the end.
+  __device__ __forceinline__ void clean(const Pages& now, int t, const uint32_t (&may)[MT], V& v) const {
+    using Codes = Odd<FMT>;
+    constexpr int kWords = S::VU * S::VW, kCodes = S::VC / S::VW;
+    constexpr uint32_t kUnit = FMT == FMT_NVFP4 ? 0x38u : 127u;        // a scale of 1
+    uint32_t any = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
       const bool none = !now.there[j / 4] || pos >= w.end;
 #pragma unroll
       for (int u = 0; u < S::VU; ++u) {
-        uint32_t more[S::VS];         // kHalf - least
+        uint32_t more[S::VS];
 #pragma unroll
         for (int i = 0; i < S::VS; ++i) {
-          const int least = least_odd<FMT>(v.s[j][u][i]);
-          more[i] = none ? 0u : (kHalf - least) * kOnes;
-          v.s[j][u][i] = none || least == 0 ? (FMT == FMT_NVFP4 ? 0x38u : 127u) : v.s[j][u][i];
+          v.s[j][u][i] = none ? kUnit : v.s[j][u][i];
+          more[i] = (Codes::kHalf - least_odd<FMT>(v.s[j][u][i])) * Codes::kOnes;
         }
 #pragma unroll
         for (int i = 0; i < S::VW; ++i) {
-          const uint32_t word = none ? 0u : v.w[j][u][i];
-          const uint32_t f = ((word & ~kTop) + more[i * S::VS / S::VW]) & kTop;
-          v.w[j][u][i] = word & ~((f >> (kBits - 1)) * (2 * kHalf - 1));
-          bad[j][u][i] = f;
-          any |= f;
+          v.w[j][u][i] = none ? 0u : v.w[j][u][i];
+          any |= (v.w[j][u][i] & ~Codes::kTop) + more[i * S::VS / S::VW];
         }
       }
     }
-    if (__ballot(any != 0) == 0) return;
-    // the marks, a position at a time, in a loop over its codes, whose words lie in LDS behind q's fragments
-    constexpr int kWords = S::VU * S::VW, kCodes = S::VC / S::VW;
+    if (__ballot((any & Codes::kTop) != 0) == 0) return;
+    // the marks, a position at a time (its values first in line), in a loop over its codes, whose words lie in LDS behind
+    // q's fragments
     uint32_t* words = reinterpret_cast<uint32_t*>(sm.big + kQBytes) + (wave * 64 + lane) * kWords;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) words[i] = bad[j][i / S::VW][i % S::VW];
-      bool sees[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) sees[mt] = may[mt] >> j & 1;
 #pragma unroll 1
-      for (int i = 0; i < kWords * kCodes; ++i) {
-        const int word = i / kCodes, code = i - word * kCodes;
-        const uint64_t all = __ballot(words[word] >> (code * kBits + kBits - 1) & 1u);
-        // the quarter's lanes hold this channel of their units, and the rows of the same positions
-        for (uint32_t lanes = (uint32_t)(all >> (quarter * 16)) & 0xFFFFu; lanes != 0; lanes &= lanes - 1) {
-          const int channel = word / S::VW * 16 * S::VC + __builtin_ctz(lanes) * S::VC + word % S::VW * kCodes + code;
+    for (int j = 0; j < 8; ++j) {
+      uint32_t more[S::VU][S::VS];
+      bool nan[S::VU][S::VS];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            if (sees[mt]) sm.nan[(mt * 16 + col) * D + channel] = 1;
+      for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+        for (int i = 0; i < S::VS; ++i) {
+          const int least = least_odd<FMT>(v.s[0][u][i]);
+          more[u][i] = (Codes::kHalf - least) * Codes::kOnes;
+          nan[u][i] = least == 0;
+          v.s[0][u][i] = nan[u][i] ? kUnit : v.s[0][u][i];
+        }
+#pragma unroll 1
+      for (int sign = 0; sign < 2; ++sign) {
+#pragma unroll
+        for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+          for (int i = 0; i < S::VW; ++i) {
+            const Codes f(v.w[0][u][i], more[u][i * S::VS / S::VW], nan[u][i * S::VS / S::VW]);
+            words[u * S::VW + i] = sign ? f.sign[1] : f.sign[0];
+          }
+#pragma unroll 1
+        for (int i = 0; i < kWords * kCodes; ++i) {
+          const int word = i / kCodes, code = i - word * kCodes;
+          const uint64_t all = __ballot(words[word] >> (code * Codes::kBits + Codes::kBits - 1) & 1u);
+          // the quarter's lanes hold this channel of their units, and the rows of the same positions
+          for (uint32_t lanes = (uint32_t)(all >> (quarter * 16)) & 0xFFFFu; lanes != 0; lanes &= lanes - 1) {
+            const int channel = word / S::VW * 16 * S::VC + __builtin_ctz(lanes) * S::VC + word % S::VW * kCodes + code;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const int at = (mt * 16 + col) * D + channel;
+              if (may[mt] >> j & 1) atomicOr(reinterpret_cast<uint32_t*>(sm.nan) + at / 4, (1u + sign) << (at % 4 * 8));
+            }
+          }
         }
       }
+#pragma unroll
+      for (int u = 0; u < S::VU; ++u)
+#pragma unroll
+        for (int i = 0; i < S::VW; ++i)
+          v.w[0][u][i] &= ~Codes(v.w[0][u][i], more[u][i * S::VS / S::VW], nan[u][i * S::VS / S::VW]).codes();
+      to_the_end(v.w);
+      to_the_end(v.s);
     }
   }
 
@@ -762,11 +855,16 @@ struct Attention {
         load_k(k, next, ahead);
         const int beyond = ahead + 4 < end ? ahead + 4 : ahead;
         const Pages after = pages_of(beyond);
-        if (!(now.there[0] && now.there[1] && (t + 1) * kTile <= w.known)) mask(now, t, s, v);
+        const bool all = now.there[0] && now.there[1] && (t + 1) * kTile <= w.known;    // every row attends to all of it
+        uint32_t may[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) may[mt] = 0xFFu;
+        if (!all) mask_scores<MT>(a, w, b, t, now.there[0], now.there[1], row_of(0), quarter, s, may);
         u32x4_t p[MT][PP];
         softmax_step<HALF, MT, PP, kTilesV>(s, a.d.scale, minus, m, l, o, p);
         from_here(v.w);
         from_here(v.s);
+        if (!all || past_bf16(v)) clean(now, t, may, v);
         passes = passes_of(v.w, v.s);
         for (int pass = 0;;) {
           values(v, p, pass, passes, o);
@@ -837,9 +935,10 @@ struct Attention {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += from[e];
       }
+      const u32x2_t marks = *reinterpret_cast<const u32x2_t*>(sm.nan + r * D + ch);
+      if (marks.x | marks.y)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (sm.nan[r * D + ch + e]) x[e] = __builtin_nanf("");
+        for (int e = 0; e < 8; ++e) x[e] = marked_value(x[e], (e < 4 ? marks.x : marks.y) >> (e % 4 * 8) & 3u);
       const float top = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
       float sum = 0.0f;
 #pragma unroll
@@ -890,9 +989,10 @@ struct SharedAttention {
   struct Shared {
     __attribute__((aligned(16))) u32x4_t key[kTiles][2][S::kSteps][64];
     __attribute__((aligned(16))) u32x4_t value[kTiles][kTilesV][64];
-    uint32_t odd[kStep][kWords];          // channels of a position whose value is not finite
-    uint32_t nan[kRows][kWords];          // outputs that one reached
+    uint32_t odd[kStep][2 * kWords];      // channels of a position whose value is +inf or NaN, then -inf or NaN
+    uint32_t nan[kRows][2 * kWords];      // outputs that one reached
     int marked;                           // the step that `odd` is of
+    int reached;                          // whether `nan` has marks
     int there[kTiles];                    // which halves of a tile have a page
     int again;                            // a scale was met that fp16 does not hold
     int first[kThreads];
@@ -996,7 +1096,16 @@ struct SharedAttention {
     if constexpr (TO_HALF) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, f16x2_t));
     return pack_bf16(lo, hi);
   }
-  // Raw to LDS; positions that are none become 0, and values of partly attended tiles that are not finite too, with a mark.
+  // Whether a value of the wave's part of the step may be infinite in bf16.
+  __device__ __forceinline__ static bool past_bf16(const Raw& x) {
+    if constexpr (FMT == FMT_NVFP4) return false;
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = max(most, x.vs[j]);
+    return __ballot(most >= kPastBf16<FMT>) != 0;
+  }
+  // Raw to LDS; positions that are none become 0, and values that are not finite, in tiles that are attended to in part or
+  // hold infinities, too, with a mark.
   __device__ __forceinline__ void decode_step(Raw& x, int step, int tag) const {
     const int t = my_tile(step);
     from_here(x.k);
@@ -1004,7 +1113,7 @@ struct SharedAttention {
     from_here(x.v);
     from_here(x.vs);
     if (lane == 0) sm.there[wave / kPartsOfTile] = (int)(x.page[0] >= 0) + 2 * (int)(x.page[1] >= 0);   // each part says the same
-    if (!(x.page[0] >= 0 && x.page[1] >= 0 && (t + 1) * kTile <= w.known)) clean(x, t, tag);
+    if (!(x.page[0] >= 0 && x.page[1] >= 0 && (t + 1) * kTile <= w.known) || past_bf16(x)) clean(x, t, tag);
     if constexpr (HALF && !kHalfOnly<DT, FMT>) {
       uint32_t least = 255, most = 0;
 #pragma unroll
@@ -1067,33 +1176,47 @@ struct SharedAttention {
     });
   }
   __device__ __forceinline__ void clean(Raw& x, int t, int tag) const {
-    constexpr uint32_t kOnes = S::kFp8 ? 0x01010101u : 0x11111111u, kTop = S::kFp8 ? 0x80808080u : 0x88888888u;
-    constexpr int kBits = S::kFp8 ? 8 : 4, kHalf = 1 << (kBits - 1);
-    uint32_t bad[8][VW], any = 0;
+    using Codes = Odd<FMT>;
+    constexpr uint32_t kUnit = FMT == FMT_NVFP4 ? 0x38u : 127u;        // a scale of 1
+    uint32_t any = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int pos = t * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
       const bool none = x.page[j / 4] < 0 || pos >= w.end;
-      const int least = least_odd<FMT>(x.vs[j]);
-      x.vs[j] = none || least == 0 ? (FMT == FMT_NVFP4 ? 0x38u : 127u) : x.vs[j];
+      x.vs[j] = none ? kUnit : x.vs[j];
+      const uint32_t more = (Codes::kHalf - least_odd<FMT>(x.vs[j])) * Codes::kOnes;
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
-        const uint32_t word = none ? 0u : x.v[j][i];
-        bad[j][i] = none ? 0u : ((word & ~kTop) + (kHalf - least) * kOnes) & kTop;
-        x.v[j][i] = word & ~((bad[j][i] >> (kBits - 1)) * (2 * kHalf - 1));
-        any |= bad[j][i];
+        x.v[j][i] = none ? 0u : x.v[j][i];
+        any |= (x.v[j][i] & ~Codes::kTop) + more;
       }
     }
-    if (__ballot(any != 0) == 0) return;
+    if (__ballot((any & Codes::kTop) != 0) == 0) return;
     if (lane == 0) sm.marked = tag;
     const int channel = my_channels() * 128 + col * VC;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {          // a position at a time, its values first in line
+      const int least = least_odd<FMT>(x.vs[0]);
+      const uint32_t more = (Codes::kHalf - least) * Codes::kOnes;
+      const int row = wave / kPartsOfTile * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
+#pragma unroll 1
+      for (int sign = 0; sign < 2; ++sign) {
+        uint32_t odd[VW], bits = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t bits = 0;
+        for (int i = 0; i < VW; ++i) {
+          const Codes f(x.v[0][i], more, least == 0);
+          odd[i] = sign ? f.sign[1] : f.sign[0];
+        }
 #pragma unroll
-      for (int c = 0; c < VC; ++c) bits |= (bad[j][c * kBits / 32] >> (c * kBits % 32 + kBits - 1) & 1u) << c;
-      const int pos = wave / kPartsOfTile * kTile + (j / 4) * 16 + quarter * 4 + j % 4;
-      if (bits) atomicOr(&sm.odd[pos][channel / 32], bits << (channel % 32));
+        for (int c = 0; c < VC; ++c)
+          bits |= (odd[c * Codes::kBits / 32] >> (c * Codes::kBits % 32 + Codes::kBits - 1) & 1u) << c;
+        if (bits) atomicOr(&sm.odd[row][sign * kWords + channel / 32], bits << (channel % 32));
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i) x.v[0][i] &= ~Codes(x.v[0][i], more, least == 0).codes();
+      x.vs[0] = least == 0 ? kUnit : x.vs[0];
+      to_the_end(x.v);
+      to_the_end(x.vs);
     }
   }
 
@@ -1101,10 +1224,11 @@ struct SharedAttention {
   // where fp16 does not hold the values.
   __device__ __forceinline__ bool piece(int first, int last, bool whole, float* slot) {
     place();
-    for (int i = wave * 64 + lane; i < kRows * kWords; i += kThreads) sm.nan[i / kWords][i % kWords] = 0;
-    for (int i = wave * 64 + lane; i < kStep * kWords; i += kThreads) sm.odd[i / kWords][i % kWords] = 0;
+    for (int i = wave * 64 + lane; i < 2 * kRows * kWords; i += kThreads) sm.nan[i / (2 * kWords)][i % (2 * kWords)] = 0;
+    clear_odd();
     if (wave == 0 && lane == 0) {
       sm.marked = -1;
+      sm.reached = 0;
       sm.again = 0;
     }
     Raw x;
@@ -1141,7 +1265,7 @@ struct SharedAttention {
       for (int step = first; step < last; ++step) {
         __syncthreads();                   // the fragments of the step before have been read
         if (odd) {
-          for (int i = wave * 64 + lane; i < kStep * kWords; i += kThreads) sm.odd[i / kWords][i % kWords] = 0;
+          clear_odd();
           __syncthreads();
         }
         decode_step(x, step, step);
@@ -1154,6 +1278,9 @@ struct SharedAttention {
     }
     finish(o, m, l, whole, slot);
     return true;
+  }
+  __device__ __forceinline__ void clear_odd() const {
+    for (int i = wave * 64 + lane; i < 2 * kStep * kWords; i += kThreads) sm.odd[i / (2 * kWords)][i % (2 * kWords)] = 0;
   }
   __device__ __forceinline__ void products(int step, const bf16x8_t (&q)[MT][S::kSteps][QP], bool odd, float (&m)[MT],
                                            float (&l)[MT], f32x4_t (&o)[MT][kTilesV]) const {
@@ -1177,19 +1304,23 @@ struct SharedAttention {
             for (int h = 0; h < 2; ++h) s[mt][h] = mfma_key<kHalfKeys<DT, FMT>>(key[h], q[mt][st][p], s[mt][h]);
       }
       const int there = __builtin_amdgcn_readfirstlane(sm.there[ti]);
-      if (there != 3 || (t + 1) * kTile > w.known) {
+      if (odd || there != 3 || (t + 1) * kTile > w.known) {
         uint32_t may[MT];
         mask_scores<MT>(a, w, b, t, there & 1, there >> 1, row_of(0), quarter, s, may);
         if (odd) {
+          uint32_t sees = 0;               // a bit for each row and position
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt) sees |= may[mt] << (8 * mt);
 #pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-              if (!(may[mt] >> j & 1)) continue;
-              const uint32_t* from = sm.odd[ti * kTile + (j / 4) * 16 + quarter * 4 + j % 4];
-              for (int i = 0; i < kWords; ++i)
-                if (from[i]) atomicOr(&sm.nan[(wave * MT + mt) * 16 + col][i], from[i]);
+          for (int i = 0; i < 8 * MT * 2 * kWords; ++i) {
+            const int at = i / (2 * kWords), word = i % (2 * kWords), j = at % 8;
+            if (!(sees >> at & 1)) continue;
+            const uint32_t bits = sm.odd[ti * kTile + (j / 4) * 16 + quarter * 4 + j % 4][word];
+            if (bits) {
+              atomicOr(&sm.nan[(wave * MT + at / 8) * 16 + col][word], bits);
+              sm.reached = 1;
             }
+          }
         }
       }
       u32x4_t p[MT][PP];
@@ -1212,6 +1343,21 @@ struct SharedAttention {
     place();
     __syncthreads();                       // the marks are all there
     const int rows = a.d.tokens * a.d.group, live = w.count * a.d.group;
+    if (__builtin_amdgcn_readfirstlane(sm.reached)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int u = 0; u < kTilesV / VC; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* marks = sm.nan[(wave * MT + mt) * 16 + col];
+            const int ch = u * 16 * VC + (quarter * 4 + i) * VC;
+            const uint32_t up = marks[ch / 32] >> (ch % 32), down = marks[kWords + ch / 32] >> (ch % 32);
+#pragma unroll
+            for (int e = 0; e < VC; ++e)
+              o[mt][u * VC + e][i] = marked_value(o[mt][u * VC + e][i], (up >> e & 1u) + 2 * (down >> e & 1u));
+          }
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const float sum = row_sum(l[mt]);
@@ -1219,12 +1365,6 @@ struct SharedAttention {
 #pragma unroll
       for (int u = 0; u < kTilesV / VC; ++u) {
         const int ch = u * 16 * VC + quarter * 4 * VC;                   // four times VC channels
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t bits = sm.nan[r][(ch + i * VC) / 32] >> ((ch + i * VC) % 32);
-#pragma unroll
-          for (int e = 0; e < VC; ++e) o[mt][u * VC + e][i] = bits >> e & 1 ? __builtin_nanf("") : o[mt][u * VC + e][i];
-        }
         if (!whole && kFragments) {
 #pragma unroll
           for (int e = 0; e < VC; ++e)
@@ -1422,8 +1562,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
         lo = *reinterpret_cast<const f32x4_t*>(slot + from);
         hi = *reinterpret_cast<const f32x4_t*>(slot + from + 4);
       }
-      // nothing met, or NaN alone: l is 0 or NaN
-      const float keep = m == -__builtin_inff() ? l : __builtin_amdgcn_exp2f(m - top);
+      const float keep = share_of_part(m, l, top);
       sum += m == -__builtin_inff() ? l : l * keep;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -1446,7 +1585,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_cache_attention_join(AttnArgs 
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const float m = sums[s][lane][8], l = sums[s][lane][9];
-    const float keep = m == -__builtin_inff() ? l : __builtin_amdgcn_exp2f(m - best);
+    const float keep = share_of_part(m, l, best);
     whole += m == -__builtin_inff() ? l : l * keep;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] += sums[s][lane][e] * keep;
