@@ -60,7 +60,6 @@ int64_t attention_workspace_bytes(const CacheArgs& c, int64_t sequences, int64_t
 hipError_t launch_cache_attention(const CacheArgs& c, const TableArgs& t, const AttentionArgs& x, int dt,
                                   void* workspace, hipStream_t st) {
   const Plan p = plan_of(c, t.sequences, t.width, dt, x.tokens, x.heads);
-  if (p.problems > 0xFFFFFFFFll / kAttnThreads) return hipErrorInvalidConfiguration;
   AttnArgs a = {c.k_codes, c.k_scales, c.v_codes, c.v_scales, t.table, t.lengths, x.counts, (const uint8_t*)x.q, x.mask,
                 (uint8_t*)x.out, x.lse, (float*)workspace, log2_of(c.block), {}};
   a.d = {t.sequences, x.tokens, x.heads, x.heads / c.kv_heads, c.kv_heads, t.width, log2_of(c.page_size), p.row_tiles,

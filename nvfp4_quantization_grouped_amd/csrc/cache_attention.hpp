@@ -1437,12 +1437,15 @@ __device__ __forceinline__ void work_on(const AttnArgs& a, typename A::Shared& s
   }
 }
 
-// One workgroup for each problem.
+// One workgroup for each problem, in rows of kGridRow: a grid's first size times the threads has to stay below 2^32, and there
+// may be 2^31 problems.
+constexpr int64_t kGridRow = int64_t(1) << 20;
 template <class A>
 __global__ void __launch_bounds__(A::kThreads, A::kWaves) k_cache_attention(AttnArgs a) {
   __shared__ typename A::Shared sm;
-  const int each = a.d.kv_heads * a.d.row_tiles;
-  const int b = blockIdx.x / each, kv = (blockIdx.x - b * each) / a.d.row_tiles, tile = blockIdx.x % a.d.row_tiles;
+  const uint32_t at = blockIdx.y * gridDim.x + blockIdx.x, each = a.d.kv_heads * a.d.row_tiles;
+  const int b = at / each, kv = (at - b * each) / a.d.row_tiles, tile = at % a.d.row_tiles;
+  if (b >= a.d.sequences) return;          // the last row's rest
   const Work w = work_of_all<A>(a, b);
   work_on<A>(a, sm, b, kv, tile, w, 0, tile < w.tiles ? w.steps : 0, true, nullptr);
 }
@@ -1619,7 +1622,8 @@ struct AttnShape {
 template <class A>
 hipError_t launch_attention_of(const AttnArgs& a, int64_t problems, hipStream_t st) {
   if (a.d.workgroups == 0) {
-    k_cache_attention<A><<<(unsigned)problems, A::kThreads, 0, st>>>(a);
+    const dim3 grid((unsigned)min(problems, kGridRow), (unsigned)((problems + kGridRow - 1) / kGridRow));
+    k_cache_attention<A><<<grid, A::kThreads, 0, st>>>(a);
   } else {
     k_cache_attention_split<A><<<(unsigned)a.d.workgroups, A::kThreads, 0, st>>>(a);
     k_cache_attention_join<A><<<dim3((unsigned)problems, A::kRows * A::kDim / 512), kAttnThreads, 0, st>>>(a);
