@@ -230,7 +230,7 @@ def cache_attention(q, cache, table, *, mask=None, counts=None, scale=None, retu
     if q.dim() != 4 or q.shape[3] != args.head_dim or q.device != device:
         raise ValueError("cache_attention: q must be [sequences, tokens, heads, head_dim], on the cache's device")
     B, T, H, D = q.shape
-    if H == 0 or H % args.kv_heads:
+    if H == 0 or (args.kv_heads and H % args.kv_heads):        # (a cache without heads: the library's check)
         raise ValueError("cache_attention: heads must be a multiple of the cache's kv_heads")
     _no_gradient("cache_attention", q)
     rows, lengths, _ = _table_args(table, args.pages, device, "cache_attention")
