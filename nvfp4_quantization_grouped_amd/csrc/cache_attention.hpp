@@ -1096,9 +1096,10 @@ struct SharedAttention {
     if constexpr (TO_HALF) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, f16x2_t));
     return pack_bf16(lo, hi);
   }
-  // Whether a value of the wave's part of the step may be infinite in bf16.
+  // Whether a value of the wave's part of the step may be infinite in bf16.  (Where fp16 is tried, such a scale starts the
+  // piece again.)
   __device__ __forceinline__ static bool past_bf16(const Raw& x) {
-    if constexpr (FMT == FMT_NVFP4) return false;
+    if constexpr (HALF || FMT == FMT_NVFP4) return false;
     uint32_t most = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = max(most, x.vs[j]);
