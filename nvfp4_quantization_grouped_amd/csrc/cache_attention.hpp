@@ -12,7 +12,10 @@
 // sum is free, so V^T takes the same.  The order of channels within K Q^T is
 // free too: a lane's 8 channels of a step are chosen so that a lane loads 16
 // consecutive bytes.  V is decoded two channels at a time for 8 positions and
-// turned by v_perm.  There is no LDS traffic until the four waves' sums join.
+// turned by v_perm.  Up to 16 or 32 rows (Attention) keys, values and
+// probabilities stay in registers; LDS holds the waves' sums in the end, q where
+// its parts are too many for the registers, and the marks of values that are not
+// finite.  Beyond (SharedAttention) keys and values pass through LDS, decoded.
 //
 // Softmax.  m is a row's running maximum in units of log2, moved only when a
 // score exceeds it by 2^8 (probabilities stay below 2^8 relative to it, which
@@ -28,8 +31,11 @@
 // nothing to see, at as many products.
 // For bf16 outputs one fp16 part does (2^-11; the error is 1.01 times the
 // rounding's) where the values fit fp16 exactly, which the scales tell: always
-// for nvfp4, else (and where there are many rows) for scales of 2^-23 to 2^13 or
-// so.  A workgroup that meets others starts its piece again with two bf16 parts.
+// for nvfp4, else (and where there are many rows) for scales of 2^-15 to 2^7
+// (fp8) or 2^-23 to 2^13 (mxfp4).  A workgroup that meets others starts its piece
+// again with two bf16 parts: blocks of zeros are among them, as they are
+// quantized with byte 1 (64-token trees with a row of zeros in every page 300 us
+// against 259).
 //
 // What bounds it.  One token a sequence: memory (64 contexts of up to 16384, 8
 // heads of 8 queries, mxfp4: 638 MB in 138 us, 4.6 TB/s).  Trees: the products
