@@ -7,7 +7,7 @@
 // loads, not bytes: each is one or two launches.  Whatever depends on an order
 // (which sequence gets which free page) is decided by one workgroup with prefix
 // sums; counts are integer atomics, whose sum does not depend on their order.
-// Measured: fork 3 us, the plan of a reserve 9 to 12 (four loads in a row, three
+// Measured: fork 3 us, the plan of a reserve 9 to 11 (four loads in a row, three
 // more round trips where pages are shared, then the scans over the sequences and
 // the pages) and its copies 4 to 9, accept 3.6, the plan of a compaction 6; its
 // copies 13 us for 55 MB, 4.2 TB/s.
@@ -200,7 +200,8 @@ __device__ __forceinline__ void shared_store(int32_t* p, int v) {
 //
 // An entry that asks for a page which others name too (refs > 1) gets another one, unless it is the last to ask and all
 // that name the page ask.  So each page needs two numbers, how many entries ask and which is the last: a count and a
-// maximum, whose order does not matter, where comparing the entries would take the square of their number.
+// maximum, whose order does not matter, where comparing the entries would take the square of their number (a token each for
+// 1024 beams of four 27 us with both launches, 41 by comparing; 4096 of them 89 and 295).
 __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve_plan(const int32_t* __restrict__ table,
                                                                      const int32_t* __restrict__ lengths,
                                                                      const int32_t* __restrict__ refs,
@@ -227,18 +228,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve_plan(const int32
   const int lane = tid & (lanes - 1);
   const uint64_t group = (lanes == 64 ? ~0ull : (1ull << lanes) - 1) << (tid & 63 & ~(lanes - 1));
   const uint64_t below_me = (1ull << (tid & 63)) - 1;
-  // f(sequence, entry of the table, whether it is asked for, its page or -1, refs of the page or 0), the lanes of a
-  // sequence at its entries in turn; begin(sequence) and end(sequence) around them
+  // f(entry of the table, whether it is asked for, its page or -1, refs of the page or 0), the lanes of a sequence at its
+  // entries in turn; begin(sequence) and end(sequence) around them.  A lane's loads go out kAtOnce entries at a time.
+  constexpr int kAtOnce = 4;
   auto walk = [&](auto begin, auto f, auto end) {
     for (int b = tid >> shift; b < d.sequences; b += kPlanThreads >> shift) {
       const Need n = need_of(lengths[b], tokens_each ? tokens_each[b] : d.tokens, d);
       begin(b);
-      for (int s0 = n.slot; s0 < n.end; s0 += lanes) {
-        const int s = s0 + lane;
-        const bool in = s < n.end;
-        int page = table[(int64_t)b * d.width + min(s, d.width - 1)];
-        page = in && valid_page(page, d.pages) ? page : -1;
-        f(b * d.width + s, in, page, page >= 0 ? refs[page] : 0);
+      for (int s0 = n.slot; s0 < n.end; s0 += lanes * kAtOnce) {
+        int page[kAtOnce], held[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int s = s0 + u * lanes + lane;
+          page[u] = s < n.end ? table[(int64_t)b * d.width + s] : -1;
+          page[u] = valid_page(page[u], d.pages) ? page[u] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) held[u] = page[u] >= 0 ? refs[page[u]] : 0;
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int s = s0 + u * lanes + lane;
+          f(b * d.width + s, s < n.end, page[u], held[u]);
+        }
       }
       end(b);
     }
