@@ -199,10 +199,11 @@ __device__ __forceinline__ float marked_value(float x, uint32_t marks) {
   return marks == 0 ? x : marks == 1 ? inf : marks == 2 ? -inf : __builtin_nanf("");
 }
 // What a part's sums are multiplied by whose maximum is m, where the whole's is `top`.  Never 0, so that an infinity stays
-// one however small the part's share is (2^-126 of any other is nothing).  A part that met nothing, or NaN alone, has an m
-// of -inf and an l of 0 or NaN.
+// one however small the part's share is: 2^-149 in the place of a share below 2^-126, as others' sums, of n values of up to
+// 2^8 |v|, come to nothing by it (n 2^-141 of the largest value).  A part that met nothing, or NaN alone, has an m of -inf
+// and an l of 0 or NaN.
 __device__ __forceinline__ float share_of_part(float m, float l, float top) {
-  return m == -__builtin_inff() ? l : fmaxf(__builtin_amdgcn_exp2f(m - top), 0x1p-126f);
+  return m == -__builtin_inff() ? l : fmaxf(__builtin_amdgcn_exp2f(m - top), 0x1p-149f);
 }
 
 __device__ __forceinline__ bf16x8_t as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {

@@ -115,3 +115,31 @@ def test_however_small_the_probability(T, heads, length):
     for p, channel in ((2, 0), (length // 2, 33), (length - 1, 63)):
         put(cache, table[0][0, p // 16], 0, p % 16, channel, "+")
     check(values(g, (1, T, heads, 64), "bf16"), cache, table, "far apart", scale=6.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,heads", [(1, 2), (24, 2)])
+def test_large_values_of_no_probability_change_nothing(dtype, T, heads):
+    """Values of 2^118 whose probabilities are e^-256, in parts of their own of a context that is shared out: the answer is
+    that of the other positions, and what a share of 2^-149 adds is 2^118 * 2^8 * 2048 * 2^-149 = 2^-12 at most."""
+    g = np.random.default_rng(T)
+    n, size, dim = 4096 - T, 64, 64
+    cache = pools(g, 64, 1, size, dim, "fp8", 64)
+    table = counted(np.arange(64, dtype=np.int32)[None], [n], 64)
+    cache["k_codes"][:32], cache["k_codes"][32:] = 0x38, 0xB8          # 1 and -1
+    cache["k_scales"][:] = 127
+    cache["v_codes"][:] &= 0x3F                                        # up to 1.875
+    cache["v_scales"][:32] = 127
+    q = torch.ones(1, T, heads, dim).to(values(g, (1,), dtype).dtype)
+    mask = np.zeros((T, T), bool)
+    cache["v_scales"][32:] = 127 + 117
+    large = paged_run(q, cache, table, mask)
+    cache["v_codes"][32:] = 0
+    clean = paged_run(q, cache, table, mask)
+    assert torch.isfinite(clean).all() and bool((clean > 2.0 ** -10).all())
+    assert torch.allclose(large, clean, rtol=2.0 ** -7 if dtype == "bf16" else 2.0 ** -10, atol=2.0 ** -12)
+
+
+def paged_run(q, cache, table, mask):
+    return mxq.cache_attention(q.to(dev()), on_gpu(cache), table_on_gpu(table), mask=torch.from_numpy(mask).to(dev()),
+                               scale=2.0).float()
