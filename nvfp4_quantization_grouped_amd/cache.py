@@ -320,7 +320,9 @@ def cache_accept(cache, table, accepted):
     """The drafted tokens that were accepted become cached ones: the rows of
     tokens ``accepted[b, 0], accepted[b, 1], ...`` (int32 [sequences, up to 64],
     rising, -1 behind the last) move together to positions lengths, lengths + 1,
-    ..., in place, and the result's lengths include them."""
+    ..., in place, and the result's lengths include them.  A list ends before a
+    token whose row or place has no page, or whose place is in a page that other
+    sequences share (a table forked between the drafts and this call)."""
     args, device = _cache_args(cache, "cache_accept")
     rows, lengths, refs = _table_args(table, args.pages, device, "cache_accept")
     if accepted.dtype != torch.int32 or accepted.dim() != 2 or accepted.shape[0] != rows.shape[0]:
